@@ -421,6 +421,160 @@ MOE_API moe_status_t moe_route_noalloc(moe_plan_t plan, const float* logits,
                                        int32_t* counts, int32_t* offsets,
                                        int32_t* perm, int32_t* dest, void* stream);
 
+/* ------------------------------------------------------------------ training
+ *
+ * The operators that a training step of the layer needs around and behind the
+ * forward calls above.  One step, with `up` the plan of the SwiGLU up
+ * projection (N = 2F, out_dtype bf16) and `down` the plan of the down
+ * projection (d = F, N = the model's width), both of the same T, E and k:
+ *   forward   moe_layernorm, moe_router_logits, moe_route,
+ *             moe_dispatch_gemm(up) -> GU, moe_swiglu_checkpoint(up) -> H, codes,
+ *             moe_grouped_gemm(down) -> Y, moe_combine(down) -> out
+ *   backward  moe_combine_backward(down) -> dY, dtopk_w,
+ *             moe_grouped_gemm_dgrad(down) -> dH,
+ *             moe_swiglu_checkpoint_backward(up) -> dGU and H again,
+ *             moe_grouped_gemm_wgrad(down; H, dY) -> dW2,
+ *             moe_grouped_gemm_wgrad(up; dispatched rows, dGU) -> dW1,
+ *             moe_grouped_gemm_dgrad(up; dGU) -> dA,
+ *             moe_combine with weights 1 on dA -> the gradient of the normed
+ *             rows (the dispatch's gradient), moe_layernorm_backward -> dx.
+ * The conventions at the top of this file hold: dense rows, asynchronous calls,
+ * no allocation.  Where an argument may be fp32 or bf16 a dtype argument beside
+ * it says which (MOE_OUT_F32 or MOE_OUT_BF16).  fp32 [d] weights (gamma, beta,
+ * dgamma, dbeta) are 16-byte aligned.  All sums are fp32, in an order that
+ * does not depend on timing: two calls on the same inputs give the same bits.
+ */
+
+/*
+ * moe_backward_scratch -- bytes of device scratch that moe_layernorm_backward of
+ * this plan needs.  The caller allocates it, 256-byte aligned, and fills it
+ * with zeros ONCE before the first call, as for moe_plan's workspace.  Calls that
+ * share one scratch must be ordered on one stream.  Host only.
+ */
+MOE_API moe_status_t moe_backward_scratch(moe_plan_t plan, size_t* bytes);
+
+/*
+ * moe_layernorm -- layer norm of the plan's T token rows of width d, the step
+ * before the router and the dispatch.
+ *   x       in:  [T][d] of x_dtype.
+ *   gamma   in:  fp32 [d], or NULL for ones.
+ *   beta    in:  fp32 [d], or NULL for zeros.
+ *   eps     in:  > 0, finite.
+ *   y       out: bf16 [T][d]; (x - mean) * rstd * gamma + beta in fp32, rounded
+ *                once.  mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps).
+ *   mean, rstd out: fp32 [T], each may be NULL (inference).
+ * A row that holds an infinity or a NaN gives NaN, as the formula does.
+ * Launches one kernel.
+ */
+MOE_API moe_status_t moe_layernorm(moe_plan_t plan, const void* x, int32_t x_dtype, const float* gamma,
+                                   const float* beta, float eps, uint16_t* y, float* mean, float* rstd,
+                                   void* stream);
+
+/*
+ * moe_layernorm_backward -- the gradient of moe_layernorm.  With
+ * xh = (x - mean) * rstd and v = dy * gamma,
+ *   dx = rstd * (v - sum(v) / d - xh * sum(v * xh) / d) + dres,
+ *   dgamma = sum over the rows of dy * xh,  dbeta = sum over the rows of dy.
+ *   dy      in:  [T][d] of dy_dtype (moe_combine gives fp32).
+ *   x       in:  [T][d] of x_dtype; gamma as in the forward call; mean, rstd
+ *                fp32 [T] from it.
+ *   dres    in:  [T][d] of x_dtype: a gradient to add (the residual branch's), or
+ *                NULL.  May be dx itself.
+ *   dx      out: [T][d] of x_dtype.  May not overlap dy or x.
+ *   dgamma, dbeta out: fp32 [d], each may be NULL.
+ *   scratch in/out: moe_backward_scratch; may be NULL when dgamma and dbeta are.
+ *                MOE_ERR_WORKSPACE if it is missing or misaligned.
+ * T = 0 writes zeros to dgamma and dbeta.
+ */
+MOE_API moe_status_t moe_layernorm_backward(moe_plan_t plan, const void* dy, int32_t dy_dtype, const void* x,
+                                            int32_t x_dtype, const float* gamma, const float* mean,
+                                            const float* rstd, const void* dres, void* dx, float* dgamma,
+                                            float* dbeta, void* scratch, void* stream);
+
+/*
+ * moe_swiglu_checkpoint -- the SwiGLU activation of the up projection, keeping
+ * its inputs in 8 bits for the backward pass (1.03 bytes a value in place of
+ * 2 or 4).  The plan's N is 2F, F a multiple of 8.
+ *   GU      in:  [S][2F] in the plan's out_dtype: gate g in columns [0, F), up u
+ *                in [F, 2F), from moe_dispatch_gemm, moe_gather_gemm or
+ *                moe_grouped_gemm.
+ *   H       out: bf16 [S][F] = silu(g) * u of the values themselves, fp32
+ *                arithmetic rounded once; NULL to store the checkpoint alone.
+ *   codes   out: int8 [S][2F], 16-byte aligned.
+ *   scales  out: fp32 [S][2B], B = ceil(F / 128): the gate's blocks, then the
+ *                up's.  Each half row is cut into blocks of 128 columns (the last
+ *                one may be shorter).  With amax the block's largest magnitude,
+ *                  scale = amax / 127,  code = round(x * (127 / amax)),
+ *                every operation rounded to fp32, round to the nearest even integer;
+ *                a stored value is code * scale.  A block whose amax is below 2^-121
+ *                gets scale 0 and codes 0.  A block that holds an infinity or a
+ *                NaN gets scale NaN: it is restored as NaN throughout.
+ * Launches one kernel.
+ */
+MOE_API moe_status_t moe_swiglu_checkpoint(moe_plan_t plan, const void* GU, uint16_t* H, int8_t* codes,
+                                           float* scales, void* stream);
+
+/*
+ * moe_swiglu_checkpoint_backward -- the gradient of the SwiGLU activation from
+ * its 8-bit checkpoint.  With g, u the stored values and s = 1 / (1 + e^-g),
+ *   dGU = [ dH * u * s * (1 + g * (1 - s)) | dH * g * s ],  H = g * s * u.
+ *   dH      in:  [S][F] of dh_dtype (moe_grouped_gemm_dgrad of the down projection).
+ *   codes, scales in: from moe_swiglu_checkpoint on the same plan.
+ *   H       out: bf16 [S][F], the activation again for the down projection's
+ *                weight gradient (so that the forward pass need not keep it); or NULL.
+ *   dGU     out: bf16 [S][2F].
+ * fp32 arithmetic, rounded once.  Launches one kernel.
+ */
+MOE_API moe_status_t moe_swiglu_checkpoint_backward(moe_plan_t plan, const void* dH, int32_t dh_dtype,
+                                                    const int8_t* codes, const float* scales, uint16_t* H,
+                                                    uint16_t* dGU, void* stream);
+
+/*
+ * moe_combine_backward -- the gradient of moe_combine:
+ *   dY[dest[t*k+j]]  = topk_w[t][j] * dout[t]          (bf16, rounded once)
+ *   dtopk_w[t][j]    = sum_n dout[t][n] * Y[dest[t*k+j]][n]   (fp32)
+ *   dout    in:  [T][N] of dout_dtype.
+ *   Y, topk_w, dest in: as for moe_combine.  Slots whose dest is outside [0, S)
+ *                are skipped (dtopk_w 0).
+ *   dY      out: bf16 [S][N], destination order.
+ *   dtopk_w out: fp32 [T][k].
+ * Launches one kernel; no workspace.
+ */
+MOE_API moe_status_t moe_combine_backward(moe_plan_t plan, const void* dout, int32_t dout_dtype, const void* Y,
+                                          const float* topk_w, const int32_t* dest, uint16_t* dY,
+                                          float* dtopk_w, void* stream);
+
+/*
+ * moe_grouped_gemm_dgrad -- the input gradient of moe_grouped_gemm (and of
+ * moe_dispatch_gemm's product): dA[i] = dY[i] x W[e(i)]^T.
+ *   dY      in:  bf16 [S][N], destination order.
+ *   offsets in:  int32 [E+1] from moe_route.
+ *   W       in:  bf16 [E][d][N], the forward call's.
+ *   dA      out: [S][d] of da_dtype, fp32 sums.
+ * Workspace and status as for moe_grouped_gemm.  Offsets that are not an
+ * ascending list from 0 to S write MOE_ERR_DEVICE to dev_status and nothing to dA.
+ */
+MOE_API moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY, const int32_t* offsets,
+                                            const uint16_t* W, void* dA, int32_t da_dtype, void* workspace,
+                                            int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_gemm_wgrad -- the weight gradient of the per-expert product:
+ * dW[e] = sum over expert e's rows i of A[i]^T dY[i].
+ *   A       in:  bf16 [S][d], destination order (moe_dispatch_gemm's receive buffer
+ *                when num_ranks is 1).
+ *   dY      in:  bf16 [S][N].
+ *   offsets in:  int32 [E+1] from moe_route.
+ *   dW      out: [E][d][N] of dw_dtype.  An expert without rows gets zeros.
+ *   accumulate in: 1: dW += (fp32 only, MOE_ERR_UNSUPPORTED otherwise); 0: dW =.
+ * T = 0 writes zeros (accumulate: nothing).  Workspace, status and invalid
+ * offsets as for moe_grouped_gemm_dgrad.
+ */
+MOE_API moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const uint16_t* dY,
+                                            const int32_t* offsets, void* dW, int32_t dw_dtype,
+                                            int32_t accumulate, void* workspace, int32_t* dev_status,
+                                            void* stream);
+
 /* Static string naming a status code. */
 MOE_API const char* moe_status_string(moe_status_t status);
 

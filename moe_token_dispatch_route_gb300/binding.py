@@ -68,7 +68,10 @@ class PlanInfo(ctypes.Structure):
 EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_plan_info", "moe_route", "moe_dispatch_gemm",
             "moe_read_status", "moe_status_string", "moe_route_noalloc", "moe_combine",
             "moe_router_logits", "moe_route_biased", "moe_dispatch_gemm_swiglu",
-            "moe_grouped_gemm", "moe_gather_gemm", "moe_set_trace", "moe_dispatch_gemm_combine")
+            "moe_grouped_gemm", "moe_gather_gemm", "moe_set_trace", "moe_dispatch_gemm_combine",
+            "moe_backward_scratch", "moe_layernorm", "moe_layernorm_backward", "moe_swiglu_checkpoint",
+            "moe_swiglu_checkpoint_backward", "moe_combine_backward", "moe_grouped_gemm_dgrad",
+            "moe_grouped_gemm_wgrad")
 
 
 def load_library(path: str = LIB_PATH):
@@ -112,6 +115,17 @@ def load_library(path: str = LIB_PATH):
     lib.moe_combine.restype = I32
     lib.moe_route_noalloc.argtypes = [VP] * 9
     lib.moe_route_noalloc.restype = I32
+    F32 = ctypes.c_float
+    lib.moe_backward_scratch.argtypes = [VP, P(ctypes.c_size_t)]
+    lib.moe_layernorm.argtypes = [VP, VP, I32, VP, VP, F32, VP, VP, VP, VP]
+    lib.moe_layernorm_backward.argtypes = [VP, VP, I32, VP, I32] + [VP] * 9
+    lib.moe_swiglu_checkpoint.argtypes = [VP] * 6
+    lib.moe_swiglu_checkpoint_backward.argtypes = [VP, VP, I32] + [VP] * 5
+    lib.moe_combine_backward.argtypes = [VP, VP, I32] + [VP] * 6
+    lib.moe_grouped_gemm_dgrad.argtypes = [VP] * 5 + [I32] + [VP] * 3
+    lib.moe_grouped_gemm_wgrad.argtypes = [VP] * 5 + [I32, I32] + [VP] * 3
+    for name in EXPORTED[-8:]:  # the training operators
+        getattr(lib, name).restype = I32
     lib.moe_status_string.argtypes = [I32]
     lib.moe_status_string.restype = ctypes.c_char_p
     if path == LIB_PATH:
@@ -280,6 +294,129 @@ def moe_combine(plan: Plan, Y, topk_w, dest, out, stream=None) -> None:
     rc = load_library().moe_combine(plan.handle, _ptr(Y), _ptr(topk_w), _ptr(dest), _ptr(out),
                                     _stream(stream, plan.device))
     _check(rc, "moe_combine")
+
+
+# ---------------------------------------------------------------- training operators
+
+_DTYPES = {torch.float32: MOE_OUT_F32, torch.bfloat16: MOE_OUT_BF16}
+
+
+def _arg(call: str, plan: Plan, name: str, t, numel: int, *dtypes, optional: bool = False) -> int | None:
+    """Device pointer of a dense tensor on the plan's device with `numel` elements and one of
+    `dtypes`; the C ABI sees addresses alone, so a tensor it would misread is refused here."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{call}: {name} is missing")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{call}: {name} is {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{call}: {name} must be dense with {numel} elements, got {tuple(t.shape)}"
+                         f"{'' if t.is_contiguous() else ', strided'}")
+    if t.get_device() != plan.device:
+        raise ValueError(f"{call}: {name} is on {t.device}, the plan on cuda:{plan.device}")
+    return t.data_ptr()
+
+
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
+def backward_scratch(plan: Plan, device=None) -> torch.Tensor:
+    """Zeroed scratch of moe_layernorm_backward (the caller keeps it, like the workspace)."""
+    n = ctypes.c_size_t()
+    _check(load_library().moe_backward_scratch(plan.handle, ctypes.byref(n)), "moe_backward_scratch")
+    return torch.zeros(n.value, dtype=torch.uint8, device=torch.device("cuda", plan.device) if device is None else device)
+
+
+def moe_layernorm(plan: Plan, x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
+    """y = (x - mean) rstd gamma + beta over the plan's T rows of width d; gamma, beta, mean and
+    rstd may be None."""
+    s, c = plan.shape, "moe_layernorm"
+    n = s.T * s.d
+    _check(load_library().moe_layernorm(
+        plan.handle, _arg(c, plan, "x", x, n, _BF16, _F32), _DTYPES[x.dtype],
+        _arg(c, plan, "gamma", gamma, s.d, _F32, optional=True), _arg(c, plan, "beta", beta, s.d, _F32, optional=True),
+        eps, _arg(c, plan, "y", y, n, _BF16), _arg(c, plan, "mean", mean, s.T, _F32, optional=True),
+        _arg(c, plan, "rstd", rstd, s.T, _F32, optional=True), _stream(stream, plan.device)), c)
+
+
+def moe_layernorm_backward(plan: Plan, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, scratch,
+                           stream=None) -> None:
+    """Gradient of moe_layernorm; dres (added to dx), gamma, dgamma and dbeta may be None."""
+    s, c = plan.shape, "moe_layernorm_backward"
+    n = s.T * s.d
+    px = _arg(c, plan, "x", x, n, _BF16, _F32)
+    _check(load_library().moe_layernorm_backward(
+        plan.handle, _arg(c, plan, "dy", dy, n, _BF16, _F32), _DTYPES[dy.dtype], px, _DTYPES[x.dtype],
+        _arg(c, plan, "gamma", gamma, s.d, _F32, optional=True), _arg(c, plan, "mean", mean, s.T, _F32),
+        _arg(c, plan, "rstd", rstd, s.T, _F32), _arg(c, plan, "dres", dres, n, x.dtype, optional=True),
+        _arg(c, plan, "dx", dx, n, x.dtype), _arg(c, plan, "dgamma", dgamma, s.d, _F32, optional=True),
+        _arg(c, plan, "dbeta", dbeta, s.d, _F32, optional=True), _ptr(scratch), _stream(stream, plan.device)), c)
+
+
+def _out_dtype(plan: Plan):
+    return _BF16 if plan.shape.out_dtype == MOE_OUT_BF16 else _F32
+
+
+def checkpoint_blocks(F: int) -> int:
+    """Scales of one half row of the 8-bit checkpoint: blocks of 128 columns."""
+    return (F + 127) // 128
+
+
+def moe_swiglu_checkpoint(plan: Plan, GU, H, codes, scales, stream=None) -> None:
+    """H = silu(gate) * up (H may be None), and GU in 8 bits: int8 codes [S][2F] and fp32 scales
+    [S][2 * checkpoint_blocks(F)]."""
+    s, c = plan.shape, "moe_swiglu_checkpoint"
+    S, F = s.T * s.k, s.N // 2
+    _check(load_library().moe_swiglu_checkpoint(
+        plan.handle, _arg(c, plan, "GU", GU, S * 2 * F, _out_dtype(plan)),
+        _arg(c, plan, "H", H, S * F, _BF16, optional=True), _arg(c, plan, "codes", codes, S * 2 * F, torch.int8),
+        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _F32), _stream(stream, plan.device)), c)
+
+
+def moe_swiglu_checkpoint_backward(plan: Plan, dH, codes, scales, H, dGU, stream=None) -> None:
+    """dGU from dH and the 8-bit checkpoint, and the activation H again (H may be None)."""
+    s, c = plan.shape, "moe_swiglu_checkpoint_backward"
+    S, F = s.T * s.k, s.N // 2
+    _check(load_library().moe_swiglu_checkpoint_backward(
+        plan.handle, _arg(c, plan, "dH", dH, S * F, _BF16, _F32), _DTYPES[dH.dtype],
+        _arg(c, plan, "codes", codes, S * 2 * F, torch.int8),
+        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _F32),
+        _arg(c, plan, "H", H, S * F, _BF16, optional=True), _arg(c, plan, "dGU", dGU, S * 2 * F, _BF16),
+        _stream(stream, plan.device)), c)
+
+
+def moe_combine_backward(plan: Plan, dout, Y, topk_w, dest, dY, dtopk_w, stream=None) -> None:
+    """dY[dest[t,j]] = topk_w[t,j] dout[t] and dtopk_w[t,j] = <dout[t], Y[dest[t,j]]>."""
+    s, c = plan.shape, "moe_combine_backward"
+    S = s.T * s.k
+    _check(load_library().moe_combine_backward(
+        plan.handle, _arg(c, plan, "dout", dout, s.T * s.N, _BF16, _F32), _DTYPES[dout.dtype],
+        _arg(c, plan, "Y", Y, S * s.N, _out_dtype(plan)), _arg(c, plan, "topk_w", topk_w, S, _F32),
+        _arg(c, plan, "dest", dest, S, torch.int32), _arg(c, plan, "dY", dY, S * s.N, _BF16),
+        _arg(c, plan, "dtopk_w", dtopk_w, S, _F32), _stream(stream, plan.device)), c)
+
+
+def moe_grouped_gemm_dgrad(plan: Plan, dY, offsets, W, dA, workspace, dev_status, stream=None) -> None:
+    """dA[i] = dY[i] W[e(i)]^T, fp32 or bf16 by dA's type."""
+    s, c = plan.shape, "moe_grouped_gemm_dgrad"
+    S = s.T * s.k
+    _check(load_library().moe_grouped_gemm_dgrad(
+        plan.handle, _arg(c, plan, "dY", dY, S * s.N, _BF16), _arg(c, plan, "offsets", offsets, s.E + 1, torch.int32),
+        _arg(c, plan, "W", W, s.E * s.d * s.N, _BF16), _arg(c, plan, "dA", dA, S * s.d, _BF16, _F32),
+        _DTYPES[dA.dtype], _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
+
+
+def moe_grouped_gemm_wgrad(plan: Plan, A, dY, offsets, dW, workspace, dev_status, accumulate: bool = False,
+                           stream=None) -> None:
+    """dW[e] = A_e^T dY_e (accumulate: added to dW, fp32), fp32 or bf16 by dW's type."""
+    s, c = plan.shape, "moe_grouped_gemm_wgrad"
+    S = s.T * s.k
+    _check(load_library().moe_grouped_gemm_wgrad(
+        plan.handle, _arg(c, plan, "A", A, S * s.d, _BF16), _arg(c, plan, "dY", dY, S * s.N, _BF16),
+        _arg(c, plan, "offsets", offsets, s.E + 1, torch.int32),
+        _arg(c, plan, "dW", dW, s.E * s.d * s.N, _BF16, _F32), _DTYPES[dW.dtype], int(accumulate),
+        _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
 
 
 def moe_read_status(dev_status, stream=None) -> tuple[int, list[int]]:

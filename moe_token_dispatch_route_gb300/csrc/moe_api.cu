@@ -12,6 +12,7 @@
 
 #include "moe.h"
 #include "moe_internal.cuh"
+#include "train.cuh"
 
 using namespace moe;
 
@@ -152,6 +153,13 @@ bool plan_route_shape(moe_plan_t plan, int* T, int* E, int* k, int* route_blocks
     *k = plan->k;
     *route_blocks = plan->route_blocks;
     *device = plan->device;
+    return true;
+}
+
+bool plan_view(moe_plan_t plan, PlanView* v) {
+    if (!plan) return false;
+    *v = PlanView{plan->T, plan->d, plan->E, plan->k, plan->N, plan->S, plan->shape.out_dtype == MOE_OUT_BF16,
+                  plan->device, plan->sm_count, plan->timeout_ns};
     return true;
 }
 }  // namespace moe
