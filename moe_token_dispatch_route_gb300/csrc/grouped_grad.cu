@@ -1,8 +1,31 @@
-// The two gradients of the per-expert grouped product Y_i = A_i W_e(i):
+// The two gradients of the per-expert grouped product Y_i = A_i W_e(i), one persistent kernel:
 //   input gradient   dA_i = dY_i W_e(i)^T            (i over expert e's rows)
 //   weight gradient  dW_e = A_e^T dY_e               (summed over expert e's rows)
 // bf16 operands, fp32 sums, output fp32 or bf16 (rounded once).
+//
+// Both are written as out[r][c] = sum_k Q[r][k] P[c][k] with c the contiguous axis of the output:
+//   input gradient:  r = expert row, c = d, k = N;  P = W_e [d][N],   Q = dY [rows][N]  (K-major)
+//   weight gradient: r = d,          c = N, k = row; P = dY [rows][N], Q = A [rows][d]  (MN-major)
+// A tile is 256 c by up to 256 r, computed by a pair of CTAs (tcgen05 cta_group::2): P gives the
+// 256 rows of the MMA (128 per CTA), Q its columns.  So
+//  * the accumulator's TMEM lanes are consecutive c: the epilogue stores 128 contiguous bytes of
+//    an output row per warp straight from registers, with no transposition;
+//  * the ragged axis of the input gradient is the MMA's N, which goes in steps of 32: an expert
+//    with few rows costs few columns, and a row past the segment is a column that is not stored.
+// The weight gradient's ragged axis is the reduction.  Its last k-block is loaded in boxes of 16
+// rows, the MMAs stop at the last 16, and a warp zeroes the rows past the segment (another
+// expert's, whose NaN or infinity times zero would spread) in shared memory before the MMAs.
+//
+// Roles of a CTA (384 threads): warp 0 claims tiles (leader CTA) and loads P, warp 2 loads Q (two
+// issuing threads keep the stages fuller than one), warp 1 of the leader issues the MMAs, warp 3
+// zeroes the rows past a segment, warps 4-11 are the epilogue, each with one TMEM lane quarter and half of the columns.
+//
+// fp32 outputs: the tensor cores' running sum rounds towards zero at every step of 16 products,
+// which over a long reduction is a bias (relative error 1e-6 at 1024 products, 1.6e-5 at 14336).
+// So a sum runs in TMEM over 512 products and the epilogue adds these in registers; the two
+// accumulators alternate, so the MMAs do not wait.  bf16 outputs (2e-3 apart) take one sum.
 #include <algorithm>
+#include <atomic>
 
 #include "moe_internal.cuh"
 #include "train.cuh"
@@ -10,112 +33,669 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kChunk = 512, kCtaThreads = 256;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kGradThreads = 384;
+constexpr int kStages = 6;
+constexpr int kGradRing = 4;
+constexpr int kOpBytes = kTileM * kTileK * 2;  // 16 KB: one CTA's 128 rows (or columns) of an operand
+constexpr int kEpiFirst = 4, kEpiWarps = 8;
+constexpr int kBand = 8;       // row tiles per schedule band
+constexpr int kChunkKb = 8;    // k-blocks (of 64) per TMEM sum of an fp32 output
 
-__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+struct GradTile {
+    int e, c, r, pad;  // expert (-1: no more), column tile, row tile
+};
 
-__device__ __forceinline__ void put(const GroupedGradArgs& a, size_t i, float v) {
-    if (a.out_bf16) static_cast<uint16_t*>(a.out)[i] = (uint16_t)bf16x2(v, 0.f);
-    else if (a.accumulate) static_cast<float*>(a.out)[i] += v;
-    else static_cast<float*>(a.out)[i] = v;
-}
+struct GradCtl {
+    uint64_t full[kStages];   // leader: the stage's loads of both CTAs (its own of a block to be zeroed)
+    uint64_t empty[kStages];
+    uint64_t tail[kStages];   // peer: its own loads of a block to be zeroed
+    uint64_t fixed[kStages];  // leader: both CTAs have zeroed
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t sfull[kGradRing];
+    uint64_t sempty[kGradRing];
+    uint64_t mma_done;
+    GradTile ring[kGradRing];
+    uint32_t tmem_base;
+    int abort;
+};
 
-// Offsets have to ascend from 0 to S: they bound every access.
-__device__ __forceinline__ bool offsets_ok(const GroupedGradArgs& a) {
-    int bad = __ldg(a.offsets) != 0 || __ldg(a.offsets + a.E) != a.S;
-    for (int e = threadIdx.x; e < a.E; e += kCtaThreads) bad |= __ldg(a.offsets + e + 1) < __ldg(a.offsets + e);
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0) report_error(a.status, kStDevice, -2, __ldg(a.offsets + a.E), 0);
-    return !bad;
-}
+struct GradParams {
+    CUtensorMap p_map, q_map;      // whole blocks
+    CUtensorMap p_tail, q_tail;    // boxes of 16 rows
+    CUtensorMap p_pair, q_pair;    // weight gradient: two 64-column chunks in one copy
+    int p_paired, q_paired;
+    GroupedGradArgs a;
+    int c_tiles, r_tiles;          // r_tiles: weight gradient only
+    int chunk_kb;
+    int c_size;                    // extent of c: d or N
+};
 
-// A 64 x 64 tile of P Q with P [m][k] and Q [k][n] read through the given strides; 4 x 4
-// values a thread.  Sums of kChunk products are added up one by one: a single running sum
-// over 16384 products was 1.5e-6 (norm) from the 64-bit result.
-__device__ __forceinline__ void tile_product(const uint16_t* P, size_t pm, size_t pk, int m, const uint16_t* Q,
-                                             size_t qk, size_t qn, int n, int K, float (&sum)[4][4]) {
-    float acc[4][4] = {};
-    __shared__ float sp[kStep][kTile + 1], sq[kStep][kTile + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int k0 = 0; k0 < K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kCtaThreads) {
-            const int kp = pk == 1 ? i % kStep : i / kTile, r = pk == 1 ? i / kStep : i % kTile;
-            sp[kp][r] = (r < m && k0 + kp < K) ? widen(__ldg(P + r * pm + (k0 + kp) * pk)) : 0.f;
-            const int kq = qk == 1 ? i % kStep : i / kTile, c = qk == 1 ? i / kStep : i % kTile;
-            sq[kq][c] = (c < n && k0 + kq < K) ? widen(__ldg(Q + (k0 + kq) * qk + c * qn)) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kStep; ++kk) {
-            float p[4], q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = sp[kk][ty * 4 + i];
-                q[i] = sq[kk][tx * 4 + i];
+struct Wait {
+    volatile int* abort;
+    int32_t* status;
+    long long timeout_ns;
+};
+
+__device__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w, int where, bool honor_abort = true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((i & 127u) == 0) {
+            if (honor_abort && *w.abort) return false;
+            if (global_timer_ns() - t0 > (uint64_t)w.timeout_ns) {
+                report_error(w.status, kStDevice, where, -1, 0);
+                *w.abort = 1;
+                return false;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(p[i], q[j], acc[i][j]);
         }
-        __syncthreads();
-        if ((k0 + kStep) % kChunk == 0 || k0 + kStep >= K) {
+    }
+}
+
+// What a tile asks of every role.
+struct Shape {
+    int seg0;    // expert's first row
+    int nkb;     // k-blocks
+    int ksteps;  // MMA steps of 16 in the last k-block
+    int half;    // Q rows (columns) per CTA: half of the MMA's N
+    int fix;     // rows of the last k-block that are the expert's, when they end inside a step; else 0
+    int rows;    // valid output rows
+};
+
+template <bool WG>
+__device__ __forceinline__ Shape shape_of(const GradParams& p, const int* off, const GradTile& t) {
+    Shape s;
+    s.seg0 = off[t.e];
+    const int cnt = off[t.e + 1] - s.seg0;
+    const int K = WG ? cnt : p.a.N;
+    s.rows = min(256, (WG ? p.a.d : cnt) - 256 * t.r);
+    s.half = ((s.rows + 31) & ~31) / 2;
+    s.nkb = (K + kTileK - 1) / kTileK;
+    const int last = K - kTileK * (s.nkb - 1);
+    s.ksteps = (last + kUmmaK - 1) / kUmmaK;
+    s.fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
+    return s;
+}
+
+// the next slot of the schedule ring
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ void next() {
+        if (++slot == kGradRing) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+struct Stage {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ void next() {
+        if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ void skip(int n) {
+        s += n;
+        phase ^= (uint32_t)(s / kStages) & 1u;
+        s %= kStages;
+    }
+};
+
+// Takes the next tile from the ring and hands the slot back to the leader's scheduler; called by
+// one thread, or (WARP) by all lanes of a warp, which arrives once.
+template <bool WARP>
+__device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, const Wait& w, int where, bool leader,
+                                     uint32_t lead) {
+    bool got = bar_wait(smem_addr(&ctl->sfull[ring.slot]), ring.phase, w, where);
+    if (WARP) got = __all_sync(kFull, got);
+    if (!got) return false;
+    t = ctl->ring[ring.slot];
+    if (WARP) __syncwarp();  // every lane has read it
+    if (!WARP || (threadIdx.x & 31) == 0) {
+        const uint32_t se = smem_addr(&ctl->sempty[ring.slot]);
+        if (leader) mbar_arrive(se);
+        else mbar_arrive_remote(mapa_shared(se, lead));
+    }
+    ring.next();
+    return true;
+}
+
+// Loads of one operand of one k-block into `dst`.  K-major (input gradient): 64 k by `rows` rows
+// from (x = k, y = row).  MN-major (weight gradient): chunks of 64 columns by 64 rows (the last
+// k-block: by 16 * steps).
+__device__ __forceinline__ void load_kmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
+                                            uint32_t bar, int k, int row, int rows) {
+    if (rows == kTileM) {
+        tma_load_2d_pair(dst, whole, bar, k, row);
+    } else {
+        for (int i = 0; i < rows; i += 16) tma_load_2d_pair(dst + i * 128, part, bar, k, row + i);
+    }
+}
+
+__device__ __forceinline__ void load_mnmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
+                                             const CUtensorMap* pair, bool paired, uint32_t bar, int col, int row,
+                                             int chunks, int steps) {
+    if (steps == kTileK / kUmmaK) {
+        if (paired && chunks == 2) {
+            tma_load_3d_pair(dst, pair, bar, 0, row, col >> 6);
+        } else {
+            for (int j = 0; j < chunks; ++j) tma_load_2d_pair(dst + j * 8192, whole, bar, col + 64 * j, row);
+        }
+    } else {
+        for (int j = 0; j < chunks; ++j)
+            for (int i = 0; i < steps; ++i) tma_load_2d_pair(dst + j * 8192 + i * 2048, part, bar, col + 64 * j, row + 16 * i);
+    }
+}
+
+template <bool WG>
+__device__ __forceinline__ uint32_t q_bytes(const Shape& s, bool last) {
+    if (!WG) return (uint32_t)s.half * 128u;
+    const int chunks = (s.half + 63) / 64;
+    return (uint32_t)(chunks * (last ? s.ksteps * 2048 : 8192));
+}
+
+template <bool WG>
+__device__ __forceinline__ uint32_t p_bytes(const Shape& s, bool last) {
+    return WG && last ? (uint32_t)(2 * s.ksteps * 2048) : (uint32_t)kOpBytes;
+}
+
+// Warp 0, one thread: the leader claims tiles; both CTAs load their half of P.
+template <bool WG>
+__device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, const int* base, const short* order,
+                           uint8_t* sP, const Wait& w, bool leader, uint32_t peer, uint32_t rank) {
+    const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 0u;
+    const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
+    const uint32_t lead = leader ? rank : peer;
+    Ring ring;
+    Stage st;
+    int last_use[kStages];
+    uint32_t tail_phase = 0, tail_used = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum[i][j] += acc[i][j];
-                    acc[i][j] = 0.f;
+    for (int s = 0; s < kStages; ++s) last_use[s] = -1;
+
+    auto claim = [&](GradTile& t) -> bool {
+        if (!leader) {
+            const uint32_t sf = smem_addr(&ctl->sfull[ring.slot]);
+            mbar_arrive_expect_tx(sf, (uint32_t)sizeof(GradTile));
+            return take<false>(ctl, ring, t, w, 51, false, lead);
+        }
+        if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 52)) return false;
+        const uint32_t i = atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
+        t.e = -1;
+        t.c = t.r = t.pad = 0;
+        if (i < total) {
+            int local, rt;
+            if (WG) {
+                t.e = order[i / per_expert];
+                local = (int)(i % per_expert);
+                rt = p.r_tiles;
+            } else {
+                const int u = (int)(i / (uint32_t)p.c_tiles);
+                int lo = 0, hi = p.a.E;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (base[mid] <= u) lo = mid;
+                    else hi = mid;
                 }
+                t.e = lo;
+                local = (int)(i - (uint32_t)base[lo] * (uint32_t)p.c_tiles);
+                rt = base[lo + 1] - base[lo];
+            }
+            // bands of kBand row tiles, all column tiles of a band together: about as many row as
+            // column tiles run at a time, so each operand is read from DRAM about once
+            const int band = local / (kBand * p.c_tiles);
+            const int nr = min(kBand, rt - band * kBand);
+            const int j = local - band * kBand * p.c_tiles;
+            t.c = j / nr;
+            t.r = band * kBand + j % nr;
+        }
+        ctl->ring[ring.slot] = t;
+        const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), peer);
+        const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), peer);
+        st_async_v2(dst, (uint32_t)t.e, (uint32_t)t.c, bar);
+        st_async_v2(dst + 8, (uint32_t)t.r, 0u, bar);
+        mbar_arrive(smem_addr(&ctl->sfull[ring.slot]));
+        ring.next();
+        return true;
+    };
+
+    tma_prefetch_map(&p.p_map);
+    GradTile t, nxt;
+    bool ok = claim(t);
+    while (ok && t.e >= 0) {
+        const Shape s = shape_of<WG>(p, off, t);
+        const int c0 = 256 * t.c + 128 * (int)(rank & 1u);
+        bool have = false;
+        for (int kb = 0; kb < s.nkb; ++kb) {
+            if (leader && kb == 2) {  // the claim's round trip runs beside the loads
+                if (!(ok = claim(nxt))) break;
+                have = true;
+            }
+            if (!(ok = bar_wait(smem_addr(&ctl->empty[st.s]), st.phase ^ 1u, w, 53))) break;
+            const bool last = kb == s.nkb - 1;
+            const bool fix = WG && last && s.fix;
+            const uint32_t bytes = p_bytes<WG>(s, last) + q_bytes<WG>(s, last);
+            const uint32_t fl = smem_addr(&ctl->full[st.s]), tl = smem_addr(&ctl->tail[st.s]);
+            // a block to be zeroed lands on each CTA's own barrier, every other on the leader's
+            if (leader) mbar_arrive_expect_tx(fl, fix ? bytes : 2 * bytes);
+            else if (fix) mbar_arrive_expect_tx(tl, bytes);
+            const uint32_t bar = fix && !leader ? mapa_shared(tl, rank) : mapa_shared(fl, lead);
+            const uint32_t dst = smem_addr(sP + st.s * kOpBytes);
+            if (WG) load_mnmajor(dst, &p.p_map, &p.p_tail, &p.p_pair, p.p_paired && c0 + 128 <= p.c_size, bar, c0,
+                                 s.seg0 + kb * kTileK, 2, last ? s.ksteps : kTileK / kUmmaK);
+            else load_kmajor(dst, &p.p_map, nullptr, bar, kb * kTileK, t.e * p.a.d + c0, kTileM);
+            last_use[st.s] = (int)st.phase;
+            if (fix && !leader) {
+                tail_used |= 1u << st.s;
+                tail_phase ^= 1u << st.s;
+            }
+            st.next();
+        }
+        if (!ok) break;
+        if (!have && !claim(nxt)) break;
+        t = nxt;
+    }
+    // no load may still be landing when the CTA leaves
+    if (leader) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+            if (last_use[s] >= 0) bar_wait(smem_addr(&ctl->full[s]), (uint32_t)last_use[s], w, 54, false);
+    } else {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+            if (tail_used >> s & 1u) bar_wait(smem_addr(&ctl->tail[s]), (tail_phase >> s & 1u) ^ 1u, w, 55, false);
+    }
+}
+
+// Warp 2, one thread: both CTAs load their half of Q.
+template <bool WG>
+__device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sQ, const Wait& w, bool leader,
+                           uint32_t lead, uint32_t rank) {
+    Ring ring;
+    Stage st;
+    GradTile t;
+    tma_prefetch_map(&p.q_map);
+    for (;;) {
+        if (!take<false>(ctl, ring, t, w, 56, leader, lead) || t.e < 0) return;
+        const Shape s = shape_of<WG>(p, off, t);
+        const int r0 = 256 * t.r + s.half * (int)(rank & 1u);
+        const int chunks = (s.half + 63) / 64;
+        for (int kb = 0; kb < s.nkb; ++kb) {
+            if (!bar_wait(smem_addr(&ctl->empty[st.s]), st.phase ^ 1u, w, 57)) return;
+            const bool last = kb == s.nkb - 1;
+            const uint32_t bar = WG && last && s.fix && !leader ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank)
+                                                                : mapa_shared(smem_addr(&ctl->full[st.s]), lead);
+            const uint32_t dst = smem_addr(sQ + st.s * kOpBytes);
+            if (WG) load_mnmajor(dst, &p.q_map, &p.q_tail, &p.q_pair, p.q_paired && s.half == 128, bar, r0,
+                                 s.seg0 + kb * kTileK, chunks, last ? s.ksteps : kTileK / kUmmaK);
+            else load_kmajor(dst, &p.q_map, &p.q_tail, bar, kb * kTileK, s.seg0 + r0, s.half);
+            st.next();
         }
     }
 }
 
-// grid: (d / 64, row tiles strided over the CTAs of y, expert)
-__global__ void __launch_bounds__(kCtaThreads) dgrad_kernel(const GroupedGradArgs a) {
-    if (!offsets_ok(a)) return;
-    const int e = blockIdx.z, seg0 = __ldg(a.offsets + e), cnt = __ldg(a.offsets + e + 1) - seg0;
-    const int c0 = blockIdx.x * kTile, cols = min(kTile, a.d - c0);
-    for (int r0 = blockIdx.y * kTile; r0 < cnt; r0 += gridDim.y * kTile) {
-        const int rows = min(kTile, cnt - r0);
-        float acc[4][4] = {};
-        tile_product(a.dY + (size_t)(seg0 + r0) * a.N, a.N, 1, rows, a.W + ((size_t)e * a.d + c0) * a.N, 1, a.N, cols,
-                     a.N, acc);
-        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-                if (ty * 4 + i < rows && tx * 4 + j < cols)
-                    put(a, (size_t)(seg0 + r0 + ty * 4 + i) * a.d + c0 + tx * 4 + j, acc[i][j]);
+// Warp 3 (weight gradient): zeroes the rows of a last k-block that are not the expert's, up to
+// the end of its last step of 16, in both operands.
+__device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, const Wait& w,
+                          bool leader, uint32_t lead) {
+    const int lane = threadIdx.x & 31;
+    Ring ring;
+    Stage st;
+    uint32_t tail_phase = 0;
+    GradTile t;
+    for (;;) {
+        if (!take<true>(ctl, ring, t, w, 58, leader, lead) || t.e < 0) return;
+        const Shape s = shape_of<true>(p, off, t);
+        if (s.fix) {
+            Stage at = st;
+            at.skip(s.nkb - 1);
+            const bool landed = leader ? bar_wait(smem_addr(&ctl->full[at.s]), at.phase, w, 59)
+                                       : bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 60);
+            if (!__all_sync(kFull, landed)) return;
+            tail_phase ^= 1u << at.s;
+            const int rows = s.ksteps * kUmmaK - s.fix, chunks = (s.half + 63) / 64;
+            for (int i = lane; i < rows * 8 * (2 + chunks); i += 32) {
+                const int v = i & 7, r = (i >> 3) % rows, c = (i >> 3) / rows;
+                uint8_t* op = c < 2 ? sP + c * 8192 : sQ + (c - 2) * 8192;
+                *reinterpret_cast<uint4*>(op + at.s * kOpBytes + (s.fix + r) * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // before the MMAs read it
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&ctl->fixed[at.s]), lead));
+        }
+        st.skip(s.nkb);
     }
 }
 
-// grid: (N / 64, d / 64 strided over the CTAs of y, expert)
-__global__ void __launch_bounds__(kCtaThreads) wgrad_kernel(const GroupedGradArgs a) {
-    if (!offsets_ok(a)) return;
-    const int e = blockIdx.z, seg0 = __ldg(a.offsets + e), cnt = __ldg(a.offsets + e + 1) - seg0;
-    const int c0 = blockIdx.x * kTile, cols = min(kTile, a.N - c0);
-    for (int r0 = blockIdx.y * kTile; r0 < a.d; r0 += gridDim.y * kTile) {
-        const int rows = min(kTile, a.d - r0);
-        float acc[4][4] = {};
-        tile_product(a.A + (size_t)seg0 * a.d + r0, 1, a.d, rows, a.dY + (size_t)seg0 * a.N + c0, a.N, 1, cols, cnt, acc);
-        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-                if (ty * 4 + i < rows && tx * 4 + j < cols)
-                    put(a, ((size_t)e * a.d + r0 + ty * 4 + i) * a.N + c0 + tx * 4 + j, acc[i][j]);
+template <bool WG>
+__device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, uint32_t tmem,
+                         const Wait& w) {
+    // fp32 accumulator, bf16 operands; MN-major operands for the weight gradient; M = 256
+    constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (WG ? (1u << 15) | (1u << 16) : 0u) | (16u << 24);
+    constexpr uint32_t kLbo = WG ? 8192 : 16, kStep = WG ? 2048 : 32;
+    Ring ring;
+    Stage st;
+    uint32_t fixed_phase = 0;
+    int acc = 0;
+    uint32_t aphase = 0;
+    GradTile t;
+    bool ok = true;
+    while (ok) {
+        if (!take<false>(ctl, ring, t, w, 61, true, 0) || t.e < 0) break;
+        const Shape s = shape_of<WG>(p, off, t);
+        const uint32_t idesc = kDesc | ((uint32_t)(2 * s.half) >> 3) << 17;
+        int in_chunk = 0;
+        for (int kb = 0; kb < s.nkb; ++kb) {
+            if (in_chunk == 0) {
+                if (!(ok = bar_wait(smem_addr(&ctl->tempty[acc]), aphase ^ 1u, w, 62))) break;
+                tc_fence_after();
+            }
+            const bool last = kb == s.nkb - 1;
+            if (WG && last && s.fix) {
+                ok = bar_wait(smem_addr(&ctl->fixed[st.s]), fixed_phase >> st.s & 1u, w, 63);
+                fixed_phase ^= 1u << st.s;
+            } else {
+                ok = bar_wait(smem_addr(&ctl->full[st.s]), st.phase, w, 64);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc * 256);
+            const uint64_t pd = smem_desc_sw128(smem_addr(sP + st.s * kOpBytes), kLbo, 1024);
+            const uint64_t qd = smem_desc_sw128(smem_addr(sQ + st.s * kOpBytes), kLbo, 1024);
+            if (!last) {
+#pragma unroll
+                for (int kk = 0; kk < kTileK / kUmmaK; ++kk)
+                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (in_chunk | kk) != 0);
+            } else {
+                for (int kk = 0; kk < s.ksteps; ++kk)
+                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (in_chunk | kk) != 0);
+            }
+            umma_commit_pair_mc(smem_addr(&ctl->empty[st.s]), 0x3);
+            st.next();
+            if (++in_chunk == p.chunk_kb || last) {
+                umma_commit_pair_mc(smem_addr(&ctl->tfull[acc]), 0x3);
+                in_chunk = 0;
+                if ((acc ^= 1) == 0) aphase ^= 1u;
+            }
+        }
     }
+    umma_commit_pair(smem_addr(&ctl->mma_done));
+    bar_wait(smem_addr(&ctl->mma_done), 0u, w, 65, false);
+}
+
+// Warps 4-11: lane quarter q = warp & 3 (c), columns [128 h, 128 h + 128) (r).  All sums of a
+// thread, one c by 128 r, are in registers before the first store, so the accumulator is handed
+// back while the stores are still leaving.
+template <bool WG>
+__device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off, uint32_t tmem, const Wait& w,
+                              bool leader, uint32_t lead, uint32_t rank) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int q = warp & 3, h = (warp - kEpiFirst) >> 2;
+    Ring ring;
+    int acc = 0;
+    uint32_t aphase = 0;
+    GradTile t;
+    for (;;) {
+        if (!take<true>(ctl, ring, t, w, 66, leader, lead) || t.e < 0) return;
+        const Shape s = shape_of<WG>(p, off, t);
+        const int cols = min(128, s.rows - 128 * h);  // this warp's valid columns, may be <= 0
+        float sum[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        for (int kb = 0; kb < s.nkb; kb += p.chunk_kb) {
+            const bool ready = bar_wait(smem_addr(&ctl->tfull[acc]), aphase, w, 67);
+            if (!__all_sync(kFull, ready)) return;
+            tc_fence_after();
+            const uint32_t base = tmem + (uint32_t)(acc * 256 + 128 * h) + ((uint32_t)(32 * q) << 16);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                if (32 * g < cols) {
+                    uint32_t v[32];
+                    tmem_ld_32x32(base + 32 * g, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[32 * g + i] += __uint_as_float(v[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t te = smem_addr(&ctl->tempty[acc]);
+                if (leader) mbar_arrive(te);
+                else mbar_arrive_remote(mapa_shared(te, lead));
+            }
+            if ((acc ^= 1) == 0) aphase ^= 1u;
+        }
+        const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
+        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + 256 * t.r + 128 * h;
+        const size_t ld = (size_t)p.c_size;
+        const bool live = c < p.c_size;
+        if (WG && p.a.accumulate) {
+            if (live && s.nkb > 0) {
+                float* o = static_cast<float*>(p.a.out) + row0 * ld + c;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i < cols) atomicAdd(o + i * ld, sum[i]);  // one addition per element and call
+            }
+        } else if (p.a.out_bf16) {
+            // two rows at a time: even lanes store columns c, c + 1 of the first, odd lanes of the second
+            const int odd = lane & 1;
+            uint16_t* o = static_cast<uint16_t*>(p.a.out) + (row0 + odd) * ld + (c - odd);
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) {
+                const float give = odd ? sum[i] : sum[i + 1];
+                const float got2 = __shfl_xor_sync(kFull, give, 1);
+                const uint32_t v = odd ? bf16x2(got2, sum[i + 1]) : bf16x2(sum[i], got2);
+                if (live && i + odd < cols) __stcs(reinterpret_cast<uint32_t*>(o + i * ld), v);
+            }
+        } else if (live) {
+            float* o = static_cast<float*>(p.a.out) + row0 * ld + c;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                if (i < cols) __stcs(o + i * ld, sum[i]);
+        }
+    }
+}
+
+template <bool WG>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
+    grouped_grad_kernel(const __grid_constant__ GradParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* sP = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t* sQ = sP + kStages * kOpBytes;
+    GradCtl* ctl = reinterpret_cast<GradCtl*>(sQ + kStages * kOpBytes);
+    int* off = reinterpret_cast<int*>(ctl + 1);        // [E+1]
+    int* base = off + kMaxE + 1;                       // [E+1] row tiles before expert e (input gradient)
+    short* order = reinterpret_cast<short*>(base);     // [E] experts, most rows first (weight gradient)
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = (rank & 1u) == 0u;
+    const uint32_t peer = rank ^ 1u, lead = rank & ~1u;
+    const int E = p.a.E;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_addr(&ctl->full[s]), 1);
+            mbar_init(smem_addr(&ctl->empty[s]), 1);
+            mbar_init(smem_addr(&ctl->tail[s]), 1);
+            mbar_init(smem_addr(&ctl->fixed[s]), 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_addr(&ctl->tfull[a]), 1);
+            mbar_init(smem_addr(&ctl->tempty[a]), 2 * kEpiWarps);
+        }
+        for (int r = 0; r < kGradRing; ++r) {
+            mbar_init(smem_addr(&ctl->sfull[r]), 1);
+            // the leader's MMA thread, the peer's warp 0, and of both CTAs warp 2, the epilogue and warp 3
+            mbar_init(smem_addr(&ctl->sempty[r]), 2 + 2 * (1 + kEpiWarps + (WG ? 1 : 0)));
+        }
+        mbar_init(smem_addr(&ctl->mma_done), 1);
+        ctl->abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 2) {
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    // offsets have to ascend from 0 to S: they bound every access
+    int bad = 0;
+    for (int e = tid; e <= E; e += kGradThreads) {
+        const int v = __ldg(p.a.offsets + e);
+        off[e] = v;
+        bad |= e == 0 ? v != 0 : v < __ldg(p.a.offsets + e - 1);
+        bad |= e == E && v != p.a.S;
+    }
+    bad = __syncthreads_or(bad);
+    if (WG) {
+        // longest reductions first, so that none is left for the end
+        for (int e = tid; e < E; e += kGradThreads) {
+            const int cnt = off[e + 1] - off[e];
+            int before = 0, prev = off[0];
+            for (int f = 0; f < E; ++f) {
+                const int nx = off[f + 1], n = nx - prev;
+                prev = nx;
+                before += (n > cnt) || (n == cnt && f < e);
+            }
+            order[before] = (short)e;
+        }
+    } else if (warp == 0) {
+        int run = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < E ? (off[e + 1] - off[e] + 255) / 256 : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (e < E) base[e] = run + incl - n;
+            run += __shfl_sync(kFull, incl, 31);
+        }
+        if (lane == 0) base[E] = run;
+    }
+    if (bad && tid == 0) report_error(p.a.status, kStDevice, -2, off[E], 0);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // barriers and TMEM address of both CTAs are there
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const long long timeout = p.a.timeout_ns * 2 > 500000000LL ? p.a.timeout_ns * 2 : 500000000LL;
+    const Wait w{&ctl->abort, p.a.status, timeout};
+
+    if (!bad) {
+        if (warp == 0) {
+            if (lane == 0) producer_p<WG>(p, ctl, off, base, order, sP, w, leader, peer, rank);
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0 && leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w);
+            __syncwarp();
+        } else if (warp == 2) {
+            if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, lead, rank);
+            __syncwarp();
+        } else if (warp == 3) {
+            if (WG) zero_rows(p, ctl, off, sP, sQ, w, leader, lead);
+        } else {
+            epilogue_role<WG>(p, ctl, off, tmem, w, leader, lead, rank);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+    if (tid == 0) {
+        __threadfence();
+        const uint32_t prev = atomicAdd(p.a.hdr + kHdrDoneCtr, 1u);
+        if (prev == gridDim.x - 1) {  // every CTA has finished with the counters
+            __threadfence();
+            p.a.hdr[kHdrTileCtr] = 0u;
+            p.a.hdr[kHdrDoneCtr] = 0u;
+            __threadfence();
+        }
+    }
+}
+
+constexpr size_t kGradSmem = 1024 + (size_t)2 * kStages * kOpBytes + sizeof(GradCtl) + 2 * sizeof(int) * (kMaxE + 1);
+static_assert(kGradSmem <= 232448, "more than 227 KB of shared memory per CTA");
+static_assert(sizeof(GradTile) == 16, "a tile travels as two 8-byte stores");
+
+// Pairs of CTAs that are resident together on the current device; the kernel's attributes are set once per device.
+template <bool WG>
+cudaError_t resident_pairs(int device, int* pairs) {
+    static std::atomic<int> known[64];
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    *pairs = known[device].load(std::memory_order_acquire);
+    if (*pairs > 0) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(grouped_grad_kernel<WG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(pairs, grouped_grad_kernel<WG>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+    known[device].store(*pairs, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <bool WG>
+cudaError_t launch(GradParams& p, const GroupedGradArgs& a, int device, long long max_tiles, cudaStream_t stream) {
+    p.a = a;
+    p.chunk_kb = a.out_bf16 ? 1 << 30 : kChunkKb;
+    int pairs = 0;
+    const cudaError_t e = resident_pairs<WG>(device, &pairs);
+    if (e != cudaSuccess) return e;
+    pairs = (int)std::min<long long>(pairs, max_tiles);
+    grouped_grad_kernel<WG><<<2 * pairs, kGradThreads, kGradSmem, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int, cudaStream_t stream) {
-    dgrad_kernel<<<dim3((a.d + kTile - 1) / kTile, std::min(64, (a.S + kTile - 1) / kTile), a.E), kCtaThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
+    GradParams p = {};
+    p.c_size = a.d;
+    p.c_tiles = (a.d + 255) / 256;
+    const uint64_t S = (uint64_t)a.S, N = (uint64_t)a.N, wrows = (uint64_t)a.E * a.d;
+    if (!map_bf16_2d(&p.p_map, a.W, wrows, N, kTileK, kTileM) || !map_bf16_2d(&p.q_map, a.dY, S, N, kTileK, kTileM) ||
+        !map_bf16_2d(&p.q_tail, a.dY, S, N, kTileK, 16))
+        return cudaErrorInvalidValue;
+    return launch<false>(p, a, device, ((long long)a.S / 256 + a.E) * p.c_tiles, stream);
 }
 
-cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int, cudaStream_t stream) {
-    wgrad_kernel<<<dim3((a.N + kTile - 1) / kTile, std::min(64, (a.d + kTile - 1) / kTile), a.E), kCtaThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
+    GradParams p = {};
+    p.c_size = a.N;
+    p.c_tiles = (a.N + 255) / 256;
+    p.r_tiles = (a.d + 255) / 256;
+    const uint64_t S = (uint64_t)a.S, N = (uint64_t)a.N, d = (uint64_t)a.d;
+    if (!map_bf16_2d(&p.p_map, a.dY, S, N, 64, kTileK) || !map_bf16_2d(&p.p_tail, a.dY, S, N, 64, kUmmaK) ||
+        !map_bf16_2d(&p.q_map, a.A, S, d, 64, kTileK) || !map_bf16_2d(&p.q_tail, a.A, S, d, 64, kUmmaK))
+        return cudaErrorInvalidValue;
+    // two chunks of 64 columns in one copy where rows are whole chunks
+    p.p_paired = map_bf16_chunks(&p.p_pair, a.dY, S, N);
+    p.q_paired = map_bf16_chunks(&p.q_pair, a.A, S, d);
+    const long long tiles = (long long)a.E * p.c_tiles * p.r_tiles;
+    if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
+    return launch<true>(p, a, device, tiles, stream);
 }
 
 }  // namespace moe

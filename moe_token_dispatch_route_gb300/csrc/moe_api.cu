@@ -156,6 +156,15 @@ bool plan_route_shape(moe_plan_t plan, int* T, int* E, int* k, int* route_blocks
     return true;
 }
 
+bool map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                 uint32_t box_rows) {
+    return encode_bf16_2d(map, base, rows, cols, box_cols, box_rows);
+}
+
+bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols) {
+    return encode_bf16_chunks(map, base, rows, cols);
+}
+
 bool plan_view(moe_plan_t plan, PlanView* v) {
     if (!plan) return false;
     *v = PlanView{plan->T, plan->d, plan->E, plan->k, plan->N, plan->S, plan->shape.out_dtype == MOE_OUT_BF16,

@@ -105,8 +105,14 @@ struct GroupedGradArgs {
     long long timeout_ns;
     int S, d, E, N;
 };
-cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int sm_count, cudaStream_t stream);
-cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int sm_count, cudaStream_t stream);
+cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream);
+cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStream_t stream);
+
+// bf16 [rows][cols], 128-byte swizzle, and the same as 64-column chunks loaded two at a time
+// (false where cols % 64 != 0)
+bool map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                 uint32_t box_rows);
+bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols);
 
 #if defined(__CUDACC__)
 

@@ -138,7 +138,7 @@ moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY, const i
     if (!scope.ok) return MOE_ERR_CUDA;
     GroupedGradArgs a{nullptr, dY, W, offsets, dA, da_dtype == MOE_OUT_BF16, 0, dev_status,
                       static_cast<uint32_t*>(workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
-    return launched(launch_grouped_dgrad(a, v.sm_count, as_stream(stream)));
+    return launched(launch_grouped_dgrad(a, v.device, as_stream(stream)));
 }
 
 moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const uint16_t* dY, const int32_t* offsets,
@@ -160,7 +160,7 @@ moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const ui
     if (!need(A, 16) || !need(dY, 16) || !need(offsets, 4)) return MOE_ERR_INVALID_ARG;
     GroupedGradArgs a{A, dY, nullptr, offsets, dW, dw_dtype == MOE_OUT_BF16, accumulate, dev_status,
                       static_cast<uint32_t*>(workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
-    return launched(launch_grouped_wgrad(a, v.sm_count, s));
+    return launched(launch_grouped_wgrad(a, v.device, s));
 }
 
 }  // extern "C"
