@@ -47,9 +47,9 @@ struct GradTile {
 };
 
 struct GradCtl {
-    uint64_t full[kStages];   // leader: the stage's loads of both CTAs (its own of a block to be zeroed)
+    uint64_t full[kStages];   // leader: the stage's loads of both CTAs
     uint64_t empty[kStages];
-    uint64_t tail[kStages];   // peer: its own loads of a block to be zeroed
+    uint64_t tail[kStages];   // each CTA's own loads of a block to be zeroed
     uint64_t fixed[kStages];  // leader: both CTAs have zeroed
     uint64_t tfull[2];
     uint64_t tempty[2];
@@ -282,16 +282,22 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, co
             const bool fix = WG && last && s.fix;
             const uint32_t bytes = p_bytes<WG>(s, last) + q_bytes<WG>(s, last);
             const uint32_t fl = smem_addr(&ctl->full[st.s]), tl = smem_addr(&ctl->tail[st.s]);
-            // a block to be zeroed lands on each CTA's own barrier, every other on the leader's
-            if (leader) mbar_arrive_expect_tx(fl, fix ? bytes : 2 * bytes);
-            else if (fix) mbar_arrive_expect_tx(tl, bytes);
-            const uint32_t bar = fix && !leader ? mapa_shared(tl, rank) : mapa_shared(fl, lead);
+            // A block to be zeroed lands on each CTA's own tail barrier, which its warp 3 waits for:
+            // a stage's next tail comes only after the MMAs have read this one, so that warp, which
+            // skips the blocks in between, never falls a whole phase behind.  The leader's stage
+            // barrier then gets its arrival alone and keeps its phase.
+            if (fix) mbar_arrive_expect_tx(tl, bytes);
+            if (leader) {
+                if (fix) mbar_arrive(fl);
+                else mbar_arrive_expect_tx(fl, 2 * bytes);
+            }
+            const uint32_t bar = fix ? mapa_shared(tl, rank) : mapa_shared(fl, lead);
             const uint32_t dst = smem_addr(sP + st.s * kOpBytes);
             if (WG) load_mnmajor(dst, &p.p_map, &p.p_tail, &p.p_pair, p.p_paired && c0 + 128 <= p.c_size, bar, c0,
                                  s.seg0 + kb * kTileK, 2, last ? s.ksteps : kTileK / kUmmaK);
             else load_kmajor(dst, &p.p_map, nullptr, bar, kb * kTileK, t.e * p.a.d + c0, kTileM);
             last_use[st.s] = (int)st.phase;
-            if (fix && !leader) {
+            if (fix) {
                 tail_used |= 1u << st.s;
                 tail_phase ^= 1u << st.s;
             }
@@ -306,11 +312,10 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, co
 #pragma unroll
         for (int s = 0; s < kStages; ++s)
             if (last_use[s] >= 0) bar_wait(smem_addr(&ctl->full[s]), (uint32_t)last_use[s], w, 54, false);
-    } else {
-#pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            if (tail_used >> s & 1u) bar_wait(smem_addr(&ctl->tail[s]), (tail_phase >> s & 1u) ^ 1u, w, 55, false);
     }
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+        if (tail_used >> s & 1u) bar_wait(smem_addr(&ctl->tail[s]), (tail_phase >> s & 1u) ^ 1u, w, 55, false);
 }
 
 // Warp 2, one thread: both CTAs load their half of Q.
@@ -329,8 +334,8 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, ui
         for (int kb = 0; kb < s.nkb; ++kb) {
             if (!bar_wait(smem_addr(&ctl->empty[st.s]), st.phase ^ 1u, w, 57)) return;
             const bool last = kb == s.nkb - 1;
-            const uint32_t bar = WG && last && s.fix && !leader ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank)
-                                                                : mapa_shared(smem_addr(&ctl->full[st.s]), lead);
+            const uint32_t bar = WG && last && s.fix ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank)
+                                                     : mapa_shared(smem_addr(&ctl->full[st.s]), lead);
             const uint32_t dst = smem_addr(sQ + st.s * kOpBytes);
             if (WG) load_mnmajor(dst, &p.q_map, &p.q_tail, &p.q_pair, p.q_paired && s.half == 128, bar, r0,
                                  s.seg0 + kb * kTileK, chunks, last ? s.ksteps : kTileK / kUmmaK);
@@ -355,8 +360,7 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
         if (s.fix) {
             Stage at = st;
             at.skip(s.nkb - 1);
-            const bool landed = leader ? bar_wait(smem_addr(&ctl->full[at.s]), at.phase, w, 59)
-                                       : bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 60);
+            const bool landed = bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 59);
             if (!__all_sync(kFull, landed)) return;
             tail_phase ^= 1u << at.s;
             const int rows = s.ksteps * kUmmaK - s.fix, chunks = (s.half + 63) / 64;

@@ -439,6 +439,8 @@ GRAD_CASES = [
     ([255, 0, 257, 256], 512, 144),
     ([700], 1040, 528),
     ([2000, 5, 0, 300], 80, 592),
+    ([701, 1003, 77, 1], 272, 336),   # long odd reductions before another expert's rows
+    ([513] * 5 + [449], 528, 512),
     ([2] * 64, 256, 512),
     ([0] * 31 + [100], 128, 256),
 ]
