@@ -78,8 +78,7 @@ struct Wait {
     long long timeout_ns;
 };
 
-__device__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w, int where, bool honor_abort = true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, const Wait& w, int where, bool honor_abort) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
@@ -92,6 +91,11 @@ __device__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w, int where
             }
         }
     }
+}
+
+// Bounded wait on a barrier of this CTA; false when it gave up or the CTA is leaving.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w, int where, bool honor_abort = true) {
+    return mbar_try_wait_cluster(bar, parity) || bar_wait_slow(bar, parity, w, where, honor_abort);
 }
 
 // What a tile asks of every role.
@@ -386,6 +390,8 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     Ring ring;
     Stage st;
     uint32_t fixed_phase = 0;
+    const uint64_t pd0 = smem_desc_sw128(smem_addr(sP), kLbo, 1024), qd0 = smem_desc_sw128(smem_addr(sQ), kLbo, 1024);
+    const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
     int acc = 0;
     uint32_t aphase = 0;
     GradTile t;
@@ -394,43 +400,68 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
         if (!take<false>(ctl, ring, t, w, 61, true, 0) || t.e < 0) break;
         const Shape s = shape_of<WG>(p, off, t);
         const uint32_t idesc = kDesc | ((uint32_t)(2 * s.half) >> 3) << 17;
-        int in_chunk = 0;
-        for (int kb = 0; kb < s.nkb; ++kb) {
-            if (in_chunk == 0) {
-                if (!(ok = bar_wait(smem_addr(&ctl->tempty[acc]), aphase ^ 1u, w, 62))) break;
-                tc_fence_after();
-            }
-            const bool last = kb == s.nkb - 1;
-            if (WG && last && s.fix) {
-                ok = bar_wait(smem_addr(&ctl->fixed[st.s]), fixed_phase >> st.s & 1u, w, 63);
-                fixed_phase ^= 1u << st.s;
-            } else {
-                ok = bar_wait(smem_addr(&ctl->full[st.s]), st.phase, w, 64);
-            }
-            if (!ok) break;
+        for (int kb0 = 0; ok && kb0 < s.nkb; kb0 += p.chunk_kb) {
+            if (!(ok = bar_wait(smem_addr(&ctl->tempty[acc]), aphase ^ 1u, w, 62))) break;
             tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * 256);
-            const uint64_t pd = smem_desc_sw128(smem_addr(sP + st.s * kOpBytes), kLbo, 1024);
-            const uint64_t qd = smem_desc_sw128(smem_addr(sQ + st.s * kOpBytes), kLbo, 1024);
-            if (!last) {
+            // blocks of four steps in the loop (this thread's issue rate bounds the kernel), a
+            // short or zeroed last block after it
+            const int end = min(s.nkb - kb0, p.chunk_kb);
+            const bool tail = kb0 + end == s.nkb && (s.ksteps < kTileK / kUmmaK || (WG && s.fix));
+            const int whole = tail ? end - 1 : end;
+            for (int i = 0; i < whole; ++i) {
+                if (!(ok = bar_wait(full0 + st.s * 8, st.phase, w, 63))) break;
+                tc_fence_after();
+                const uint64_t pd = pd0 + (uint32_t)(st.s * (kOpBytes >> 4)), qd = qd0 + (uint32_t)(st.s * (kOpBytes >> 4));
+                umma_bf16_pair(d, pd, qd, idesc, i != 0);
 #pragma unroll
-                for (int kk = 0; kk < kTileK / kUmmaK; ++kk)
-                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (in_chunk | kk) != 0);
-            } else {
+                for (int kk = 1; kk < kTileK / kUmmaK; ++kk)
+                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, 1u);
+                umma_commit_pair_mc(empty0 + st.s * 8, 0x3);
+                st.next();
+            }
+            if (!ok) break;
+            if (tail) {
+                if (WG && s.fix) {
+                    ok = bar_wait(smem_addr(&ctl->fixed[st.s]), fixed_phase >> st.s & 1u, w, 64);
+                    fixed_phase ^= 1u << st.s;
+                } else {
+                    ok = bar_wait(full0 + st.s * 8, st.phase, w, 63);
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t pd = pd0 + (uint32_t)(st.s * (kOpBytes >> 4)), qd = qd0 + (uint32_t)(st.s * (kOpBytes >> 4));
                 for (int kk = 0; kk < s.ksteps; ++kk)
-                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (in_chunk | kk) != 0);
+                    umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (whole | kk) != 0);
+                umma_commit_pair_mc(empty0 + st.s * 8, 0x3);
+                st.next();
             }
-            umma_commit_pair_mc(smem_addr(&ctl->empty[st.s]), 0x3);
-            st.next();
-            if (++in_chunk == p.chunk_kb || last) {
-                umma_commit_pair_mc(smem_addr(&ctl->tfull[acc]), 0x3);
-                in_chunk = 0;
-                if ((acc ^= 1) == 0) aphase ^= 1u;
-            }
+            umma_commit_pair_mc(smem_addr(&ctl->tfull[acc]), 0x3);
+            if ((acc ^= 1) == 0) aphase ^= 1u;
         }
     }
     umma_commit_pair(smem_addr(&ctl->mma_done));
     bar_wait(smem_addr(&ctl->mma_done), 0u, w, 65, false);
+}
+
+// put(address, i, i < n) for i = 0, STEP, ... 126 with addresses `pitch` bytes apart.  The address is
+// stepped, not multiplied out: 128 products and bounds in flight spilled, and the whole epilogue
+// ran at 2.6 TB/s.  A warp whose lanes all have 128 rows skips the bounds.
+template <int STEP, class Put>
+__device__ __forceinline__ void store_rows(uint8_t* at, size_t pitch, int n, Put put) {
+    if (__all_sync(kFull, n > 128 - STEP)) {
+#pragma unroll
+        for (int i = 0; i < 128; i += STEP) {
+            put(at, i, true);
+            asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 128; i += STEP) {
+            put(at, i, i < n);
+            asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
+        }
+    }
 }
 
 // Warps 4-11: lane quarter q = warp & 3 (c), columns [128 h, 128 h + 128) (r).  All sums of a
@@ -450,8 +481,10 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
         const Shape s = shape_of<WG>(p, off, t);
         const int cols = min(128, s.rows - 128 * h);  // this warp's valid columns, may be <= 0
         float sum[128];
+        if (s.nkb == 0) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+            for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        }
         for (int kb = 0; kb < s.nkb; kb += p.chunk_kb) {
             const bool ready = bar_wait(smem_addr(&ctl->tfull[acc]), aphase, w, 67);
             if (!__all_sync(kFull, ready)) return;
@@ -464,7 +497,8 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
                     tmem_ld_32x32(base + 32 * g, v);
                     tmem_ld_wait(v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[32 * g + i] += __uint_as_float(v[i]);
+                    for (int i = 0; i < 32; ++i)
+                        sum[32 * g + i] = kb == 0 ? __uint_as_float(v[i]) : sum[32 * g + i] + __uint_as_float(v[i]);
                 }
             }
             tc_fence_before();
@@ -480,29 +514,27 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
         const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + 256 * t.r + 128 * h;
         const size_t ld = (size_t)p.c_size;
         const bool live = c < p.c_size;
-        if (WG && p.a.accumulate) {
-            if (live && s.nkb > 0) {
-                float* o = static_cast<float*>(p.a.out) + row0 * ld + c;
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i < cols) atomicAdd(o + i * ld, sum[i]);  // one addition per element and call
-            }
-        } else if (p.a.out_bf16) {
+        if (p.a.out_bf16) {
             // two rows at a time: even lanes store columns c, c + 1 of the first, odd lanes of the second
             const int odd = lane & 1;
-            uint16_t* o = static_cast<uint16_t*>(p.a.out) + (row0 + odd) * ld + (c - odd);
-#pragma unroll
-            for (int i = 0; i < 128; i += 2) {
-                const float give = odd ? sum[i] : sum[i + 1];
-                const float got2 = __shfl_xor_sync(kFull, give, 1);
-                const uint32_t v = odd ? bf16x2(got2, sum[i + 1]) : bf16x2(sum[i], got2);
-                if (live && i + odd < cols) __stcs(reinterpret_cast<uint32_t*>(o + i * ld), v);
+            uint8_t* o = static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2;
+            store_rows<2>(o, ld * 4, live ? cols - odd : 0, [&](uint8_t* at, int i, bool put) {
+                const float other = __shfl_xor_sync(kFull, odd ? sum[i] : sum[i + 1], 1);
+                const uint32_t v = odd ? bf16x2(other, sum[i + 1]) : bf16x2(sum[i], other);
+                if (put) __stcs(reinterpret_cast<uint32_t*>(at), v);
+            });
+        } else {
+            uint8_t* o = static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4;
+            if (WG && p.a.accumulate) {
+                // one addition per element and call: the order of the calls is the order of the sums
+                store_rows<1>(o, ld * 4, live && s.nkb > 0 ? cols : 0, [&](uint8_t* at, int i, bool put) {
+                    if (put) atomicAdd(reinterpret_cast<float*>(at), sum[i]);
+                });
+            } else {
+                store_rows<1>(o, ld * 4, live ? cols : 0, [&](uint8_t* at, int i, bool put) {
+                    if (put) __stcs(reinterpret_cast<float*>(at), sum[i]);
+                });
             }
-        } else if (live) {
-            float* o = static_cast<float*>(p.a.out) + row0 * ld + c;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-                if (i < cols) __stcs(o + i * ld, sum[i]);
         }
     }
 }
@@ -594,21 +626,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const long long timeout = p.a.timeout_ns * 2 > 500000000LL ? p.a.timeout_ns * 2 : 500000000LL;
     const Wait w{&ctl->abort, p.a.status, timeout};
 
-    if (!bad) {
-        if (warp == 0) {
-            if (lane == 0) producer_p<WG>(p, ctl, off, base, order, sP, w, leader, peer, rank);
+    // 384 threads x 168 registers: the four warps of single threads hand some to the epilogue's
+    if (warp < kEpiFirst) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (!bad) {
+            if (warp == 0) {
+                if (lane == 0) producer_p<WG>(p, ctl, off, base, order, sP, w, leader, peer, rank);
+            } else if (warp == 1) {
+                if (lane == 0 && leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w);
+            } else if (warp == 2) {
+                if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, lead, rank);
+            } else if (WG) {
+                zero_rows(p, ctl, off, sP, sQ, w, leader, lead);
+            }
             __syncwarp();
-        } else if (warp == 1) {
-            if (lane == 0 && leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w);
-            __syncwarp();
-        } else if (warp == 2) {
-            if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, lead, rank);
-            __syncwarp();
-        } else if (warp == 3) {
-            if (WG) zero_rows(p, ctl, off, sP, sQ, w, leader, lead);
-        } else {
-            epilogue_role<WG>(p, ctl, off, tmem, w, leader, lead, rank);
         }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if (!bad) epilogue_role<WG>(p, ctl, off, tmem, w, leader, lead, rank);
     }
 
     tc_fence_before();
