@@ -16,9 +16,12 @@
 // rows, the MMAs stop at the last 16, and a warp zeroes the rows past the segment (another
 // expert's, whose NaN or infinity times zero would spread) in shared memory before the MMAs.
 //
-// Roles of a CTA (384 threads): warp 0 claims tiles (leader CTA) and loads P, warp 2 loads Q (two
-// issuing threads keep the stages fuller than one), warp 1 of the leader issues the MMAs, warp 3
-// zeroes the rows past a segment, warps 4-11 are the epilogue, each with one TMEM lane quarter and half of the columns.
+// Roles of a CTA (384 threads): warp 0 loads P and warp 2 loads Q, warp 1 issues the MMAs (leader)
+// or claims the pair's tiles (peer), warp 3 zeroes the rows past a segment, warps 4-11 are the
+// epilogue, each with one TMEM lane quarter and half of the columns.  A k-block is 512 cycles of
+// the tensor cores; the loading threads have to issue theirs in less, so they do nothing else
+// (claims and tails inside their loop cost 250 cycles more, and the weight gradient waited for
+// loads 35% of the time).
 //
 // fp32 outputs: the tensor cores' running sum rounds towards zero at every step of 16 products,
 // which over a long reduction is a bias (relative error 1e-6 at 1024 products, 1.6e-5 at 14336).
@@ -63,8 +66,10 @@ struct GradCtl {
 
 struct GradParams {
     CUtensorMap p_map, q_map;      // whole blocks
-    CUtensorMap p_tail, q_tail;    // boxes of 16 rows
-    CUtensorMap p_pair, q_pair;    // weight gradient: two 64-column chunks in one copy
+    CUtensorMap q_tail;            // input gradient: boxes of 16 rows
+    // weight gradient, where rows are whole chunks of 64 columns: two chunks in one copy,
+    // of 64, 32 and 16 rows
+    CUtensorMap p_pair[3], q_pair[3];
     int p_paired, q_paired;
     GroupedGradArgs a;
     int c_tiles, r_tiles;          // r_tiles: weight gradient only
@@ -106,6 +111,10 @@ struct Shape {
     int half;    // Q rows (columns) per CTA: half of the MMA's N
     int fix;     // rows of the last k-block that are the expert's, when they end inside a step; else 0
     int rows;    // valid output rows
+    // weight gradient, last k-block: rows of its boxes (a last block of one or two steps is loaded in
+    // boxes of 16 or 32 rows where the columns are paired: an expert of a few rows costs few bytes)
+    int p_box, q_box;
+    bool q_paired;
 };
 
 template <bool WG>
@@ -120,6 +129,11 @@ __device__ __forceinline__ Shape shape_of(const GradParams& p, const int* off, c
     const int last = K - kTileK * (s.nkb - 1);
     s.ksteps = (last + kUmmaK - 1) / kUmmaK;
     s.fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
+    if (WG) {
+        s.q_paired = p.q_paired && s.half % 64 == 0;  // the peer's first column starts a chunk
+        s.p_box = p.p_paired && s.ksteps <= 2 ? kUmmaK * s.ksteps : kTileK;
+        s.q_box = s.q_paired && s.ksteps <= 2 ? kUmmaK * s.ksteps : kTileK;
+    }
     return s;
 }
 
@@ -151,11 +165,11 @@ struct Stage {
     }
 };
 
-// Takes the next tile from the ring and hands the slot back to the leader's scheduler; called by
-// one thread, or (WARP) by all lanes of a warp, which arrives once.
+// Takes the next tile from the ring and hands the slot back to the scheduler in the peer CTA;
+// called by one thread, or (WARP) by all lanes of a warp, which arrives once.
 template <bool WARP>
 __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, const Wait& w, int where, bool leader,
-                                     uint32_t lead) {
+                                     uint32_t sched) {
     bool got = bar_wait(smem_addr(&ctl->sfull[ring.slot]), ring.phase, w, where);
     if (WARP) got = __all_sync(kFull, got);
     if (!got) return false;
@@ -163,76 +177,24 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
     if (WARP) __syncwarp();  // every lane has read it
     if (!WARP || (threadIdx.x & 31) == 0) {
         const uint32_t se = smem_addr(&ctl->sempty[ring.slot]);
-        if (leader) mbar_arrive(se);
-        else mbar_arrive_remote(mapa_shared(se, lead));
+        if (leader) mbar_arrive_remote(mapa_shared(se, sched));
+        else mbar_arrive(se);
     }
     ring.next();
     return true;
 }
 
-// Loads of one operand of one k-block into `dst`.  K-major (input gradient): 64 k by `rows` rows
-// from (x = k, y = row).  MN-major (weight gradient): chunks of 64 columns by 64 rows (the last
-// k-block: by 16 * steps).
-__device__ __forceinline__ void load_kmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
-                                            uint32_t bar, int k, int row, int rows) {
-    if (rows == kTileM) {
-        tma_load_2d_pair(dst, whole, bar, k, row);
-    } else {
-        for (int i = 0; i < rows; i += 16) tma_load_2d_pair(dst + i * 128, part, bar, k, row + i);
-    }
-}
-
-__device__ __forceinline__ void load_mnmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
-                                             const CUtensorMap* pair, bool paired, uint32_t bar, int col, int row,
-                                             int chunks, int steps) {
-    if (steps == kTileK / kUmmaK) {
-        if (paired && chunks == 2) {
-            tma_load_3d_pair(dst, pair, bar, 0, row, col >> 6);
-        } else {
-            for (int j = 0; j < chunks; ++j) tma_load_2d_pair(dst + j * 8192, whole, bar, col + 64 * j, row);
-        }
-    } else {
-        for (int j = 0; j < chunks; ++j)
-            for (int i = 0; i < steps; ++i) tma_load_2d_pair(dst + j * 8192 + i * 2048, part, bar, col + 64 * j, row + 16 * i);
-    }
-}
-
+// Peer CTA's warp 1, one thread: claims tiles and writes them into both CTAs' rings.
 template <bool WG>
-__device__ __forceinline__ uint32_t q_bytes(const Shape& s, bool last) {
-    if (!WG) return (uint32_t)s.half * 128u;
-    const int chunks = (s.half + 63) / 64;
-    return (uint32_t)(chunks * (last ? s.ksteps * 2048 : 8192));
-}
-
-template <bool WG>
-__device__ __forceinline__ uint32_t p_bytes(const Shape& s, bool last) {
-    return WG && last ? (uint32_t)(2 * s.ksteps * 2048) : (uint32_t)kOpBytes;
-}
-
-// Warp 0, one thread: the leader claims tiles; both CTAs load their half of P.
-template <bool WG>
-__device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, const int* base, const short* order,
-                           uint8_t* sP, const Wait& w, bool leader, uint32_t peer, uint32_t rank) {
+__device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, const short* order, const Wait& w,
+                          uint32_t lead) {
     const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 0u;
     const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
-    const uint32_t lead = leader ? rank : peer;
     Ring ring;
-    Stage st;
-    int last_use[kStages];
-    uint32_t tail_phase = 0, tail_used = 0;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) last_use[s] = -1;
-
-    auto claim = [&](GradTile& t) -> bool {
-        if (!leader) {
-            const uint32_t sf = smem_addr(&ctl->sfull[ring.slot]);
-            mbar_arrive_expect_tx(sf, (uint32_t)sizeof(GradTile));
-            return take<false>(ctl, ring, t, w, 51, false, lead);
-        }
-        if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 52)) return false;
+    for (;;) {
+        if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
         const uint32_t i = atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
-        t.e = -1;
-        t.c = t.r = t.pad = 0;
+        GradTile t{-1, 0, 0, 0};
         if (i < total) {
             int local, rt;
             if (WG) {
@@ -260,90 +222,135 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, co
             t.r = band * kBand + j % nr;
         }
         ctl->ring[ring.slot] = t;
-        const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), peer);
-        const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), peer);
+        const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), lead);
+        const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), lead);
         st_async_v2(dst, (uint32_t)t.e, (uint32_t)t.c, bar);
         st_async_v2(dst + 8, (uint32_t)t.r, 0u, bar);
         mbar_arrive(smem_addr(&ctl->sfull[ring.slot]));
+        if (t.e < 0) return;
         ring.next();
-        return true;
-    };
+    }
+}
 
+// Loads of one operand of one k-block into `dst`.  K-major (input gradient): 64 k by `rows` rows
+// from (x = k, y = row).
+__device__ __forceinline__ void load_kmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
+                                            uint32_t bar, int k, int row, int rows) {
+    if (rows == kTileM) {
+        tma_load_2d_pair(dst, whole, bar, k, row);
+    } else {
+        for (int i = 0; i < rows; i += 16) tma_load_2d_pair(dst + i * 128, part, bar, k, row + i);
+    }
+}
+
+// MN-major (weight gradient): one or two chunks of 64 columns by `box` rows, one after the other.
+__device__ __forceinline__ void load_mnmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* pair, bool paired,
+                                             uint32_t bar, int col, int row, int chunks, int box) {
+    if (paired) {
+        tma_load_3d_pair(dst, pair + (box == kTileK ? 0 : box == 32 ? 1 : 2), bar, 0, row, col >> 6);
+    } else {
+        tma_load_2d_pair(dst, whole, bar, col, row);
+        if (chunks == 2) tma_load_2d_pair(dst + 8192, whole, bar, col + 64, row);
+    }
+}
+
+// bytes of one CTA's Q loads of a k-block whose boxes are `box` rows
+template <bool WG>
+__device__ __forceinline__ uint32_t q_bytes(const Shape& s, int box) {
+    if (!WG) return (uint32_t)s.half * 128u;
+    return s.q_paired || s.half > 64 ? (uint32_t)box * 256u : (uint32_t)box * 128u;
+}
+
+// Warp 0, one thread: this CTA's half of P, and the stage barriers' expected bytes.
+template <bool WG>
+__device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, const Wait& w, bool leader,
+                           uint32_t peer, uint32_t lead, uint32_t rank) {
+    const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
+    const uint32_t full_lead = mapa_shared(full0, lead), dst0 = smem_addr(sP);
+    const int side = 128 * (int)(rank & 1u);
+    Ring ring;
+    Stage st;
+    uint32_t uses = 0, tail_phase = 0, tail_used = 0;
+    GradTile t;
+    bool ok = true;
     tma_prefetch_map(&p.p_map);
-    GradTile t, nxt;
-    bool ok = claim(t);
-    while (ok && t.e >= 0) {
+    while (ok) {
+        if (leader)  // the description comes from the peer's scheduler
+            mbar_arrive_expect_tx(smem_addr(&ctl->sfull[ring.slot]), (uint32_t)sizeof(GradTile));
+        if (!take<false>(ctl, ring, t, w, 52, leader, peer) || t.e < 0) break;
         const Shape s = shape_of<WG>(p, off, t);
-        const int c0 = 256 * t.c + 128 * (int)(rank & 1u);
-        bool have = false;
-        for (int kb = 0; kb < s.nkb; ++kb) {
-            if (leader && kb == 2) {  // the claim's round trip runs beside the loads
-                if (!(ok = claim(nxt))) break;
-                have = true;
-            }
-            if (!(ok = bar_wait(smem_addr(&ctl->empty[st.s]), st.phase ^ 1u, w, 53))) break;
-            const bool last = kb == s.nkb - 1;
-            const bool fix = WG && last && s.fix;
-            const uint32_t bytes = p_bytes<WG>(s, last) + q_bytes<WG>(s, last);
-            const uint32_t fl = smem_addr(&ctl->full[st.s]), tl = smem_addr(&ctl->tail[st.s]);
+        const int c0 = 256 * t.c + side;
+        const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
+        const int row0 = WG ? s.seg0 : t.e * p.a.d + c0;
+        const uint32_t bytes = 2 * (kOpBytes + q_bytes<WG>(s, kTileK));
+        for (int kb = 0; kb < whole; ++kb) {
+            if (!(ok = bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 53))) break;
+            if (leader) mbar_arrive_expect_tx(full0 + 8 * st.s, bytes);
+            if (WG) load_mnmajor(dst0 + st.s * kOpBytes, &p.p_map, p.p_pair, p.p_paired, full_lead + 8 * st.s, c0,
+                                 row0 + kb * kTileK, 2, kTileK);
+            else tma_load_2d_pair(dst0 + st.s * kOpBytes, &p.p_map, full_lead + 8 * st.s, kb * kTileK, row0);
+            st.next();
+            ++uses;
+        }
+        if (ok && whole < s.nkb) {  // weight gradient: the last block
+            if (!(ok = bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 53))) break;
+            const uint32_t last = (uint32_t)s.p_box * 256u + q_bytes<WG>(s, s.q_box);
+            const uint32_t tail = smem_addr(&ctl->tail[st.s]);
             // A block to be zeroed lands on each CTA's own tail barrier, which its warp 3 waits for:
             // a stage's next tail comes only after the MMAs have read this one, so that warp, which
             // skips the blocks in between, never falls a whole phase behind.  The leader's stage
             // barrier then gets its arrival alone and keeps its phase.
-            if (fix) mbar_arrive_expect_tx(tl, bytes);
-            if (leader) {
-                if (fix) mbar_arrive(fl);
-                else mbar_arrive_expect_tx(fl, 2 * bytes);
-            }
-            const uint32_t bar = fix ? mapa_shared(tl, rank) : mapa_shared(fl, lead);
-            const uint32_t dst = smem_addr(sP + st.s * kOpBytes);
-            if (WG) load_mnmajor(dst, &p.p_map, &p.p_tail, &p.p_pair, p.p_paired && c0 + 128 <= p.c_size, bar, c0,
-                                 s.seg0 + kb * kTileK, 2, last ? s.ksteps : kTileK / kUmmaK);
-            else load_kmajor(dst, &p.p_map, nullptr, bar, kb * kTileK, t.e * p.a.d + c0, kTileM);
-            last_use[st.s] = (int)st.phase;
-            if (fix) {
+            if (s.fix) {
+                mbar_arrive_expect_tx(tail, last);
                 tail_used |= 1u << st.s;
                 tail_phase ^= 1u << st.s;
             }
+            if (leader) {
+                if (s.fix) mbar_arrive(full0 + 8 * st.s);
+                else mbar_arrive_expect_tx(full0 + 8 * st.s, 2 * last);
+            }
+            load_mnmajor(dst0 + st.s * kOpBytes, &p.p_map, p.p_pair, p.p_paired,
+                         s.fix ? mapa_shared(tail, rank) : full_lead + 8 * st.s, c0, row0 + whole * kTileK, 2, s.p_box);
             st.next();
+            ++uses;
         }
-        if (!ok) break;
-        if (!have && !claim(nxt)) break;
-        t = nxt;
     }
     // no load may still be landing when the CTA leaves
-    if (leader) {
-#pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            if (last_use[s] >= 0) bar_wait(smem_addr(&ctl->full[s]), (uint32_t)last_use[s], w, 54, false);
-    }
-#pragma unroll
-    for (int s = 0; s < kStages; ++s)
-        if (tail_used >> s & 1u) bar_wait(smem_addr(&ctl->tail[s]), (tail_phase >> s & 1u) ^ 1u, w, 55, false);
+    if (leader)
+        for (uint32_t u = uses > kStages ? uses - kStages : 0; u < uses; ++u)
+            bar_wait(full0 + 8 * (u % kStages), (u / kStages) & 1u, w, 54, false);
+    for (int i = 0; i < kStages; ++i)
+        if (tail_used >> i & 1u) bar_wait(smem_addr(&ctl->tail[i]), (tail_phase >> i & 1u) ^ 1u, w, 55, false);
 }
 
-// Warp 2, one thread: both CTAs load their half of Q.
+// Warp 2, one thread: this CTA's half of Q.
 template <bool WG>
 __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sQ, const Wait& w, bool leader,
-                           uint32_t lead, uint32_t rank) {
+                           uint32_t peer, uint32_t lead, uint32_t rank) {
+    const uint32_t empty0 = smem_addr(&ctl->empty[0]), full_lead = mapa_shared(smem_addr(&ctl->full[0]), lead);
+    const uint32_t dst0 = smem_addr(sQ);
     Ring ring;
     Stage st;
     GradTile t;
     tma_prefetch_map(&p.q_map);
     for (;;) {
-        if (!take<false>(ctl, ring, t, w, 56, leader, lead) || t.e < 0) return;
+        if (!take<false>(ctl, ring, t, w, 56, leader, peer) || t.e < 0) return;
         const Shape s = shape_of<WG>(p, off, t);
         const int r0 = 256 * t.r + s.half * (int)(rank & 1u);
-        const int chunks = (s.half + 63) / 64;
-        for (int kb = 0; kb < s.nkb; ++kb) {
-            if (!bar_wait(smem_addr(&ctl->empty[st.s]), st.phase ^ 1u, w, 57)) return;
-            const bool last = kb == s.nkb - 1;
-            const uint32_t bar = WG && last && s.fix ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank)
-                                                     : mapa_shared(smem_addr(&ctl->full[st.s]), lead);
-            const uint32_t dst = smem_addr(sQ + st.s * kOpBytes);
-            if (WG) load_mnmajor(dst, &p.q_map, &p.q_tail, &p.q_pair, p.q_paired && s.half == 128, bar, r0,
-                                 s.seg0 + kb * kTileK, chunks, last ? s.ksteps : kTileK / kUmmaK);
-            else load_kmajor(dst, &p.q_map, &p.q_tail, bar, kb * kTileK, s.seg0 + r0, s.half);
+        const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
+        const int chunks = s.half > 64 ? 2 : 1;
+        for (int kb = 0; kb < whole; ++kb) {
+            if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
+            if (WG) load_mnmajor(dst0 + st.s * kOpBytes, &p.q_map, p.q_pair, s.q_paired, full_lead + 8 * st.s, r0,
+                                 s.seg0 + kb * kTileK, chunks, kTileK);
+            else load_kmajor(dst0 + st.s * kOpBytes, &p.q_map, &p.q_tail, full_lead + 8 * st.s, kb * kTileK, s.seg0 + r0, s.half);
+            st.next();
+        }
+        if (whole < s.nkb) {
+            if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
+            load_mnmajor(dst0 + st.s * kOpBytes, &p.q_map, p.q_pair, s.q_paired,
+                         s.fix ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank) : full_lead + 8 * st.s, r0,
+                         s.seg0 + whole * kTileK, chunks, s.q_box);
             st.next();
         }
     }
@@ -352,14 +359,14 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, ui
 // Warp 3 (weight gradient): zeroes the rows of a last k-block that are not the expert's, up to
 // the end of its last step of 16, in both operands.
 __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, const Wait& w,
-                          bool leader, uint32_t lead) {
+                          bool leader, uint32_t peer, uint32_t lead) {
     const int lane = threadIdx.x & 31;
     Ring ring;
     Stage st;
     uint32_t tail_phase = 0;
     GradTile t;
     for (;;) {
-        if (!take<true>(ctl, ring, t, w, 58, leader, lead) || t.e < 0) return;
+        if (!take<true>(ctl, ring, t, w, 58, leader, peer) || t.e < 0) return;
         const Shape s = shape_of<true>(p, off, t);
         if (s.fix) {
             Stage at = st;
@@ -367,10 +374,10 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
             const bool landed = bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 59);
             if (!__all_sync(kFull, landed)) return;
             tail_phase ^= 1u << at.s;
-            const int rows = s.ksteps * kUmmaK - s.fix, chunks = (s.half + 63) / 64;
+            const int rows = s.ksteps * kUmmaK - s.fix, chunks = s.half > 64 ? 2 : 1;
             for (int i = lane; i < rows * 8 * (2 + chunks); i += 32) {
                 const int v = i & 7, r = (i >> 3) % rows, c = (i >> 3) / rows;
-                uint8_t* op = c < 2 ? sP + c * 8192 : sQ + (c - 2) * 8192;
+                uint8_t* op = c < 2 ? sP + c * s.p_box * 128 : sQ + (c - 2) * s.q_box * 128;
                 *reinterpret_cast<uint4*>(op + at.s * kOpBytes + (s.fix + r) * 128 + v * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();  // before the MMAs read it
@@ -383,7 +390,7 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
 
 template <bool WG>
 __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, uint32_t tmem,
-                         const Wait& w) {
+                         const Wait& w, uint32_t peer) {
     // fp32 accumulator, bf16 operands; MN-major operands for the weight gradient; M = 256
     constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (WG ? (1u << 15) | (1u << 16) : 0u) | (16u << 24);
     constexpr uint32_t kLbo = WG ? 8192 : 16, kStep = WG ? 2048 : 32;
@@ -397,7 +404,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     GradTile t;
     bool ok = true;
     while (ok) {
-        if (!take<false>(ctl, ring, t, w, 61, true, 0) || t.e < 0) break;
+        if (!take<false>(ctl, ring, t, w, 61, true, peer) || t.e < 0) break;
         const Shape s = shape_of<WG>(p, off, t);
         const uint32_t idesc = kDesc | ((uint32_t)(2 * s.half) >> 3) << 17;
         for (int kb0 = 0; ok && kb0 < s.nkb; kb0 += p.chunk_kb) {
@@ -430,7 +437,8 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
                 }
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t pd = pd0 + (uint32_t)(st.s * (kOpBytes >> 4)), qd = qd0 + (uint32_t)(st.s * (kOpBytes >> 4));
+                const uint64_t pd = smem_desc_sw128(smem_addr(sP) + st.s * kOpBytes, WG ? s.p_box * 128 : kLbo, 1024);
+                const uint64_t qd = smem_desc_sw128(smem_addr(sQ) + st.s * kOpBytes, WG ? s.q_box * 128 : kLbo, 1024);
                 for (int kk = 0; kk < s.ksteps; ++kk)
                     umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (whole | kk) != 0);
                 umma_commit_pair_mc(empty0 + st.s * 8, 0x3);
@@ -444,21 +452,21 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     bar_wait(smem_addr(&ctl->mma_done), 0u, w, 65, false);
 }
 
-// put(address, i, i < n) for i = 0, STEP, ... 126 with addresses `pitch` bytes apart.  The address is
-// stepped, not multiplied out: 128 products and bounds in flight spilled, and the whole epilogue
-// ran at 2.6 TB/s.  A warp whose lanes all have 128 rows skips the bounds.
-template <int STEP, class Put>
-__device__ __forceinline__ void store_rows(uint8_t* at, size_t pitch, int n, Put put) {
+// visit(address, i, i < n) for i = 0, STEP, ... 126, addresses `pitch` bytes apart for each step.  The
+// address is stepped, not multiplied out: 128 products in flight spilled, and the whole epilogue
+// ran at 2.6 TB/s.  A warp whose lanes all have their 128 rows skips the bounds.
+template <int STEP, class Visit>
+__device__ __forceinline__ void walk_rows(uint8_t* at, size_t pitch, int n, Visit visit) {
     if (__all_sync(kFull, n > 128 - STEP)) {
 #pragma unroll
         for (int i = 0; i < 128; i += STEP) {
-            put(at, i, true);
+            visit(at, i, true);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 128; i += STEP) {
-            put(at, i, i < n);
+            visit(at, i, i < n);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     }
@@ -469,7 +477,7 @@ __device__ __forceinline__ void store_rows(uint8_t* at, size_t pitch, int n, Put
 // back while the stores are still leaving.
 template <bool WG>
 __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off, uint32_t tmem, const Wait& w,
-                              bool leader, uint32_t lead, uint32_t rank) {
+                              bool leader, uint32_t peer, uint32_t lead, uint32_t rank) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int q = warp & 3, h = (warp - kEpiFirst) >> 2;
     Ring ring;
@@ -477,11 +485,20 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
     uint32_t aphase = 0;
     GradTile t;
     for (;;) {
-        if (!take<true>(ctl, ring, t, w, 66, leader, lead) || t.e < 0) return;
+        if (!take<true>(ctl, ring, t, w, 66, leader, peer) || t.e < 0) return;
         const Shape s = shape_of<WG>(p, off, t);
         const int cols = min(128, s.rows - 128 * h);  // this warp's valid columns, may be <= 0
+        const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
+        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + 256 * t.r + 128 * h;
+        const size_t ld = (size_t)p.c_size;
+        const int mine = c < p.c_size ? cols : 0;  // this lane's valid rows
+        const bool add = WG && p.a.accumulate;
+        if (add && s.nkb == 0) continue;  // nothing to add
         float sum[128];
-        if (s.nkb == 0) {
+        if (add) {  // what is there already, read while the MMAs run
+            walk_rows<1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
+                         [&](uint8_t* at, int i, bool in) { sum[i] = in ? __ldcs(reinterpret_cast<float*>(at)) : 0.f; });
+        } else if (s.nkb == 0) {
 #pragma unroll
             for (int i = 0; i < 128; ++i) sum[i] = 0.f;
         }
@@ -489,6 +506,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
             const bool ready = bar_wait(smem_addr(&ctl->tfull[acc]), aphase, w, 67);
             if (!__all_sync(kFull, ready)) return;
             tc_fence_after();
+            const bool first = kb == 0 && !add;
             const uint32_t base = tmem + (uint32_t)(acc * 256 + 128 * h) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -498,7 +516,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
                     tmem_ld_wait(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        sum[32 * g + i] = kb == 0 ? __uint_as_float(v[i]) : sum[32 * g + i] + __uint_as_float(v[i]);
+                        sum[32 * g + i] = first ? __uint_as_float(v[i]) : sum[32 * g + i] + __uint_as_float(v[i]);
                 }
             }
             tc_fence_before();
@@ -510,31 +528,18 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
             }
             if ((acc ^= 1) == 0) aphase ^= 1u;
         }
-        const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
-        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + 256 * t.r + 128 * h;
-        const size_t ld = (size_t)p.c_size;
-        const bool live = c < p.c_size;
         if (p.a.out_bf16) {
             // two rows at a time: even lanes store columns c, c + 1 of the first, odd lanes of the second
             const int odd = lane & 1;
-            uint8_t* o = static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2;
-            store_rows<2>(o, ld * 4, live ? cols - odd : 0, [&](uint8_t* at, int i, bool put) {
+            walk_rows<2>(static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2, ld * 4, mine - odd,
+                         [&](uint8_t* at, int i, bool in) {
                 const float other = __shfl_xor_sync(kFull, odd ? sum[i] : sum[i + 1], 1);
                 const uint32_t v = odd ? bf16x2(other, sum[i + 1]) : bf16x2(sum[i], other);
-                if (put) __stcs(reinterpret_cast<uint32_t*>(at), v);
+                if (in) __stcs(reinterpret_cast<uint32_t*>(at), v);
             });
         } else {
-            uint8_t* o = static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4;
-            if (WG && p.a.accumulate) {
-                // one addition per element and call: the order of the calls is the order of the sums
-                store_rows<1>(o, ld * 4, live && s.nkb > 0 ? cols : 0, [&](uint8_t* at, int i, bool put) {
-                    if (put) atomicAdd(reinterpret_cast<float*>(at), sum[i]);
-                });
-            } else {
-                store_rows<1>(o, ld * 4, live ? cols : 0, [&](uint8_t* at, int i, bool put) {
-                    if (put) __stcs(reinterpret_cast<float*>(at), sum[i]);
-                });
-            }
+            walk_rows<1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
+                         [&](uint8_t* at, int i, bool in) { if (in) __stcs(reinterpret_cast<float*>(at), sum[i]); });
         }
     }
 }
@@ -554,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = (rank & 1u) == 0u;
-    const uint32_t peer = rank ^ 1u, lead = rank & ~1u;
+    const uint32_t lead = rank & ~1u, sched = rank | 1u;
     const int E = p.a.E;
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -569,8 +574,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
         for (int r = 0; r < kGradRing; ++r) {
             mbar_init(smem_addr(&ctl->sfull[r]), 1);
-            // the leader's MMA thread, the peer's warp 0, and of both CTAs warp 2, the epilogue and warp 3
-            mbar_init(smem_addr(&ctl->sempty[r]), 2 + 2 * (1 + kEpiWarps + (WG ? 1 : 0)));
+            // (the peer's) the leader's MMA thread, and of both CTAs warps 0, 2, the epilogue and warp 3
+            mbar_init(smem_addr(&ctl->sempty[r]), 1 + 2 * (2 + kEpiWarps + (WG ? 1 : 0)));
         }
         mbar_init(smem_addr(&ctl->mma_done), 1);
         ctl->abort = 0;
@@ -631,19 +636,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (!bad) {
             if (warp == 0) {
-                if (lane == 0) producer_p<WG>(p, ctl, off, base, order, sP, w, leader, peer, rank);
+                if (lane == 0) producer_p<WG>(p, ctl, off, sP, w, leader, sched, lead, rank);
             } else if (warp == 1) {
-                if (lane == 0 && leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w);
+                if (lane == 0) {
+                    if (leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w, sched);
+                    else scheduler<WG>(p, ctl, base, order, w, lead);
+                }
             } else if (warp == 2) {
-                if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, lead, rank);
+                if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, sched, lead, rank);
             } else if (WG) {
-                zero_rows(p, ctl, off, sP, sQ, w, leader, lead);
+                zero_rows(p, ctl, off, sP, sQ, w, leader, sched, lead);
             }
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if (!bad) epilogue_role<WG>(p, ctl, off, tmem, w, leader, lead, rank);
+        if (!bad) epilogue_role<WG>(p, ctl, off, tmem, w, leader, sched, lead, rank);
     }
 
     tc_fence_before();
@@ -726,12 +734,13 @@ cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStrea
     p.c_tiles = (a.N + 255) / 256;
     p.r_tiles = (a.d + 255) / 256;
     const uint64_t S = (uint64_t)a.S, N = (uint64_t)a.N, d = (uint64_t)a.d;
-    if (!map_bf16_2d(&p.p_map, a.dY, S, N, 64, kTileK) || !map_bf16_2d(&p.p_tail, a.dY, S, N, 64, kUmmaK) ||
-        !map_bf16_2d(&p.q_map, a.A, S, d, 64, kTileK) || !map_bf16_2d(&p.q_tail, a.A, S, d, 64, kUmmaK))
+    if (!map_bf16_2d(&p.p_map, a.dY, S, N, 64, kTileK) || !map_bf16_2d(&p.q_map, a.A, S, d, 64, kTileK))
         return cudaErrorInvalidValue;
-    // two chunks of 64 columns in one copy where rows are whole chunks
-    p.p_paired = map_bf16_chunks(&p.p_pair, a.dY, S, N);
-    p.q_paired = map_bf16_chunks(&p.q_pair, a.A, S, d);
+    p.p_paired = p.q_paired = 1;
+    for (int i = 0; i < 3; ++i) {
+        p.p_paired &= map_bf16_chunks(&p.p_pair[i], a.dY, S, N, kTileK >> i);
+        p.q_paired &= map_bf16_chunks(&p.q_pair[i], a.A, S, d, kTileK >> i);
+    }
     const long long tiles = (long long)a.E * p.c_tiles * p.r_tiles;
     if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
     return launch<true>(p, a, device, tiles, stream);

@@ -104,14 +104,14 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 }
 
 // W [rows][cols] bf16 (cols % 64 == 0) as 64-column chunks: dims {64, rows, cols/64}
-// with strides {cols*2, 128} bytes, box 64 x 64 x 2, 128-byte swizzle: one copy moves
+// with strides {cols*2, 128} bytes, box 64 x box_rows x 2, 128-byte swizzle: one copy moves
 // two adjacent chunks, landing exactly as two boxes of the 2-D map one after the other.
-bool encode_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols) {
+bool encode_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 64) {
     auto enc = tensor_map_encoder();
     if (!enc || cols % 64 != 0) return false;
     cuuint64_t dims[3] = {64, rows, cols / 64};
     cuuint64_t strides[2] = {cols * 2, 128};
-    cuuint32_t box[3] = {64, 64, 2};
+    cuuint32_t box[3] = {64, box_rows, 2};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -161,8 +161,8 @@ bool map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
     return encode_bf16_2d(map, base, rows, cols, box_cols, box_rows);
 }
 
-bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols) {
-    return encode_bf16_chunks(map, base, rows, cols);
+bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    return encode_bf16_chunks(map, base, rows, cols, box_rows);
 }
 
 bool plan_view(moe_plan_t plan, PlanView* v) {

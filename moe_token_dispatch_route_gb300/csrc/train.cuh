@@ -112,7 +112,7 @@ cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStrea
 // (false where cols % 64 != 0)
 bool map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
                  uint32_t box_rows);
-bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols);
+bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 #if defined(__CUDACC__)
 
