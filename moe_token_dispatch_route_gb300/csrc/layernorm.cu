@@ -4,8 +4,16 @@
 // and, with xh = (x - mean) rstd and v = dy gamma,
 //   dx = rstd (v - sum v / d - xh (sum v xh) / d) + dres,
 //   dgamma = sum_t dy xh,  dbeta = sum_t dy.
-// All sums are fp32.
+// All sums are fp32.  Both directions are bound by HBM: each input is read once and stays in
+// registers between the sums over a row and the row's result.
+//
+// A row is held by TPR threads (a power of two from 8 to 1024), VPT vectors of 8 columns each, so
+// that the sums are one shuffle tree and, above a warp, one exchange through shared memory.  The
+// backward kernel also keeps dgamma and dbeta of its columns, over all the rows of its CTA, in
+// registers (shared memory for d > 8192); the CTAs' partial sums are added by a second kernel in
+// a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "train.cuh"
 
@@ -13,62 +21,156 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kThreads = 256;
 
-// Sums of N values over the CTA, the same bits in every thread.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Eight columns as they are in memory.
+template <bool BF16>
+struct Raw {
+    uint4 a;
+    __device__ void load(const void* base, size_t i) { a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i)); }
+    __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ float get(int j) const {
+        const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
+        return j & 1 ? bf16_hi(w) : bf16_lo(w);
+    }
+};
+template <>
+struct Raw<false> {
+    float4 a, b;
+    __device__ void load(const void* base, size_t i) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+        a = __ldcs(p);
+        b = __ldcs(p + 1);
+    }
+    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ float get(int j) const {
+        return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
+    }
+};
+
+__device__ __forceinline__ void weights8(const float* w, int c, float none, float (&v)[8]) {
+    if (w) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
-    __syncthreads();
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float s = 0.f;
-        for (int w = 0; w < kThreads / 32; ++w) s += red[i * 32 + w];
-        v[i] = s;
+        for (int j = 0; j < 8; ++j) v[j] = none;
     }
 }
 
+// CTA of a row group: at least `least` threads, whole rows.
+__host__ __device__ constexpr int cta_threads(int tpr, int least) { return tpr > least ? tpr : least; }
+
+// Sums of N values over the TPR threads of a row, the same bits in each of them.  `red` is used
+// by one call at a time: two calls in a row need a CTA barrier or another array between them.
+template <int TPR, int N, int CTA>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32]) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    if constexpr (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        const int warp = threadIdx.x >> 5, first = warp / kWarps * kWarps;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[i][warp] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += red[i][first + w];
+            v[i] = s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ forward
+
+template <bool XB, int TPR, int VPT>
+__global__ void __launch_bounds__(cta_threads(TPR, 128)) layernorm_kernel(const LayernormArgs a) {
+    constexpr int kCta = cta_threads(TPR, 128), kRows = kCta / TPR;
+    __shared__ float red_m[1][kCta / 32], red_v[1][kCta / 32];
+    const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const float inv_d = 1.f / (float)a.d;
+    for (long long t0 = (long long)blockIdx.x * kRows; t0 < a.T; t0 += (long long)gridDim.x * kRows) {
+        const long long t = t0 + group;
+        const size_t row = (size_t)t * a.d;
+        Raw<XB> x[VPT];
+        float s[1] = {0.f}, q[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c < a.d && t < a.T) x[i].load(a.x, row + c);
+            else x[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] += x[i].get(j);
+        row_sum<TPR, 1, kCta>(s, red_m);
+        const float mean = s[0] * inv_d;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if ((sub + i * TPR) * 8 < a.d) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[0] = fmaf(x[i].get(j) - mean, x[i].get(j) - mean, q[0]);
+            }
+        }
+        row_sum<TPR, 1, kCta>(q, red_v);
+        const float rstd = 1.f / sqrtf(q[0] * inv_d + a.eps);
+        if (t >= a.T) continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c >= a.d) continue;
+            float g[8], b[8], y[8];
+            weights8(a.gamma, c, 1.f, g);
+            weights8(a.beta, c, 0.f, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = fmaf((x[i].get(j) - mean) * rstd, g[j], b[j]);
+            store8<true>(a.y, row + c, y);
+        }
+        if (sub == 0) {
+            if (a.mean) a.mean[t] = mean;
+            if (a.rstd) a.rstd[t] = rstd;
+        }
+    }
+}
+
+// d > 32768: the row is read three times (from L2 after the first)
+constexpr int kWide = 1024;
 template <bool XB>
-__global__ void __launch_bounds__(kThreads) layernorm_kernel(const LayernormArgs a) {
-    __shared__ float red[64];
+__global__ void __launch_bounds__(kWide) layernorm_wide_kernel(const LayernormArgs a) {
+    __shared__ float red_m[1][kWide / 32], red_v[1][kWide / 32];
     const float inv_d = 1.f / (float)a.d;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         const size_t row = (size_t)t * a.d;
-        float s[1] = {0.f};
-        for (int c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
+        float s[1] = {0.f}, q[1] = {0.f};
+        for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8];
             load8<XB>(a.x, row + c, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] += v[j];
         }
-        block_sum(s, red);
+        row_sum<kWide, 1, kWide>(s, red_m);
         const float mean = s[0] * inv_d;
-        float q[1] = {0.f};
-        for (int c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
+        for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8];
             load8<XB>(a.x, row + c, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[0] = fmaf(v[j] - mean, v[j] - mean, q[0]);
         }
-        block_sum(q, red);
+        row_sum<kWide, 1, kWide>(q, red_v);
         const float rstd = 1.f / sqrtf(q[0] * inv_d + a.eps);
-        for (int c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
-            float v[8];
+        for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
+            float v[8], g[8], b[8];
             load8<XB>(a.x, row + c, v);
+            weights8(a.gamma, c, 1.f, g);
+            weights8(a.beta, c, 0.f, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float g = a.gamma ? __ldg(a.gamma + c + j) : 1.f;
-                const float b = a.beta ? __ldg(a.beta + c + j) : 0.f;
-                v[j] = fmaf((v[j] - mean) * rstd, g, b);
-            }
+            for (int j = 0; j < 8; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], b[j]);
             store8<true>(a.y, row + c, v);
         }
         if (threadIdx.x == 0) {
@@ -78,52 +180,213 @@ __global__ void __launch_bounds__(kThreads) layernorm_kernel(const LayernormArgs
     }
 }
 
-template <bool DYB, bool XB>
-__global__ void __launch_bounds__(kThreads) layernorm_dx_kernel(const LayernormBackwardArgs a) {
-    __shared__ float red[64];
+// ------------------------------------------------------------------ backward
+
+// A CTA has at least 256 threads, in whole rows.  Up to 512 threads of two vectors (d <= 8192) a
+// thread's dgamma and dbeta are in registers; above, 1024 threads leave 64 registers each and
+// they are in shared memory, [2][d].
+template <int TPR, bool XB>
+struct Back {
+    static constexpr int kCta = cta_threads(TPR, 256);
+    static constexpr int kRows = kCta / TPR;
+    static constexpr bool kShared = TPR > 512;
+    // 80 registers hold a row of bf16 x and fp32 dy with its residual and sums; fp32 x takes more
+    static constexpr int kCtasPerSm = kCta > 256 ? 1 : XB ? 3 : 2;
+};
+
+template <bool DYB, bool XB, int TPR, int VPT>
+__global__ void __launch_bounds__(Back<TPR, XB>::kCta, Back<TPR, XB>::kCtasPerSm)
+    layernorm_backward_kernel(const LayernormBackwardArgs a) {
+    using B = Back<TPR, XB>;
+    constexpr int kAcc = B::kShared ? 1 : VPT;
+    __shared__ float red[2][2][B::kCta / 32];
+    extern __shared__ float4 dyn4[];
+    float* dyn = reinterpret_cast<float*>(dyn4);
+    const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const float inv_d = 1.f / (float)a.d;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float dg[kAcc][8], db[kAcc][8];
+#pragma unroll
+    for (int i = 0; i < kAcc; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
+    if constexpr (B::kShared)  // every thread zeroes and uses its own columns alone
+        for (int c = sub * 8; c < a.d; c += TPR * 8)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dyn[c + j] = dyn[a.d + c + j] = 0.f;
+
+    const long long step = (long long)gridDim.x * B::kRows;
+    long long t = (long long)blockIdx.x * B::kRows + group;
+    Raw<XB> x[VPT], res[VPT];
+    Raw<DYB> dy[VPT];
+    int turn = 0;
+    for (long long t0 = (long long)blockIdx.x * B::kRows; t0 < a.T; t0 += step, t += step, turn ^= 1) {
+        const bool live = t < a.T;
+        const size_t row = (size_t)t * a.d;
+        const float mean = live ? __ldg(a.mean + t) : 0.f, rstd = live ? __ldg(a.rstd + t) : 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c < a.d && live) {
+                x[i].load(a.x, row + c);
+                dy[i].load(a.dy, row + c);
+                if (a.dres) res[i].load(a.dres, row + c);
+                else res[i].zero();
+            } else {
+                x[i].zero();
+                dy[i].zero();
+            }
+        }
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c >= a.d) continue;
+            float g[8];
+            weights8(a.gamma, c, 1.f, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float w = dy[i].get(j), xh = (x[i].get(j) - mean) * rstd, v = w * g[j];
+                s[0] += v;
+                s[1] = fmaf(v, xh, s[1]);
+                if constexpr (B::kShared) {
+                    dyn[c + j] = fmaf(w, xh, dyn[c + j]);
+                    dyn[a.d + c + j] += w;
+                } else {
+                    dg[i][j] = fmaf(w, xh, dg[i][j]);
+                    db[i][j] += w;
+                }
+            }
+        }
+        // the two arrays of `red` alternate, so one barrier a row is enough
+        row_sum<TPR, 2, B::kCta>(s, red[turn]);
+        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c >= a.d) continue;
+            float g[8], o[8];
+            weights8(a.gamma, c, 1.f, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = (x[i].get(j) - mean) * rstd;
+                o[j] = fmaf(rstd, dy[i].get(j) * g[j] - m1 - xh * m2, res[i].get(j));
+            }
+            store8<XB>(a.dx, row + c, o);
+        }
+    }
+    if (!a.dgamma && !a.dbeta) return;
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
+    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
+    if constexpr (B::kRows > 1) {  // the CTA's rows first: [group][2][TPR * VPT * 8]
+        constexpr int kCols = TPR * VPT * 8;
+        float* mine = dyn + (size_t)group * 2 * kCols;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                mine[(sub + i * TPR) * 8 + j] = dg[i][j];
+                mine[kCols + (sub + i * TPR) * 8 + j] = db[i][j];
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * kCols; c += B::kCta) {
+            const int col = c % kCols, half = c / kCols;
+            if (col >= a.d) continue;
+            float v = 0.f;
+            for (int g = 0; g < B::kRows; ++g) v += dyn[(size_t)g * 2 * kCols + c];
+            out[half * a.d + col] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (sub + i * TPR) * 8;
+            if (c >= a.d) continue;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 v;
+                    if constexpr (B::kShared) {
+                        v = *reinterpret_cast<const float4*>(dyn + h * a.d + c + j);
+                    } else {
+                        v = h ? make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3])
+                              : make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+                    }
+                    *reinterpret_cast<float4*>(out + h * a.d + c + j) = v;
+                }
+        }
+    }
+}
+
+// Adds the CTAs' partial sums, [parts][2 d] -> dgamma, dbeta: a CTA per 32 columns, its 16 warps
+// take every 16th part in order, then the warps' sums are added in order.
+constexpr int kJoin = 512;
+__global__ void __launch_bounds__(kJoin) layernorm_join_kernel(const float* partial, int parts, int d, float* dgamma, float* dbeta) {
+    __shared__ float sums[kJoin / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float v = 0.f;
+    if (c < 2 * d) {
+#pragma unroll 8
+        for (int p = warp; p < parts; p += kJoin / 32) v += __ldcg(partial + (size_t)p * 2 * d + c);
+    }
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < 2 * d) {
+        for (int w = 1; w < kJoin / 32; ++w) v += sums[w][lane];
+        if (c < d) {
+            if (dgamma) dgamma[c] = v;
+        } else if (dbeta) {
+            dbeta[c - d] = v;
+        }
+    }
+}
+
+// d > 16384: dx with the row read twice (from L2 the second time); dgamma and dbeta by columns
+template <bool DYB, bool XB>
+__global__ void __launch_bounds__(kWide) layernorm_wide_dx_kernel(const LayernormBackwardArgs a) {
+    __shared__ float red[2][2][kWide / 32];
+    const float inv_d = 1.f / (float)a.d;
+    int turn = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const size_t row = (size_t)t * a.d;
         const float mean = __ldg(a.mean + t), rstd = __ldg(a.rstd + t);
         float s[2] = {0.f, 0.f};
-        for (int c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
-            float v[8], x[8];
+        for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
+            float v[8], x[8], g[8];
             load8<DYB>(a.dy, row + c, v);
             load8<XB>(a.x, row + c, x);
+            weights8(a.gamma, c, 1.f, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float vg = v[j] * (a.gamma ? __ldg(a.gamma + c + j) : 1.f);
-                s[0] += vg;
-                s[1] = fmaf(vg, (x[j] - mean) * rstd, s[1]);
+                s[0] = fmaf(v[j], g[j], s[0]);
+                s[1] = fmaf(v[j] * g[j], (x[j] - mean) * rstd, s[1]);
             }
         }
-        block_sum(s, red);
+        row_sum<kWide, 2, kWide>(s, red[turn]);
         const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
-        for (int c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
-            float v[8], x[8], r[8] = {};
+        for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
+            float v[8], x[8], g[8], r[8] = {};
             load8<DYB>(a.dy, row + c, v);
             load8<XB>(a.x, row + c, x);
+            weights8(a.gamma, c, 1.f, g);
             if (a.dres) load8<XB>(a.dres, row + c, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float vg = v[j] * (a.gamma ? __ldg(a.gamma + c + j) : 1.f);
-                const float xh = (x[j] - mean) * rstd;
-                v[j] = fmaf(rstd, vg - m1 - xh * m2, r[j]);
-            }
+            for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, v[j] * g[j] - m1 - (x[j] - mean) * rstd * m2, r[j]);
             store8<XB>(a.dx, row + c, v);
         }
     }
 }
 
-// one CTA per 32 columns: 8 warps take every 8th row, then a sum over the warps
 template <bool DYB, bool XB>
-__global__ void __launch_bounds__(kThreads) layernorm_dweight_kernel(const LayernormBackwardArgs a) {
-    __shared__ float sg[kThreads / 32][32], sb[kThreads / 32][32];
+__global__ void __launch_bounds__(256) layernorm_wide_dweight_kernel(const LayernormBackwardArgs a) {
+    __shared__ float sg[8][32], sb[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float g = 0.f, b = 0.f;
     if (c < a.d) {
-        for (int t = warp; t < a.T; t += kThreads / 32) {
+        for (int t = warp; t < a.T; t += 8) {
             const size_t i = (size_t)t * a.d + c;
             const float dy = DYB ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.dy)[i] << 16)
                                  : static_cast<const float*>(a.dy)[i];
@@ -137,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) layernorm_dweight_kernel(const Layer
     sb[warp][lane] = b;
     __syncthreads();
     if (warp == 0 && c < a.d) {
-        for (int w = 1; w < kThreads / 32; ++w) {
+        for (int w = 1; w < 8; ++w) {
             g += sg[w][lane];
             b += sb[w][lane];
         }
@@ -146,24 +409,105 @@ __global__ void __launch_bounds__(kThreads) layernorm_dweight_kernel(const Layer
     }
 }
 
-template <bool DYB, bool XB>
-cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t stream) {
-    layernorm_dx_kernel<DYB, XB><<<std::min(a.T, sm_count * 8), kThreads, 0, stream>>>(a);
-    if (a.dgamma || a.dbeta)
-        layernorm_dweight_kernel<DYB, XB><<<(a.d + 31) / 32, kThreads, 0, stream>>>(a);
+// ------------------------------------------------------------------ launches
+
+int pow2_at_least(int v) {
+    int p = 8;
+    while (p < v) p *= 2;
+    return p;
+}
+
+// threads of a row: vectors of 8 columns, `vpt` a thread
+int row_threads(int d, int vpt) { return pow2_at_least((d / 8 + vpt - 1) / vpt); }
+
+constexpr int kForwardVpt = 4, kBackwardVpt = 2;
+constexpr int kForwardMax = 1024 * 8 * kForwardVpt, kBackwardMax = 1024 * 8 * kBackwardVpt;
+
+template <bool XB>
+cudaError_t forward(const LayernormArgs& a, int sm_count, cudaStream_t s) {
+    auto go = [&](auto tpr) {
+        constexpr int kTpr = decltype(tpr)::value, kCta = cta_threads(kTpr, 128), kRows = kCta / kTpr;
+        const int grid = std::min((a.T + kRows - 1) / kRows, sm_count * (2048 / kCta));
+        layernorm_kernel<XB, kTpr, kForwardVpt><<<grid, kCta, 0, s>>>(a);
+    };
+    if (a.d > kForwardMax) {
+        layernorm_wide_kernel<XB><<<std::min(a.T, sm_count), kWide, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    switch (row_threads(a.d, kForwardVpt)) {
+        case 8: go(std::integral_constant<int, 8>()); break;
+        case 16: go(std::integral_constant<int, 16>()); break;
+        case 32: go(std::integral_constant<int, 32>()); break;
+        case 64: go(std::integral_constant<int, 64>()); break;
+        case 128: go(std::integral_constant<int, 128>()); break;
+        case 256: go(std::integral_constant<int, 256>()); break;
+        case 512: go(std::integral_constant<int, 512>()); break;
+        default: go(std::integral_constant<int, 1024>()); break;
+    }
     return cudaGetLastError();
+}
+
+// CTAs of the backward kernel: resident all at once (three, two or one an SM by its registers)
+int backward_parts(int T, int d, bool x_bf16, int sm_count) {
+    const int tpr = row_threads(d, kBackwardVpt), cta = cta_threads(tpr, 256), rows = cta / tpr;
+    return std::min((T + rows - 1) / rows, sm_count * (cta > 256 ? 1 : x_bf16 ? 3 : 2));
+}
+
+cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((2 * a.d + 31) / 32);
+    cfg.blockDim = dim3(kJoin);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, layernorm_join_kernel, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
+}
+
+template <bool DYB, bool XB>
+cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t s) {
+    if (a.d > kBackwardMax) {
+        layernorm_wide_dx_kernel<DYB, XB><<<std::min(a.T, sm_count), kWide, 0, s>>>(a);
+        if (a.dgamma || a.dbeta) layernorm_wide_dweight_kernel<DYB, XB><<<(a.d + 31) / 32, 256, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    const int parts = backward_parts(a.T, a.d, XB, sm_count);
+    cudaError_t e = cudaSuccess;
+    auto go = [&](auto tpr) {
+        constexpr int kTpr = decltype(tpr)::value;
+        using B = Back<kTpr, XB>;
+        auto kernel = layernorm_backward_kernel<DYB, XB, kTpr, kBackwardVpt>;
+        const size_t smem = B::kShared ? (size_t)2 * a.d * 4 : B::kRows > 1 ? (size_t)B::kCta * kBackwardVpt * 8 * 2 * 4 : 0;
+        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) kernel<<<parts, B::kCta, smem, s>>>(a);
+    };
+    switch (row_threads(a.d, kBackwardVpt)) {
+        case 8: go(std::integral_constant<int, 8>()); break;
+        case 16: go(std::integral_constant<int, 16>()); break;
+        case 32: go(std::integral_constant<int, 32>()); break;
+        case 64: go(std::integral_constant<int, 64>()); break;
+        case 128: go(std::integral_constant<int, 128>()); break;
+        case 256: go(std::integral_constant<int, 256>()); break;
+        case 512: go(std::integral_constant<int, 512>()); break;
+        default: go(std::integral_constant<int, 1024>()); break;
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess && (a.dgamma || a.dbeta)) e = join(a, parts, s);
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_layernorm(const LayernormArgs& a, int sm_count, cudaStream_t stream) {
-    const int grid = std::min(a.T, sm_count * 8);
-    if (a.x_bf16) layernorm_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-    else layernorm_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.x_bf16 ? forward<true>(a, sm_count, stream) : forward<false>(a, sm_count, stream);
 }
 
-size_t layernorm_backward_scratch_bytes(int, int, int) { return 256; }
+size_t layernorm_backward_scratch_bytes(int T, int d, int sm_count) {
+    if (d > kBackwardMax || T == 0) return 256;
+    return (size_t)backward_parts(T, d, true, sm_count) * 2 * d * sizeof(float);
+}
 
 cudaError_t launch_layernorm_backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t stream) {
     if (a.dy_bf16) return a.x_bf16 ? backward<true, true>(a, sm_count, stream) : backward<true, false>(a, sm_count, stream);

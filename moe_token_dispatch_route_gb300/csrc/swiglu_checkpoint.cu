@@ -11,6 +11,10 @@
 //   forward:  H = silu(g) u from the values themselves;
 //   backward: with g, u the stored values and s = 1 / (1 + e^-g),
 //             dU = dH g s,  dG = dH u s (1 + g (1 - s)),  H = g s u again.
+//
+// Both kernels are bound by HBM.  A thread takes 8 columns of the gate and the same 8 of the up
+// half; the 16 threads of a block find its amax by shuffles.  The row and block of a thread's next unit are stepped,
+// not divided out.
 #include <algorithm>
 
 #include "train.cuh"
@@ -20,17 +24,18 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kLanes = kCkptBlock / 8;   // 16 lanes of 8 columns share a block
+constexpr int kLanes = kCkptBlock / 8;      // 16 threads of 8 columns share a block
 constexpr float kMinAmax = 3.7615819e-37f;  // 2^-121: the smallest amax that is stored
 
-// 1 / (1 + e^-g) from e^-|g|, which does not overflow: far negative g keeps its small result
+// 1 / (1 + e^-g) from e^-|g|, which does not overflow: far negative g keeps its small result.
+// The approximations are within a few units of 2^-24, far below the rounding to bf16 that follows.
 __device__ __forceinline__ float sigmoid(float g) {
-    const float e = expf(-fabsf(g));
-    return (g >= 0.f ? 1.f : e) / (1.f + e);
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g >= 0.f ? 1.f : e, 1.f + e);
 }
 
-// Scale of the block of 16 lanes and this lane's 8 codes (two words); every lane of the
-// warp takes part.
+// Scale of the 16 threads' block and this thread's 8 codes (two words); every lane of the warp
+// takes part.
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& scale) {
     uint32_t m = 0;  // magnitudes compare as integers: NaN > infinity > finite
 #pragma unroll
@@ -38,47 +43,65 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& scale) {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
     const float amax = __uint_as_float(m);
-    if (m >= 0x7F800000u) {
-        scale = __uint_as_float(0x7FC00000u);
-        return make_uint2(0u, 0u);
-    }
-    if (amax < kMinAmax) {
-        scale = 0.f;
+    if (m >= 0x7F800000u || amax < kMinAmax) {
+        scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
         return make_uint2(0u, 0u);
     }
     scale = __fdiv_rn(amax, 127.f);
     const float inv = __fdiv_rn(127.f, amax);
+    // fp32(x inv) is at most 127 and a bit in magnitude: adding 1.5 * 2^23 rounds it to the
+    // nearest even integer, whose two's complement is the sum's low byte
     uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = (uint32_t)__float2int_rn(__fmul_rn(v[j], inv)) & 0xFFu;
-    return make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+    for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
+    auto pack = [&](int i) {
+        return __byte_perm(__byte_perm(q[i], q[i + 1], 0x0040), __byte_perm(q[i + 2], q[i + 3], 0x0040), 0x5410);
+    };
+    return make_uint2(pack(0), pack(4));
 }
 
+// The stored values of 8 codes.  A code plus 128 is put in the low byte of 2^23's bits.
 __device__ __forceinline__ void restore8(uint2 q, float scale, float (&v)[8]) {
+    const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = (float)(int8_t)(q.x >> (8 * j)) * scale;
-        v[4 + j] = (float)(int8_t)(q.y >> (8 * j)) * scale;
-    }
+    for (int j = 0; j < 8; ++j)
+        v[j] = (__uint_as_float(__byte_perm(w[j / 4], 0x4B000000u, 0x7540 | (j & 3))) - 8388736.f) * scale;
 }
 
-// A half-warp takes one block of one row (its gate and its up columns).
+// (row, part) of unit u of `parts` per row, and the step to unit u + stride.
+struct Walk {
+    long long row, row_step;
+    int part, part_step, parts;
+    __device__ Walk(long long u, long long stride, int parts_) : parts(parts_) {
+        row = u / parts;
+        part = (int)(u - row * parts);
+        row_step = stride / parts;
+        part_step = (int)(stride - row_step * parts);
+    }
+    __device__ void next() {
+        row += row_step;
+        part += part_step;
+        if (part >= parts) {
+            part -= parts;
+            ++row;
+        }
+    }
+};
+
+// Sixteen threads take one block of one row (its gate and its up columns).
 template <bool GUB>
 __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(const SwigluCkptArgs a) {
     const int nb = ckpt_blocks(a.F);
-    const long long units = a.S * nb;
-    const int sub = threadIdx.x & (kLanes - 1);
-    const long long step = (long long)gridDim.x * (kThreads / kLanes);
-    const long long first = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    // whole warps stay in the loop (the shuffles need every lane)
-    for (long long u = first; u - (threadIdx.x & 31) / kLanes < units; u += step) {
-        const bool live_unit = u < units;
-        const long long row = live_unit ? u / nb : 0;
-        const int b = live_unit ? (int)(u % nb) : 0;
-        const int c = b * kCkptBlock + sub * 8;
-        const bool live = live_unit && c < a.F;  // F % 8 == 0
+    const int sub = threadIdx.x & (kLanes - 1), part = threadIdx.x / kLanes;
+    Walk at((long long)blockIdx.x * (kThreads / kLanes) + part, (long long)gridDim.x * (kThreads / kLanes), nb);
+    // every lane of a warp stays as long as the warp's first unit is a unit (the shuffles need all)
+    for (;; at.next()) {
+        const bool unit = at.row < a.S;
+        if (!__any_sync(kFull, unit)) return;
+        const int c = at.part * kCkptBlock + sub * 8;
+        const bool live = unit && c < a.F;  // F % 8 == 0
         float g[8] = {}, up[8] = {};
-        const size_t i = (size_t)row * 2 * a.F + c;
+        const size_t i = (size_t)at.row * 2 * a.F + c;
         if (live) {
             load8<GUB>(a.GU, i, g);
             load8<GUB>(a.GU, i + a.F, up);
@@ -86,63 +109,65 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(const Swigl
         float sg, su;
         const uint2 qg = quantize8(g, sg), qu = quantize8(up, su);
         if (!live) continue;
-        *reinterpret_cast<uint2*>(a.codes + i) = qg;
-        *reinterpret_cast<uint2*>(a.codes + i + a.F) = qu;
+        __stcs(reinterpret_cast<uint2*>(a.codes + i), qg);
+        __stcs(reinterpret_cast<uint2*>(a.codes + i + a.F), qu);
         if (sub == 0) {
-            a.scales[row * 2 * nb + b] = sg;
-            a.scales[row * 2 * nb + nb + b] = su;
+            a.scales[at.row * 2 * nb + at.part] = sg;
+            a.scales[at.row * 2 * nb + nb + at.part] = su;
         }
         if (a.H) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid(g[j]) * up[j];
-            store8<true>(a.H, (size_t)row * a.F + c, g);
+            store8<true>(a.H, (size_t)at.row * a.F + c, g);
         }
     }
 }
 
 template <bool DHB>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluCkptBackwardArgs a) {
-    const int nb = ckpt_blocks(a.F), nv = a.F / 8;
-    const long long units = a.S * nv;
-    for (long long u = (long long)blockIdx.x * kThreads + threadIdx.x; u < units; u += (long long)gridDim.x * kThreads) {
-        const long long row = u / nv;
-        const int c = (int)(u % nv) * 8;
-        const size_t i = (size_t)row * 2 * a.F + c, h = (size_t)row * a.F + c;
-        float g[8], up[8], dh[8];
-        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i)), __ldg(a.scales + row * 2 * nb + c / kCkptBlock), g);
-        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i + a.F)),
-                 __ldg(a.scales + row * 2 * nb + nb + c / kCkptBlock), up);
+    const int nb = ckpt_blocks(a.F);
+    Walk at((long long)blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads, a.F / 8);
+    for (; at.row < a.S; at.next()) {
+        const int c = at.part * 8;
+        const size_t i = (size_t)at.row * 2 * a.F + c, h = (size_t)at.row * a.F + c;
+        const float* scale = a.scales + at.row * 2 * nb + c / kCkptBlock;
+        float g[8], up[8], dh[8], dg[8], du[8];
+        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i)), __ldg(scale), g);
+        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i + a.F)), __ldg(scale + nb), up);
         load8<DHB>(a.dH, h, dh);
-        float dg[8], du[8], hh[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float s = sigmoid(g[j]), act = g[j] * s;
-            hh[j] = act * up[j];
+            const float s = sigmoid(g[j]), act = g[j] * s, du_dh = up[j] * dh[j];
+            dg[j] = du_dh * fmaf(act, 1.f - s, s);  // s (1 + g (1 - s))
             du[j] = dh[j] * act;
-            dg[j] = dh[j] * up[j] * (s * (1.f + g[j] * (1.f - s)));
+            g[j] = act * up[j];
         }
         store8<true>(a.dGU, i, dg);
         store8<true>(a.dGU, i + a.F, du);
-        if (a.H) store8<true>(a.H, h, hh);
+        if (a.H) store8<true>(a.H, h, g);
     }
+}
+
+// threads of a launch: `per_sm` CTAs on every SM, fewer where there is less to do
+template <class Kernel, class Args>
+cudaError_t go(Kernel kernel, const Args& a, long long threads, int sm_count, cudaStream_t stream) {
+    const long long ctas = (threads + kThreads - 1) / kThreads;
+    kernel<<<(int)std::min<long long>(ctas, (long long)sm_count * 8), kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu_checkpoint(const SwigluCkptArgs& a, int sm_count, cudaStream_t stream) {
-    const long long blocks = (a.S * ckpt_blocks(a.F) + kThreads / kLanes - 1) / (kThreads / kLanes);
-    const int grid = (int)std::min<long long>(blocks, (long long)sm_count * 8);
-    if (a.gu_bf16) swiglu_checkpoint_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-    else swiglu_checkpoint_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const long long threads = a.S * ckpt_blocks(a.F) * kLanes;
+    return a.gu_bf16 ? go(swiglu_checkpoint_kernel<true>, a, threads, sm_count, stream)
+                     : go(swiglu_checkpoint_kernel<false>, a, threads, sm_count, stream);
 }
 
 cudaError_t launch_swiglu_checkpoint_backward(const SwigluCkptBackwardArgs& a, int sm_count, cudaStream_t stream) {
-    const long long blocks = (a.S * (a.F / 8) + kThreads - 1) / kThreads;
-    const int grid = (int)std::min<long long>(blocks, (long long)sm_count * 8);
-    if (a.dh_bf16) swiglu_backward_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-    else swiglu_backward_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const long long threads = a.S * (a.F / 8);
+    return a.dh_bf16 ? go(swiglu_backward_kernel<true>, a, threads, sm_count, stream)
+                     : go(swiglu_backward_kernel<false>, a, threads, sm_count, stream);
 }
 
 }  // namespace moe
