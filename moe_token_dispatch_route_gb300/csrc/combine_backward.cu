@@ -45,7 +45,7 @@ struct Row8<false> {
 
 // GROUP threads (32 or 256) a token; KMAX slots at a time.
 template <bool DB, bool YB, int GROUP, int KMAX>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const CombineBackwardArgs a) {
+__global__ void __launch_bounds__(kThreads, KMAX == 8 ? (YB ? 3 : 2) : 4) combine_backward_kernel(const CombineBackwardArgs a) {
     __shared__ float red[2][KMAX][kThreads / 32];
     const int sub = threadIdx.x % GROUP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kTokens = kThreads / GROUP;

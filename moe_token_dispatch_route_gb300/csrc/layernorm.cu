@@ -209,10 +209,11 @@ __global__ void __launch_bounds__(Back<TPR, XB>::kCta, Back<TPR, XB>::kCtasPerSm
     for (int i = 0; i < kAcc; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
-    if constexpr (B::kShared)  // every thread zeroes and uses its own columns alone
-        for (int c = sub * 8; c < a.d; c += TPR * 8)
+    // kShared: four columns of vector i are float4 (4 i + 2 half + j / 4) TPR + sub: no two lanes share
+    // a bank; every thread zeroes and uses its own columns alone
+    if constexpr (B::kShared)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dyn[c + j] = dyn[a.d + c + j] = 0.f;
+        for (int i = 0; i < 4 * VPT; ++i) dyn4[i * TPR + sub] = make_float4(0.f, 0.f, 0.f, 0.f);
 
     const long long step = (long long)gridDim.x * B::kRows;
     long long t = (long long)blockIdx.x * B::kRows + group;
@@ -248,12 +249,27 @@ __global__ void __launch_bounds__(Back<TPR, XB>::kCta, Back<TPR, XB>::kCtasPerSm
                 const float w = dy[i].get(j), xh = (x[i].get(j) - mean) * rstd, v = w * g[j];
                 s[0] += v;
                 s[1] = fmaf(v, xh, s[1]);
-                if constexpr (B::kShared) {
-                    dyn[c + j] = fmaf(w, xh, dyn[c + j]);
-                    dyn[a.d + c + j] += w;
-                } else {
+                if constexpr (!B::kShared) {
                     dg[i][j] = fmaf(w, xh, dg[i][j]);
                     db[i][j] += w;
+                }
+            }
+            if constexpr (B::kShared) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    float4& g4 = dyn4[(4 * i + j / 4) * TPR + sub];
+                    float4& b4 = dyn4[(4 * i + 2 + j / 4) * TPR + sub];
+                    float4 u = g4, v = b4;
+                    u.x = fmaf(dy[i].get(j), (x[i].get(j) - mean) * rstd, u.x);
+                    u.y = fmaf(dy[i].get(j + 1), (x[i].get(j + 1) - mean) * rstd, u.y);
+                    u.z = fmaf(dy[i].get(j + 2), (x[i].get(j + 2) - mean) * rstd, u.z);
+                    u.w = fmaf(dy[i].get(j + 3), (x[i].get(j + 3) - mean) * rstd, u.w);
+                    v.x += dy[i].get(j);
+                    v.y += dy[i].get(j + 1);
+                    v.z += dy[i].get(j + 2);
+                    v.w += dy[i].get(j + 3);
+                    g4 = u;
+                    b4 = v;
                 }
             }
         }
@@ -307,7 +323,7 @@ __global__ void __launch_bounds__(Back<TPR, XB>::kCta, Back<TPR, XB>::kCtasPerSm
                 for (int h = 0; h < 2; ++h) {
                     float4 v;
                     if constexpr (B::kShared) {
-                        v = *reinterpret_cast<const float4*>(dyn + h * a.d + c + j);
+                        v = dyn4[(4 * i + 2 * h + j / 4) * TPR + sub];
                     } else {
                         v = h ? make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3])
                               : make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
@@ -479,7 +495,7 @@ cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t 
         constexpr int kTpr = decltype(tpr)::value;
         using B = Back<kTpr, XB>;
         auto kernel = layernorm_backward_kernel<DYB, XB, kTpr, kBackwardVpt>;
-        const size_t smem = B::kShared ? (size_t)2 * a.d * 4 : B::kRows > 1 ? (size_t)B::kCta * kBackwardVpt * 8 * 2 * 4 : 0;
+        const size_t smem = B::kShared ? (size_t)kTpr * kBackwardVpt * 8 * 2 * 4 : B::kRows > 1 ? (size_t)B::kCta * kBackwardVpt * 8 * 2 * 4 : 0;
         if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess) kernel<<<parts, B::kCta, smem, s>>>(a);
     };

@@ -34,23 +34,63 @@ __device__ __forceinline__ float sigmoid(float g) {
     return __fdividef(g >= 0.f ? 1.f : e, 1.f + e);
 }
 
-// Scale of the 16 threads' block and this thread's 8 codes (two words); every lane of the warp
-// takes part.
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& scale) {
-    uint32_t m = 0;  // magnitudes compare as integers: NaN > infinity > finite
+// Eight columns as they are in memory, so that the next unit's can be on their way in few registers.
+// amax(): their largest magnitude's fp32 bits.  Magnitudes compare as integers: NaN > infinity > finite.
+template <bool BF16>
+struct Raw;
+template <>
+struct Raw<true> {
+    uint4 a = {0, 0, 0, 0};
+    __device__ void load(const void* p, size_t i) { a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i)); }
+    __device__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-    const float amax = __uint_as_float(m);
-    if (m >= 0x7F800000u || amax < kMinAmax) {
-        scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
-        return make_uint2(0u, 0u);
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(w[j]);
+            v[2 * j + 1] = bf16_hi(w[j]);
+        }
     }
-    scale = __fdiv_rn(amax, 127.f);
-    const float inv = __fdiv_rn(127.f, amax);
-    // fp32(x inv) is at most 127 and a bit in magnitude: adding 1.5 * 2^23 rounds it to the
-    // nearest even integer, whose two's complement is the sum's low byte
+    __device__ uint32_t amax() const {  // two at a time
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & kAbs, a.y & kAbs), __vmaxu2(a.z & kAbs, a.w & kAbs));
+        return max(m & 0xFFFF0000u, m << 16);
+    }
+};
+template <>
+struct Raw<false> {
+    float4 a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
+    __device__ void load(const void* p, size_t i) {
+        a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+        b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
+    }
+    __device__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ uint32_t amax() const {
+        float v[8];
+        get(v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        return m;
+    }
+};
+
+// One of the four quotients of a block pair: a block's scale or its inverse.
+// amax / 127 (or NaN, or 0 below the smallest amax) and 127 / amax (0 where the codes are 0).
+__device__ __forceinline__ float quotient(uint32_t amax_bits, bool inverse) {
+    const float amax = __uint_as_float(amax_bits);
+    if (amax_bits >= 0x7F800000u) return inverse ? 0.f : __uint_as_float(0x7FC00000u);
+    if (amax < kMinAmax) return 0.f;
+    return __fdiv_rn(inverse ? 127.f : amax, inverse ? amax : 127.f);
+}
+
+// Eight codes.  fp32(x inv) is at most 127 and a bit in magnitude: adding 1.5 * 2^23 rounds it to
+// the nearest even integer, whose two's complement is the sum's low byte.  inv = 0 is a block of
+// codes 0 (x may be infinite or NaN there).
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+    if (inv == 0.f) return make_uint2(0u, 0u);
     uint32_t q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
@@ -88,37 +128,55 @@ struct Walk {
     }
 };
 
-// Sixteen threads take one block of one row (its gate and its up columns).
+// Sixteen threads take one block of one row (its gate and its up columns); the next unit's loads
+// are issued before this one's arithmetic.
 template <bool GUB>
 __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(const SwigluCkptArgs a) {
     const int nb = ckpt_blocks(a.F);
     const int sub = threadIdx.x & (kLanes - 1), part = threadIdx.x / kLanes;
     Walk at((long long)blockIdx.x * (kThreads / kLanes) + part, (long long)gridDim.x * (kThreads / kLanes), nb);
-    // every lane of a warp stays as long as the warp's first unit is a unit (the shuffles need all)
-    for (;; at.next()) {
-        const bool unit = at.row < a.S;
-        if (!__any_sync(kFull, unit)) return;
-        const int c = at.part * kCkptBlock + sub * 8;
-        const bool live = unit && c < a.F;  // F % 8 == 0
-        float g[8] = {}, up[8] = {};
-        const size_t i = (size_t)at.row * 2 * a.F + c;
-        if (live) {
-            load8<GUB>(a.GU, i, g);
-            load8<GUB>(a.GU, i + a.F, up);
+    auto live = [&] { return at.row < a.S && at.part * kCkptBlock + sub * 8 < a.F; };  // F % 8 == 0
+    Raw<GUB> rg, ru;
+    auto fetch = [&] {
+        if (live()) {
+            const size_t i = (size_t)at.row * 2 * a.F + at.part * kCkptBlock + sub * 8;
+            rg.load(a.GU, i);
+            ru.load(a.GU, i + a.F);
+        } else {
+            rg = ru = Raw<GUB>();
         }
-        float sg, su;
-        const uint2 qg = quantize8(g, sg), qu = quantize8(up, su);
-        if (!live) continue;
+    };
+    fetch();
+    // every lane of a warp stays while one of its lanes has a unit (the shuffles need all)
+    while (__any_sync(kFull, at.row < a.S)) {
+        float g[8], up[8];
+        rg.get(g);
+        ru.get(up);
+        uint32_t mg = rg.amax(), mu = ru.amax();
+        const bool mine = live(), stored = at.row < a.S;
+        const long long row = at.row;
+        const int b = at.part, c = b * kCkptBlock + sub * 8;
+        at.next();
+        fetch();
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+            mg = max(mg, __shfl_xor_sync(kFull, mg, o));
+            mu = max(mu, __shfl_xor_sync(kFull, mu, o));
+        }
+        // one division a thread: threads 0-3 of each four take the gate's inverse, the up's
+        // inverse, the gate's scale and the up's scale
+        const float quot = quotient(sub & 1 ? mu : mg, (sub & 2) == 0);
+        const float ig = __shfl_sync(kFull, quot, threadIdx.x & 28), iu = __shfl_sync(kFull, quot, (threadIdx.x & 28) + 1);
+        if ((sub == 2 || sub == 3) && stored) a.scales[row * 2 * nb + (sub & 1 ? nb : 0) + b] = quot;
+        if (!mine) continue;
+        const uint2 qg = codes8(g, ig), qu = codes8(up, iu);
+        const size_t i = (size_t)row * 2 * a.F + c;
         __stcs(reinterpret_cast<uint2*>(a.codes + i), qg);
         __stcs(reinterpret_cast<uint2*>(a.codes + i + a.F), qu);
-        if (sub == 0) {
-            a.scales[at.row * 2 * nb + at.part] = sg;
-            a.scales[at.row * 2 * nb + nb + at.part] = su;
-        }
         if (a.H) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid(g[j]) * up[j];
-            store8<true>(a.H, (size_t)at.row * a.F + c, g);
+            store8<true>(a.H, (size_t)row * a.F + c, g);
         }
     }
 }
@@ -127,14 +185,30 @@ template <bool DHB>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluCkptBackwardArgs a) {
     const int nb = ckpt_blocks(a.F);
     Walk at((long long)blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads, a.F / 8);
-    for (; at.row < a.S; at.next()) {
+    uint2 qg, qu;
+    float sg, su;
+    Raw<DHB> rh;
+    auto fetch = [&] {
+        if (at.row >= a.S) return;
+        const int c = at.part * 8;
+        const size_t i = (size_t)at.row * 2 * a.F + c;
+        const float* scale = a.scales + at.row * 2 * nb + c / kCkptBlock;
+        qg = __ldcs(reinterpret_cast<const uint2*>(a.codes + i));
+        qu = __ldcs(reinterpret_cast<const uint2*>(a.codes + i + a.F));
+        sg = __ldg(scale);
+        su = __ldg(scale + nb);
+        rh.load(a.dH, (size_t)at.row * a.F + c);
+    };
+    fetch();
+    while (at.row < a.S) {
         const int c = at.part * 8;
         const size_t i = (size_t)at.row * 2 * a.F + c, h = (size_t)at.row * a.F + c;
-        const float* scale = a.scales + at.row * 2 * nb + c / kCkptBlock;
         float g[8], up[8], dh[8], dg[8], du[8];
-        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i)), __ldg(scale), g);
-        restore8(__ldcs(reinterpret_cast<const uint2*>(a.codes + i + a.F)), __ldg(scale + nb), up);
-        load8<DHB>(a.dH, h, dh);
+        restore8(qg, sg, g);
+        restore8(qu, su, up);
+        rh.get(dh);
+        at.next();
+        fetch();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float s = sigmoid(g[j]), act = g[j] * s, du_dh = up[j] * dh[j];
