@@ -38,22 +38,34 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kGradThreads = 384;
-constexpr int kStages = 6;
+constexpr int kMaxStages = 10;
 constexpr int kGradRing = 4;
 constexpr int kOpBytes = kTileM * kTileK * 2;  // 16 KB: one CTA's 128 rows (or columns) of an operand
 constexpr int kEpiFirst = 4, kEpiWarps = 8;
 constexpr int kBand = 8;       // row tiles per schedule band
 constexpr int kChunkKb = 8;    // k-blocks (of 64) per TMEM sum of an fp32 output
 
+// The three forms of the kernel.  kNarrow is the input gradient for experts of few rows: row tiles
+// of 64, whose smaller Q leaves shared memory for ten stages of loads in flight.
+enum class Form { kInput, kNarrow, kWeight };
+template <Form F>
+struct Cfg {
+    static constexpr bool kWeight = F == Form::kWeight;
+    static constexpr int kRowTile = F == Form::kNarrow ? 64 : 256;
+    static constexpr int kQBytes = kRowTile / 2 * kTileK * 2;  // one CTA's half of Q
+    static constexpr int kStages = F == Form::kNarrow ? 10 : 6;
+    static constexpr int kWarpRows = kRowTile / 2;             // output rows of an epilogue warp
+};
+
 struct GradTile {
     int e, c, r, pad;  // expert (-1: no more), column tile, row tile
 };
 
 struct GradCtl {
-    uint64_t full[kStages];   // leader: the stage's loads of both CTAs
-    uint64_t empty[kStages];
-    uint64_t tail[kStages];   // each CTA's own loads of a block to be zeroed
-    uint64_t fixed[kStages];  // leader: both CTAs have zeroed
+    uint64_t full[kMaxStages];   // leader: the stage's loads of both CTAs
+    uint64_t empty[kMaxStages];
+    uint64_t tail[kMaxStages];   // each CTA's own loads of a block to be zeroed
+    uint64_t fixed[kMaxStages];  // leader: both CTAs have zeroed
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t sfull[kGradRing];
@@ -66,7 +78,7 @@ struct GradCtl {
 
 struct GradParams {
     CUtensorMap p_map, q_map;      // whole blocks
-    CUtensorMap q_tail;            // input gradient: boxes of 16 rows
+    CUtensorMap q_tail;            // input gradient: boxes of 16 rows (q_map: of kRowTile / 2)
     // weight gradient, where rows are whole chunks of 64 columns: two chunks in one copy,
     // of 64, 32 and 16 rows
     CUtensorMap p_pair[3], q_pair[3];
@@ -117,13 +129,15 @@ struct Shape {
     bool q_paired;
 };
 
-template <bool WG>
+template <Form F>
 __device__ __forceinline__ Shape shape_of(const GradParams& p, const int* off, const GradTile& t) {
+    constexpr bool WG = Cfg<F>::kWeight;
+    constexpr int kRow = Cfg<F>::kRowTile;
     Shape s;
     s.seg0 = off[t.e];
     const int cnt = off[t.e + 1] - s.seg0;
     const int K = WG ? cnt : p.a.N;
-    s.rows = min(256, (WG ? p.a.d : cnt) - 256 * t.r);
+    s.rows = min(kRow, (WG ? p.a.d : cnt) - kRow * t.r);
     s.half = ((s.rows + 31) & ~31) / 2;
     s.nkb = (K + kTileK - 1) / kTileK;
     const int last = K - kTileK * (s.nkb - 1);
@@ -149,6 +163,7 @@ struct Ring {
     }
 };
 
+template <int kStages>
 struct Stage {
     int s = 0;
     uint32_t phase = 0;
@@ -184,52 +199,59 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
     return true;
 }
 
-// Peer CTA's warp 1, one thread: claims tiles and writes them into both CTAs' rings.
-template <bool WG>
-__device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, const short* order, const Wait& w,
-                          uint32_t lead) {
+// Peer CTA's warp 1, one thread: claims the tiles after a pair's first (which is its own number) and
+// writes them into both CTAs' rings.
+template <Form F>
+__device__ GradTile tile_at(const GradParams& p, const int* base, const short* order, uint32_t i) {
+    constexpr bool WG = Cfg<F>::kWeight;
     const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 1u;
     const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
+    GradTile t{-1, 0, 0, 0};
+    if (i >= total) return t;
+    int local, rt;
+    if (WG) {
+        t.e = order[i / per_expert];
+        local = (int)(i % per_expert);
+        rt = p.r_tiles;
+    } else {
+        const int u = (int)(i / (uint32_t)p.c_tiles);
+        int lo = 0, hi = p.a.E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (base[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        t.e = lo;
+        local = (int)(i - (uint32_t)base[lo] * (uint32_t)p.c_tiles);
+        rt = base[lo + 1] - base[lo];
+    }
+    // bands of kBand row tiles, all column tiles of a band together: about as many row as column
+    // tiles run at a time, so each operand is read from DRAM about once
+    const int band = local / (kBand * p.c_tiles);
+    const int nr = min(kBand, rt - band * kBand);
+    const int j = local - band * kBand * p.c_tiles;
+    t.c = j / nr;
+    t.r = band * kBand + j % nr;
+    return t;
+}
+
+template <Form F>
+__device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, const short* order, const Wait& w,
+                          uint32_t lead) {
     Ring ring;
     const uint32_t pairs = gridDim.x / 2;
-    uint32_t i = blockIdx.x / 2;  // a pair's first tile needs no claim: a round trip of 1.1 us less at the start
-    for (bool first = true;; first = false) {
+    bool more = ctl->ring[0].e >= 0;
+    ring.next();  // the first tile was put into both rings before the roles began
+    while (more) {
         if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
-        if (!first) i = pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
-        GradTile t{-1, 0, 0, 0};
-        if (i < total) {
-            int local, rt;
-            if (WG) {
-                t.e = order[i / per_expert];
-                local = (int)(i % per_expert);
-                rt = p.r_tiles;
-            } else {
-                const int u = (int)(i / (uint32_t)p.c_tiles);
-                int lo = 0, hi = p.a.E;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (base[mid] <= u) lo = mid;
-                    else hi = mid;
-                }
-                t.e = lo;
-                local = (int)(i - (uint32_t)base[lo] * (uint32_t)p.c_tiles);
-                rt = base[lo + 1] - base[lo];
-            }
-            // bands of kBand row tiles, all column tiles of a band together: about as many row as
-            // column tiles run at a time, so each operand is read from DRAM about once
-            const int band = local / (kBand * p.c_tiles);
-            const int nr = min(kBand, rt - band * kBand);
-            const int j = local - band * kBand * p.c_tiles;
-            t.c = j / nr;
-            t.r = band * kBand + j % nr;
-        }
+        const GradTile t = tile_at<F>(p, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u));
         ctl->ring[ring.slot] = t;
         const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), lead);
         const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), lead);
         st_async_v2(dst, (uint32_t)t.e, (uint32_t)t.c, bar);
         st_async_v2(dst + 8, (uint32_t)t.r, 0u, bar);
         mbar_arrive(smem_addr(&ctl->sfull[ring.slot]));
-        if (t.e < 0) return;
+        more = t.e >= 0;
         ring.next();
     }
 }
@@ -237,8 +259,8 @@ __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, co
 // Loads of one operand of one k-block into `dst`.  K-major (input gradient): 64 k by `rows` rows
 // from (x = k, y = row).
 __device__ __forceinline__ void load_kmajor(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part,
-                                            uint32_t bar, int k, int row, int rows) {
-    if (rows == kTileM) {
+                                            uint32_t bar, int k, int row, int rows, int whole_rows) {
+    if (rows == whole_rows) {
         tma_load_2d_pair(dst, whole, bar, k, row);
     } else {
         for (int i = 0; i < rows; i += 16) tma_load_2d_pair(dst + i * 128, part, bar, k, row + i);
@@ -257,34 +279,36 @@ __device__ __forceinline__ void load_mnmajor(uint32_t dst, const CUtensorMap* wh
 }
 
 // bytes of one CTA's Q loads of a k-block whose boxes are `box` rows
-template <bool WG>
+template <Form F>
 __device__ __forceinline__ uint32_t q_bytes(const Shape& s, int box) {
-    if (!WG) return (uint32_t)s.half * 128u;
+    if (!Cfg<F>::kWeight) return (uint32_t)s.half * 128u;
     return s.q_paired || s.half > 64 ? (uint32_t)box * 256u : (uint32_t)box * 128u;
 }
 
 // Warp 0, one thread: this CTA's half of P, and the stage barriers' expected bytes.
-template <bool WG>
+template <Form F>
 __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, const Wait& w, bool leader,
                            uint32_t peer, uint32_t lead, uint32_t rank) {
+    using C = Cfg<F>;
+    constexpr bool WG = C::kWeight;
+    constexpr uint32_t kStages = C::kStages;
     const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
     const uint32_t full_lead = mapa_shared(full0, lead), dst0 = smem_addr(sP);
     const int side = 128 * (int)(rank & 1u);
     Ring ring;
-    Stage st;
+    Stage<C::kStages> st;
     uint32_t uses = 0, tail_phase = 0, tail_used = 0;
     GradTile t;
     bool ok = true;
-    tma_prefetch_map(&p.p_map);
-    while (ok) {
-        if (leader)  // the description comes from the peer's scheduler
+    for (bool first = true; ok; first = false) {
+        if (leader && !first)  // the description comes from the peer's scheduler
             mbar_arrive_expect_tx(smem_addr(&ctl->sfull[ring.slot]), (uint32_t)sizeof(GradTile));
         if (!take<false>(ctl, ring, t, w, 52, leader, peer) || t.e < 0) break;
-        const Shape s = shape_of<WG>(p, off, t);
+        const Shape s = shape_of<F>(p, off, t);
         const int c0 = 256 * t.c + side;
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
         const int row0 = WG ? s.seg0 : t.e * p.a.d + c0;
-        const uint32_t bytes = 2 * (kOpBytes + q_bytes<WG>(s, kTileK));
+        const uint32_t bytes = 2 * (kOpBytes + q_bytes<F>(s, kTileK));
         for (int kb = 0; kb < whole; ++kb) {
             if (!(ok = bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 53))) break;
             if (leader) mbar_arrive_expect_tx(full0 + 8 * st.s, bytes);
@@ -296,7 +320,7 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, ui
         }
         if (ok && whole < s.nkb) {  // weight gradient: the last block
             if (!(ok = bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 53))) break;
-            const uint32_t last = (uint32_t)s.p_box * 256u + q_bytes<WG>(s, s.q_box);
+            const uint32_t last = (uint32_t)s.p_box * 256u + q_bytes<F>(s, s.q_box);
             const uint32_t tail = smem_addr(&ctl->tail[st.s]);
             // A block to be zeroed lands on each CTA's own tail barrier, which its warp 3 waits for:
             // a stage's next tail comes only after the MMAs have read this one, so that warp, which
@@ -321,36 +345,37 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, ui
     if (leader)
         for (uint32_t u = uses > kStages ? uses - kStages : 0; u < uses; ++u)
             bar_wait(full0 + 8 * (u % kStages), (u / kStages) & 1u, w, 54, false);
-    for (int i = 0; i < kStages; ++i)
+    for (uint32_t i = 0; i < kStages; ++i)
         if (tail_used >> i & 1u) bar_wait(smem_addr(&ctl->tail[i]), (tail_phase >> i & 1u) ^ 1u, w, 55, false);
 }
 
 // Warp 2, one thread: this CTA's half of Q.
-template <bool WG>
+template <Form F>
 __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sQ, const Wait& w, bool leader,
                            uint32_t peer, uint32_t lead, uint32_t rank) {
+    using C = Cfg<F>;
+    constexpr bool WG = C::kWeight;
     const uint32_t empty0 = smem_addr(&ctl->empty[0]), full_lead = mapa_shared(smem_addr(&ctl->full[0]), lead);
     const uint32_t dst0 = smem_addr(sQ);
     Ring ring;
-    Stage st;
+    Stage<C::kStages> st;
     GradTile t;
-    tma_prefetch_map(&p.q_map);
     for (;;) {
         if (!take<false>(ctl, ring, t, w, 56, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<WG>(p, off, t);
-        const int r0 = 256 * t.r + s.half * (int)(rank & 1u);
+        const Shape s = shape_of<F>(p, off, t);
+        const int r0 = C::kRowTile * t.r + s.half * (int)(rank & 1u);
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
         const int chunks = s.half > 64 ? 2 : 1;
         for (int kb = 0; kb < whole; ++kb) {
             if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
-            if (WG) load_mnmajor(dst0 + st.s * kOpBytes, &p.q_map, p.q_pair, s.q_paired, full_lead + 8 * st.s, r0,
+            if (WG) load_mnmajor(dst0 + st.s * C::kQBytes, &p.q_map, p.q_pair, s.q_paired, full_lead + 8 * st.s, r0,
                                  s.seg0 + kb * kTileK, chunks, kTileK);
-            else load_kmajor(dst0 + st.s * kOpBytes, &p.q_map, &p.q_tail, full_lead + 8 * st.s, kb * kTileK, s.seg0 + r0, s.half);
+            else load_kmajor(dst0 + st.s * C::kQBytes, &p.q_map, &p.q_tail, full_lead + 8 * st.s, kb * kTileK, s.seg0 + r0, s.half, C::kRowTile / 2);
             st.next();
         }
         if (whole < s.nkb) {
             if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
-            load_mnmajor(dst0 + st.s * kOpBytes, &p.q_map, p.q_pair, s.q_paired,
+            load_mnmajor(dst0 + st.s * C::kQBytes, &p.q_map, p.q_pair, s.q_paired,
                          s.fix ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank) : full_lead + 8 * st.s, r0,
                          s.seg0 + whole * kTileK, chunks, s.q_box);
             st.next();
@@ -362,16 +387,17 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, ui
 // the end of its last step of 16, in both operands.
 __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, const Wait& w,
                           bool leader, uint32_t peer, uint32_t lead) {
+    using C = Cfg<Form::kWeight>;
     const int lane = threadIdx.x & 31;
     Ring ring;
-    Stage st;
+    Stage<C::kStages> st;
     uint32_t tail_phase = 0;
     GradTile t;
     for (;;) {
         if (!take<true>(ctl, ring, t, w, 58, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<true>(p, off, t);
+        const Shape s = shape_of<Form::kWeight>(p, off, t);
         if (s.fix) {
-            Stage at = st;
+            Stage<C::kStages> at = st;
             at.skip(s.nkb - 1);
             const bool landed = bar_wait(smem_addr(&ctl->tail[at.s]), tail_phase >> at.s & 1u, w, 59);
             if (!__all_sync(kFull, landed)) return;
@@ -397,14 +423,16 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
     }
 }
 
-template <bool WG>
+template <Form F>
 __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, uint32_t tmem,
                          const Wait& w, uint32_t peer) {
+    using C = Cfg<F>;
+    constexpr bool WG = C::kWeight;
     // fp32 accumulator, bf16 operands; MN-major operands for the weight gradient; M = 256
     constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (WG ? (1u << 15) | (1u << 16) : 0u) | (16u << 24);
     constexpr uint32_t kLbo = WG ? 8192 : 16, kStep = WG ? 2048 : 32;
     Ring ring;
-    Stage st;
+    Stage<C::kStages> st;
     uint32_t fixed_phase = 0;
     const uint64_t pd0 = smem_desc_sw128(smem_addr(sP), kLbo, 1024), qd0 = smem_desc_sw128(smem_addr(sQ), kLbo, 1024);
     const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
@@ -414,7 +442,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     bool ok = true;
     while (ok) {
         if (!take<false>(ctl, ring, t, w, 61, true, peer) || t.e < 0) break;
-        const Shape s = shape_of<WG>(p, off, t);
+        const Shape s = shape_of<F>(p, off, t);
         const uint32_t idesc = kDesc | ((uint32_t)(2 * s.half) >> 3) << 17;
         for (int kb0 = 0; ok && kb0 < s.nkb; kb0 += p.chunk_kb) {
             if (!(ok = bar_wait(smem_addr(&ctl->tempty[acc]), aphase ^ 1u, w, 62))) break;
@@ -428,7 +456,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
             for (int i = 0; i < whole; ++i) {
                 if (!(ok = bar_wait(full0 + st.s * 8, st.phase, w, 63))) break;
                 tc_fence_after();
-                const uint64_t pd = pd0 + (uint32_t)(st.s * (kOpBytes >> 4)), qd = qd0 + (uint32_t)(st.s * (kOpBytes >> 4));
+                const uint64_t pd = pd0 + (uint32_t)(st.s * (kOpBytes >> 4)), qd = qd0 + (uint32_t)(st.s * (C::kQBytes >> 4));
                 umma_bf16_pair(d, pd, qd, idesc, i != 0);
 #pragma unroll
                 for (int kk = 1; kk < kTileK / kUmmaK; ++kk)
@@ -447,7 +475,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t pd = smem_desc_sw128(smem_addr(sP) + st.s * kOpBytes, WG ? s.p_box * 128 : kLbo, 1024);
-                const uint64_t qd = smem_desc_sw128(smem_addr(sQ) + st.s * kOpBytes, WG ? s.q_box * 128 : kLbo, 1024);
+                const uint64_t qd = smem_desc_sw128(smem_addr(sQ) + st.s * C::kQBytes, WG ? s.q_box * 128 : kLbo, 1024);
                 for (int kk = 0; kk < s.ksteps; ++kk)
                     umma_bf16_pair(d, pd + kk * (kStep >> 4), qd + kk * (kStep >> 4), idesc, (whole | kk) != 0);
                 umma_commit_pair_mc(empty0 + st.s * 8, 0x3);
@@ -461,32 +489,35 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     bar_wait(smem_addr(&ctl->mma_done), 0u, w, 65, false);
 }
 
-// visit(address, i, i < n) for i = 0, STEP, ... 126, addresses `pitch` bytes apart for each step.  The
+// visit(address, i, i < n) for i = 0, STEP, ... below ROWS, addresses `pitch` bytes apart for each step.  The
 // address is stepped, not multiplied out: 128 products in flight spilled, and the whole epilogue
-// ran at 2.6 TB/s.  A warp whose lanes all have their 128 rows skips the bounds.
-template <int STEP, class Visit>
+// ran at 2.6 TB/s.  A warp whose lanes all have their rows skips the bounds.
+template <int ROWS, int STEP, class Visit>
 __device__ __forceinline__ void walk_rows(uint8_t* at, size_t pitch, int n, Visit visit) {
-    if (__all_sync(kFull, n > 128 - STEP)) {
+    if (__all_sync(kFull, n > ROWS - STEP)) {
 #pragma unroll
-        for (int i = 0; i < 128; i += STEP) {
+        for (int i = 0; i < ROWS; i += STEP) {
             visit(at, i, true);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 128; i += STEP) {
+        for (int i = 0; i < ROWS; i += STEP) {
             visit(at, i, i < n);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     }
 }
 
-// Warps 4-11: lane quarter q = warp & 3 (c), columns [128 h, 128 h + 128) (r).  All sums of a
-// thread, one c by 128 r, are in registers before the first store, so the accumulator is handed
+// Warps 4-11: lane quarter q = warp & 3 (c) and half h of the rows.  All sums of a thread, one c by
+// up to 128 r, are in registers before the first store, so the accumulator is handed
 // back while the stores are still leaving.
-template <bool WG>
+template <Form F>
 __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off, uint32_t tmem, const Wait& w,
                               bool leader, uint32_t peer, uint32_t lead, uint32_t rank) {
+    using C = Cfg<F>;
+    constexpr bool WG = C::kWeight;
+    constexpr int kRows = C::kWarpRows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int q = warp & 3, h = (warp - kEpiFirst) >> 2;
     Ring ring;
@@ -495,30 +526,30 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
     GradTile t;
     for (;;) {
         if (!take<true>(ctl, ring, t, w, 66, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<WG>(p, off, t);
-        const int cols = min(128, s.rows - 128 * h);  // this warp's valid columns, may be <= 0
+        const Shape s = shape_of<F>(p, off, t);
+        const int cols = min(kRows, s.rows - kRows * h);  // this warp's valid rows, may be <= 0
         const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
-        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + 256 * t.r + 128 * h;
+        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + (size_t)(C::kRowTile * t.r + kRows * h);
         const size_t ld = (size_t)p.c_size;
         const int mine = c < p.c_size ? cols : 0;  // this lane's valid rows
         const bool add = WG && p.a.accumulate;
         if (add && s.nkb == 0) continue;  // nothing to add
-        float sum[128];
+        float sum[kRows];
         if (add) {  // what is there already, read while the MMAs run
-            walk_rows<1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
+            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
                          [&](uint8_t* at, int i, bool in) { sum[i] = in ? __ldcs(reinterpret_cast<float*>(at)) : 0.f; });
         } else if (s.nkb == 0) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+            for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
         }
         for (int kb = 0; kb < s.nkb; kb += p.chunk_kb) {
             const bool ready = bar_wait(smem_addr(&ctl->tfull[acc]), aphase, w, 67);
             if (!__all_sync(kFull, ready)) return;
             tc_fence_after();
             const bool first = kb == 0 && !add;
-            const uint32_t base = tmem + (uint32_t)(acc * 256 + 128 * h) + ((uint32_t)(32 * q) << 16);
+            const uint32_t base = tmem + (uint32_t)(acc * 256 + kRows * h) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < kRows / 32; ++g) {
                 if (32 * g < cols) {
                     uint32_t v[32];
                     tmem_ld_32x32(base + 32 * g, v);
@@ -540,27 +571,30 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
         if (p.a.out_bf16) {
             // two rows at a time: even lanes store columns c, c + 1 of the first, odd lanes of the second
             const int odd = lane & 1;
-            walk_rows<2>(static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2, ld * 4, mine - odd,
+            walk_rows<kRows, 2>(static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2, ld * 4, mine - odd,
                          [&](uint8_t* at, int i, bool in) {
                 const float other = __shfl_xor_sync(kFull, odd ? sum[i] : sum[i + 1], 1);
                 const uint32_t v = odd ? bf16x2(other, sum[i + 1]) : bf16x2(sum[i], other);
                 if (in) __stcs(reinterpret_cast<uint32_t*>(at), v);
             });
         } else {
-            walk_rows<1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
+            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
                          [&](uint8_t* at, int i, bool in) { if (in) __stcs(reinterpret_cast<float*>(at), sum[i]); });
         }
     }
 }
 
-template <bool WG>
+template <Form F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grouped_grad_kernel(const __grid_constant__ GradParams p) {
+    using C = Cfg<F>;
+    constexpr bool WG = C::kWeight;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t* sP = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* sQ = sP + kStages * kOpBytes;
-    GradCtl* ctl = reinterpret_cast<GradCtl*>(sQ + kStages * kOpBytes);
+    GradCtl* ctl = reinterpret_cast<GradCtl*>(sQ + kStages * C::kQBytes);
     int* off = reinterpret_cast<int*>(ctl + 1);        // [E+1]
     int* base = off + kMaxE + 1;                       // [E+1] row tiles before expert e (input gradient)
     short* order = reinterpret_cast<short*>(base);     // [E] experts, most rows first (weight gradient)
@@ -593,7 +627,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     if (warp == 2) {
         tmem_alloc_pair(smem_addr(&ctl->tmem_base), 512);
         tmem_relinquish_pair();
+    } else if (warp == 3 && lane == 0) {
+        tma_prefetch_map(&p.p_map);
+        tma_prefetch_map(&p.q_map);
     }
+    // what is above runs beside the end of the kernel before this one in the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // offsets have to ascend from 0 to S: they bound every access
     int bad = 0;
     for (int e = tid; e <= E; e += kGradThreads) {
@@ -619,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         int run = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < E ? (off[e + 1] - off[e] + 255) / 256 : 0;
+            const int n = e < E ? (off[e + 1] - off[e] + C::kRowTile - 1) / C::kRowTile : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -632,6 +671,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         if (lane == 0) base[E] = run;
     }
     if (bad && tid == 0) report_error(p.a.status, kStDevice, -2, off[E], 0);
+    __syncthreads();
+    if (tid == 0) {  // a pair's first tile is its own number: both CTAs know it without a claim
+        ctl->ring[0] = tile_at<F>(p, base, order, blockIdx.x / 2);
+        mbar_arrive(smem_addr(&ctl->sfull[0]));
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // barriers and TMEM address of both CTAs are there
@@ -645,14 +689,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (!bad) {
             if (warp == 0) {
-                if (lane == 0) producer_p<WG>(p, ctl, off, sP, w, leader, sched, lead, rank);
+                if (lane == 0) producer_p<F>(p, ctl, off, sP, w, leader, sched, lead, rank);
             } else if (warp == 1) {
                 if (lane == 0) {
-                    if (leader) mma_role<WG>(p, ctl, off, sP, sQ, tmem, w, sched);
-                    else scheduler<WG>(p, ctl, base, order, w, lead);
+                    if (leader) mma_role<F>(p, ctl, off, sP, sQ, tmem, w, sched);
+                    else scheduler<F>(p, ctl, base, order, w, lead);
                 }
             } else if (warp == 2) {
-                if (lane == 0) producer_q<WG>(p, ctl, off, sQ, w, leader, sched, lead, rank);
+                if (lane == 0) producer_q<F>(p, ctl, off, sQ, w, leader, sched, lead, rank);
             } else if (WG) {
                 zero_rows(p, ctl, off, sP, sQ, w, leader, sched, lead);
             }
@@ -660,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if (!bad) epilogue_role<WG>(p, ctl, off, tmem, w, leader, sched, lead, rank);
+        if (!bad) epilogue_role<F>(p, ctl, off, tmem, w, leader, sched, lead, rank);
     }
 
     tc_fence_before();
@@ -682,18 +726,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     }
 }
 
-constexpr size_t kGradSmem = 1024 + (size_t)2 * kStages * kOpBytes + sizeof(GradCtl) + 2 * sizeof(int) * (kMaxE + 1);
-static_assert(kGradSmem <= 232448, "more than 227 KB of shared memory per CTA");
+template <Form F>
+constexpr size_t smem_bytes() {
+    return 1024 + (size_t)Cfg<F>::kStages * (kOpBytes + Cfg<F>::kQBytes) + sizeof(GradCtl) + 2 * sizeof(int) * (kMaxE + 1);
+}
+static_assert(smem_bytes<Form::kInput>() <= 232448 && smem_bytes<Form::kNarrow>() <= 232448, "more than 227 KB of shared memory per CTA");
+static_assert(Cfg<Form::kInput>::kStages <= kMaxStages && Cfg<Form::kNarrow>::kStages <= kMaxStages, "stages");
 static_assert(sizeof(GradTile) == 16, "a tile travels as two 8-byte stores");
 
 // Pairs of CTAs that are resident together on the current device; the kernel's attributes are set once per device.
-template <bool WG>
+template <Form F>
 cudaError_t resident_pairs(int device, int* pairs) {
     static std::atomic<int> known[64];
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     *pairs = known[device].load(std::memory_order_acquire);
     if (*pairs > 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(grouped_grad_kernel<WG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
+    cudaError_t e = cudaFuncSetAttribute(grouped_grad_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<F>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
@@ -702,39 +750,53 @@ cudaError_t resident_pairs(int device, int* pairs) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kGradThreads);
-    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.dynamicSmemBytes = smem_bytes<F>();
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(pairs, grouped_grad_kernel<WG>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(pairs, grouped_grad_kernel<F>, &cfg);
     if (e != cudaSuccess) return e;
     if (*pairs < 1) return cudaErrorLaunchOutOfResources;
     known[device].store(*pairs, std::memory_order_release);
     return cudaSuccess;
 }
 
-template <bool WG>
+template <Form F>
 cudaError_t launch(GradParams& p, const GroupedGradArgs& a, int device, long long max_tiles, cudaStream_t stream) {
     p.a = a;
     p.chunk_kb = a.out_bf16 ? 1 << 30 : kChunkKb;
     int pairs = 0;
-    const cudaError_t e = resident_pairs<WG>(device, &pairs);
+    const cudaError_t e = resident_pairs<F>(device, &pairs);
     if (e != cudaSuccess) return e;
-    pairs = (int)std::min<long long>(pairs, max_tiles);
-    grouped_grad_kernel<WG><<<2 * pairs, kGradThreads, kGradSmem, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;  // the kernel waits by itself for the one before it, after its own set-up
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(pairs, max_tiles));
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.dynamicSmemBytes = smem_bytes<F>();
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, grouped_grad_kernel<F>, (const GradParams&)p);
+}
+
+template <Form F>
+cudaError_t dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
+    GradParams p = {};
+    p.c_size = a.d;
+    p.c_tiles = (a.d + 255) / 256;
+    const uint64_t S = (uint64_t)a.S, N = (uint64_t)a.N, wrows = (uint64_t)a.E * a.d;
+    if (!map_bf16_2d(&p.p_map, a.W, wrows, N, kTileK, kTileM) ||
+        !map_bf16_2d(&p.q_map, a.dY, S, N, kTileK, Cfg<F>::kRowTile / 2) || !map_bf16_2d(&p.q_tail, a.dY, S, N, kTileK, 16))
+        return cudaErrorInvalidValue;
+    return launch<F>(p, a, device, ((long long)a.S / Cfg<F>::kRowTile + a.E) * p.c_tiles, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
-    GradParams p = {};
-    p.c_size = a.d;
-    p.c_tiles = (a.d + 255) / 256;
-    const uint64_t S = (uint64_t)a.S, N = (uint64_t)a.N, wrows = (uint64_t)a.E * a.d;
-    if (!map_bf16_2d(&p.p_map, a.W, wrows, N, kTileK, kTileM) || !map_bf16_2d(&p.q_map, a.dY, S, N, kTileK, kTileM) ||
-        !map_bf16_2d(&p.q_tail, a.dY, S, N, kTileK, 16))
-        return cudaErrorInvalidValue;
-    return launch<false>(p, a, device, ((long long)a.S / 256 + a.E) * p.c_tiles, stream);
+    const bool narrow = a.S <= 64LL * a.E;
+    return narrow ? dgrad<Form::kNarrow>(a, device, stream) : dgrad<Form::kInput>(a, device, stream);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
@@ -752,7 +814,7 @@ cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStrea
     }
     const long long tiles = (long long)a.E * p.c_tiles * p.r_tiles;
     if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
-    return launch<true>(p, a, device, tiles, stream);
+    return launch<Form::kWeight>(p, a, device, tiles, stream);
 }
 
 }  // namespace moe
