@@ -9,10 +9,11 @@
 //
 // A row is held by TPR threads (a power of two from 8 to 1024), VPT vectors of 8 columns each, so
 // that the sums are one shuffle tree and, above a warp, one exchange through shared memory.  The
-// backward kernel also keeps dgamma and dbeta of its columns, over all the rows of its CTA, in
-// registers (shared memory for d > 8192); the CTAs' partial sums are added by a second kernel in
-// a fixed order.
+// backward kernel also keeps dgamma and dbeta of its columns, over all the rows of
+// its CTA, in registers (shared memory for d > 8192); the CTAs' partial sums are added by a second
+// kernel in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "train.cuh"
@@ -63,8 +64,8 @@ __host__ __device__ constexpr int cta_threads(int tpr, int least) { return tpr >
 
 // Sums of N values over the TPR threads of a row, the same bits in each of them.  `red` is used
 // by one call at a time: two calls in a row need a CTA barrier or another array between them.
-template <int TPR, int N, int CTA>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32]) {
+template <int TPR, int N, int CTA, class Barrier>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32], Barrier barrier) {
 #pragma unroll
     for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -75,7 +76,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32]) {
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) red[i][warp] = v[i];
-        __syncthreads();
+        barrier();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float s = 0.f;
@@ -86,41 +87,64 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32]) {
     }
 }
 
+struct CtaBarrier {
+    __device__ void operator()() const { __syncthreads(); }
+};
+
 // ------------------------------------------------------------------ forward
 
-template <bool XB, int TPR, int VPT>
-__global__ void __launch_bounds__(cta_threads(TPR, 128)) layernorm_kernel(const LayernormArgs a) {
-    constexpr int kCta = cta_threads(TPR, 128), kRows = kCta / TPR;
-    __shared__ float red_m[1][kCta / 32], red_v[1][kCta / 32];
+// Resident CTAs that the registers are cut for: 640 (bf16) or 512 threads an SM with two rows each,
+// 1024 with one.
+__host__ __device__ constexpr int forward_ctas(int cta, bool xb, int rows) {
+    const int threads = rows == 1 ? 1024 : xb ? 640 : 512;
+    return threads > cta ? threads / cta : 1;
+}
+
+// R rows at a time: the weights, 8 bytes a column from L1 where a row has 2 or 4, are read once for R
+// rows, and R rows share each barrier (8192 x 4096: bf16 30 us with one row, 27 with two; fp32 36 and 33).
+template <bool XB, int TPR, int VPT, int R>
+__global__ void __launch_bounds__(cta_threads(TPR, 128), forward_ctas(cta_threads(TPR, 128), XB, R)) layernorm_kernel(const LayernormArgs a) {
+    constexpr int kCta = cta_threads(TPR, 128), kRows = kCta / TPR * R;
+    __shared__ float red_m[R][kCta / 32], red_v[R][kCta / 32];
     const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const float inv_d = 1.f / (float)a.d;
     for (long long t0 = (long long)blockIdx.x * kRows; t0 < a.T; t0 += (long long)gridDim.x * kRows) {
-        const long long t = t0 + group;
-        const size_t row = (size_t)t * a.d;
-        Raw<XB> x[VPT];
-        float s[1] = {0.f}, q[1] = {0.f};
+        const long long t = t0 + group * R;
+        Raw<XB> x[R][VPT];
+        float mean[R], rstd[R];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (sub + i * TPR) * 8;
-            if (c < a.d && t < a.T) x[i].load(a.x, row + c);
-            else x[i].zero();
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (sub + i * TPR) * 8;
+                if (c < a.d && t + r < a.T) x[r][i].load(a.x, (size_t)(t + r) * a.d + c);
+                else x[r][i].zero();
+            }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mean[r] += x[r][i].get(j);
         }
+        row_sum<TPR, R, kCta>(mean, red_m, CtaBarrier());
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= inv_d;
+            rstd[r] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += x[i].get(j);
-        row_sum<TPR, 1, kCta>(s, red_m);
-        const float mean = s[0] * inv_d;
+            for (int i = 0; i < VPT; ++i) {
+                if ((sub + i * TPR) * 8 < a.d) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if ((sub + i * TPR) * 8 < a.d) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[0] = fmaf(x[i].get(j) - mean, x[i].get(j) - mean, q[0]);
+                    for (int j = 0; j < 8; ++j)
+                        rstd[r] = fmaf(x[r][i].get(j) - mean[r], x[r][i].get(j) - mean[r], rstd[r]);
+                }
             }
         }
-        row_sum<TPR, 1, kCta>(q, red_v);
-        const float rstd = 1.f / sqrtf(q[0] * inv_d + a.eps);
-        if (t >= a.T) continue;
+        row_sum<TPR, R, kCta>(rstd, red_v, CtaBarrier());
+#pragma unroll
+        for (int r = 0; r < R; ++r) rstd[r] = 1.f / sqrtf(rstd[r] * inv_d + a.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (sub + i * TPR) * 8;
@@ -129,13 +153,20 @@ __global__ void __launch_bounds__(cta_threads(TPR, 128)) layernorm_kernel(const 
             weights8(a.gamma, c, 1.f, g);
             weights8(a.beta, c, 0.f, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = fmaf((x[i].get(j) - mean) * rstd, g[j], b[j]);
-            store8<true>(a.y, row + c, y);
+            for (int r = 0; r < R; ++r) {
+                if (t + r >= a.T) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = fmaf((x[r][i].get(j) - mean[r]) * rstd[r], g[j], b[j]);
+                store8<true>(a.y, (size_t)(t + r) * a.d + c, y);
+            }
         }
-        if (sub == 0) {
-            if (a.mean) a.mean[t] = mean;
-            if (a.rstd) a.rstd[t] = rstd;
-        }
+        if (sub == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (t + r >= a.T) continue;
+                if (a.mean) a.mean[t + r] = mean[r];
+                if (a.rstd) a.rstd[t + r] = rstd[r];
+            }
     }
 }
 
@@ -154,7 +185,7 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_kernel(const LayernormAr
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] += v[j];
         }
-        row_sum<kWide, 1, kWide>(s, red_m);
+        row_sum<kWide, 1, kWide>(s, red_m, CtaBarrier());
         const float mean = s[0] * inv_d;
         for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8];
@@ -162,7 +193,7 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_kernel(const LayernormAr
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[0] = fmaf(v[j] - mean, v[j] - mean, q[0]);
         }
-        row_sum<kWide, 1, kWide>(q, red_v);
+        row_sum<kWide, 1, kWide>(q, red_v, CtaBarrier());
         const float rstd = 1.f / sqrtf(q[0] * inv_d + a.eps);
         for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8], g[8], b[8];
@@ -182,155 +213,199 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_kernel(const LayernormAr
 
 // ------------------------------------------------------------------ backward
 
-// A CTA has at least 256 threads, in whole rows.  Up to 512 threads of two vectors (d <= 8192) a
-// thread's dgamma and dbeta are in registers; above, 1024 threads leave 64 registers each and
-// they are in shared memory, [2][d].
-template <int TPR, bool XB>
+// A thread has one vector of 8 columns, so its sums and the row's xh and v are 40 registers and 1024
+// threads an SM fit: it is their number that hides the round trips of a row (measured on 8192 x
+// 4096, bf16 x and fp32 dy: rows of two vectors a thread in 80 registers 65 us; the next rows on
+// their way in shared memory by cp.async, 512 threads, 71 us).
+__host__ __device__ constexpr int back_cta(int tpr) { return tpr >= 256 ? tpr : tpr == 64 ? 512 : 1024; }
+
+template <int TPR>
 struct Back {
-    static constexpr int kCta = cta_threads(TPR, 256);
+    // rows of fewer than 256 threads: one CTA an SM, whose rows' sums are joined in shared memory
+    // before they are written (two CTAs for 64 threads: there are 16 named barriers, one the CTA's);
+    // 32768 x 512: 34 us with CTAs of 256 threads, 31 with 1024; 16384 x 2048: 62 and 65
+    static constexpr int kCta = back_cta(TPR);
     static constexpr int kRows = kCta / TPR;
-    static constexpr bool kShared = TPR > 512;
-    // 80 registers hold a row of bf16 x and fp32 dy with its residual and sums; fp32 x takes more
-    static constexpr int kCtasPerSm = kCta > 256 ? 1 : XB ? 3 : 2;
+    static constexpr int kCtasPerSm = 1024 / kCta;
+    static constexpr int kCols = TPR * 8;
+    static constexpr size_t kSmem = kRows > 1 ? (size_t)kRows * 2 * kCols * 4 : 0;  // at most 64 KB
 };
 
-template <bool DYB, bool XB, int TPR, int VPT>
-__global__ void __launch_bounds__(Back<TPR, XB>::kCta, Back<TPR, XB>::kCtasPerSm)
-    layernorm_backward_kernel(const LayernormBackwardArgs a) {
-    using B = Back<TPR, XB>;
-    constexpr int kAcc = B::kShared ? 1 : VPT;
-    __shared__ float red[2][2][B::kCta / 32];
-    extern __shared__ float4 dyn4[];
-    float* dyn = reinterpret_cast<float*>(dyn4);
-    const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const float inv_d = 1.f / (float)a.d;
-    float dg[kAcc][8], db[kAcc][8];
-#pragma unroll
-    for (int i = 0; i < kAcc; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
-    // kShared: four columns of vector i are float4 (4 i + 2 half + j / 4) TPR + sub: no two lanes share
-    // a bank; every thread zeroes and uses its own columns alone
-    if constexpr (B::kShared)
-#pragma unroll
-        for (int i = 0; i < 4 * VPT; ++i) dyn4[i * TPR + sub] = make_float4(0.f, 0.f, 0.f, 0.f);
+// Barrier of the TPR threads of row group `group`.
+template <int TPR, int CTA>
+__device__ __forceinline__ void group_barrier(int group) {
+    if constexpr (TPR == CTA) __syncthreads();
+    else if constexpr (TPR > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
 
+template <bool DYB, bool XB, int TPR>
+__global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layernorm_backward_kernel(const LayernormBackwardArgs a) {
+    using B = Back<TPR>;
+    __shared__ float red[2][2][B::kCta / 32];
+    extern __shared__ float joined[];  // [group][2][kCols]
+    const int tid = threadIdx.x, sub = tid % TPR, group = tid / TPR, c = sub * 8;
+    const float inv_d = 1.f / (float)a.d;
+    const bool mine = c < a.d;  // this thread's columns exist
+    float dg[8], db[8], gamma[8];
+    weights8(mine ? a.gamma : nullptr, c, 1.f, gamma);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.f;
     const long long step = (long long)gridDim.x * B::kRows;
     long long t = (long long)blockIdx.x * B::kRows + group;
-    Raw<XB> x[VPT], res[VPT];
-    Raw<DYB> dy[VPT];
     int turn = 0;
     for (long long t0 = (long long)blockIdx.x * B::kRows; t0 < a.T; t0 += step, t += step, turn ^= 1) {
-        const bool live = t < a.T;
+        const bool live = t < a.T && mine;
+        const size_t at = live ? (size_t)t * a.d + c : 0;
+        Raw<XB> x, res;
+        Raw<DYB> dy;
+        float mean = 0.f, rstd = 0.f;
+        if (live) {
+            x.load(a.x, at);
+            dy.load(a.dy, at);
+            mean = __ldg(a.mean + t);
+            rstd = __ldg(a.rstd + t);
+        } else {
+            x.zero();
+            dy.zero();
+        }
+        if (live && a.dres) res.load(a.dres, at);
+        else res.zero();
+        // xh and v = dy gamma stay in registers between the two halves
+        float xh[8], v[8], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = dy.get(j);
+            xh[j] = (x.get(j) - mean) * rstd;
+            v[j] = w * gamma[j];
+            s[0] += v[j];
+            s[1] = fmaf(v[j], xh[j], s[1]);
+            dg[j] = fmaf(w, xh[j], dg[j]);
+            db[j] += w;
+        }
+        // the two arrays of `red` alternate, so one barrier a row is enough
+        row_sum<TPR, 2, B::kCta>(s, red[turn], [&] { group_barrier<TPR, B::kCta>(group); });
+        if (!live) continue;
+        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[j], m2, v[j] - m1), res.get(j));
+        store8<XB>(a.dx, at, v);
+    }
+    if (!a.dgamma && !a.dbeta) return;
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
+    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
+    if constexpr (B::kRows > 1) {  // the CTA's rows first
+        float* own = joined + group * 2 * B::kCols + c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            own[j] = dg[j];
+            own[B::kCols + j] = db[j];
+        }
+        __syncthreads();
+        for (int i = tid; i < 2 * B::kCols; i += B::kCta) {
+            const int col = i % B::kCols, half = i / B::kCols;
+            if (col >= a.d) continue;
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < B::kRows; ++g) v += joined[g * 2 * B::kCols + i];
+            out[half * a.d + col] = v;
+        }
+    } else if (mine) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            *reinterpret_cast<float4*>(out + c + j) = make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
+            *reinterpret_cast<float4*>(out + a.d + c + j) = make_float4(db[j], db[j + 1], db[j + 2], db[j + 3]);
+        }
+    }
+}
+
+// 8192 < d <= 16384: 1024 threads leave 64 registers each, so dgamma and dbeta are summed in shared
+// memory (128 KB, which leaves no room for rows on their way) and the rows pass through registers.
+constexpr int kTall = 1024;
+constexpr size_t kTallSmem = (size_t)kTall * 2 * 8 * 2 * 4;
+
+template <bool DYB, bool XB>
+__global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const LayernormBackwardArgs a) {
+    constexpr int VPT = 2;
+    __shared__ float red[2][2][kTall / 32];
+    extern __shared__ float4 sums4[];
+    const int tid = threadIdx.x;
+    const float inv_d = 1.f / (float)a.d;
+    // four columns of vector i are float4 (4 i + 2 half + j / 4) kTall + tid: no two lanes share a bank,
+    // and every thread uses its own alone
+#pragma unroll
+    for (int i = 0; i < 4 * VPT; ++i) sums4[i * kTall + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int turn = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const size_t row = (size_t)t * a.d;
-        const float mean = live ? __ldg(a.mean + t) : 0.f, rstd = live ? __ldg(a.rstd + t) : 0.f;
+        const float mean = __ldg(a.mean + t), rstd = __ldg(a.rstd + t);
+        Raw<XB> x[VPT];
+        Raw<DYB> dy[VPT];
+        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (sub + i * TPR) * 8;
-            if (c < a.d && live) {
+            const int c = (tid + i * kTall) * 8;
+            if (c < a.d) {
                 x[i].load(a.x, row + c);
                 dy[i].load(a.dy, row + c);
-                if (a.dres) res[i].load(a.dres, row + c);
-                else res[i].zero();
             } else {
                 x[i].zero();
                 dy[i].zero();
             }
         }
-        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (sub + i * TPR) * 8;
+            const int c = (tid + i * kTall) * 8;
             if (c >= a.d) continue;
             float g[8];
             weights8(a.gamma, c, 1.f, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float w = dy[i].get(j), xh = (x[i].get(j) - mean) * rstd, v = w * g[j];
+                const float v = dy[i].get(j) * g[j];
                 s[0] += v;
-                s[1] = fmaf(v, xh, s[1]);
-                if constexpr (!B::kShared) {
-                    dg[i][j] = fmaf(w, xh, dg[i][j]);
-                    db[i][j] += w;
-                }
+                s[1] = fmaf(v, (x[i].get(j) - mean) * rstd, s[1]);
             }
-            if constexpr (B::kShared) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    float4& g4 = dyn4[(4 * i + j / 4) * TPR + sub];
-                    float4& b4 = dyn4[(4 * i + 2 + j / 4) * TPR + sub];
-                    float4 u = g4, v = b4;
-                    u.x = fmaf(dy[i].get(j), (x[i].get(j) - mean) * rstd, u.x);
-                    u.y = fmaf(dy[i].get(j + 1), (x[i].get(j + 1) - mean) * rstd, u.y);
-                    u.z = fmaf(dy[i].get(j + 2), (x[i].get(j + 2) - mean) * rstd, u.z);
-                    u.w = fmaf(dy[i].get(j + 3), (x[i].get(j + 3) - mean) * rstd, u.w);
-                    v.x += dy[i].get(j);
-                    v.y += dy[i].get(j + 1);
-                    v.z += dy[i].get(j + 2);
-                    v.w += dy[i].get(j + 3);
-                    g4 = u;
-                    b4 = v;
-                }
+            for (int j = 0; j < 8; j += 4) {
+                float4& g4 = sums4[(4 * i + j / 4) * kTall + tid];
+                float4& b4 = sums4[(4 * i + 2 + j / 4) * kTall + tid];
+                float4 u = g4, v = b4;
+                u.x = fmaf(dy[i].get(j), (x[i].get(j) - mean) * rstd, u.x);
+                u.y = fmaf(dy[i].get(j + 1), (x[i].get(j + 1) - mean) * rstd, u.y);
+                u.z = fmaf(dy[i].get(j + 2), (x[i].get(j + 2) - mean) * rstd, u.z);
+                u.w = fmaf(dy[i].get(j + 3), (x[i].get(j + 3) - mean) * rstd, u.w);
+                v.x += dy[i].get(j);
+                v.y += dy[i].get(j + 1);
+                v.z += dy[i].get(j + 2);
+                v.w += dy[i].get(j + 3);
+                g4 = u;
+                b4 = v;
             }
         }
-        // the two arrays of `red` alternate, so one barrier a row is enough
-        row_sum<TPR, 2, B::kCta>(s, red[turn]);
+        row_sum<kTall, 2, kTall>(s, red[turn], CtaBarrier());
         const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
-        if (!live) continue;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (sub + i * TPR) * 8;
+            const int c = (tid + i * kTall) * 8;
             if (c >= a.d) continue;
-            float g[8], o[8];
+            float g[8], r[8] = {}, o[8];
             weights8(a.gamma, c, 1.f, g);
+            if (a.dres) load8<XB>(a.dres, row + c, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = (x[i].get(j) - mean) * rstd;
-                o[j] = fmaf(rstd, dy[i].get(j) * g[j] - m1 - xh * m2, res[i].get(j));
-            }
+            for (int j = 0; j < 8; ++j)
+                o[j] = fmaf(rstd, dy[i].get(j) * g[j] - m1 - (x[i].get(j) - mean) * rstd * m2, r[j]);
             store8<XB>(a.dx, row + c, o);
         }
     }
     if (!a.dgamma && !a.dbeta) return;
-    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
+    asm volatile("griddepcontrol.launch_dependents;");
     float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
-    if constexpr (B::kRows > 1) {  // the CTA's rows first: [group][2][TPR * VPT * 8]
-        constexpr int kCols = TPR * VPT * 8;
-        float* mine = dyn + (size_t)group * 2 * kCols;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * kTall) * 8;
+        if (c >= a.d) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mine[(sub + i * TPR) * 8 + j] = dg[i][j];
-                mine[kCols + (sub + i * TPR) * 8 + j] = db[i][j];
-            }
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * kCols; c += B::kCta) {
-            const int col = c % kCols, half = c / kCols;
-            if (col >= a.d) continue;
-            float v = 0.f;
-            for (int g = 0; g < B::kRows; ++g) v += dyn[(size_t)g * 2 * kCols + c];
-            out[half * a.d + col] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (sub + i * TPR) * 8;
-            if (c >= a.d) continue;
-#pragma unroll
-            for (int j = 0; j < 8; j += 4)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float4 v;
-                    if constexpr (B::kShared) {
-                        v = dyn4[(4 * i + 2 * h + j / 4) * TPR + sub];
-                    } else {
-                        v = h ? make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3])
-                              : make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
-                    }
-                    *reinterpret_cast<float4*>(out + h * a.d + c + j) = v;
-                }
-        }
+        for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<float4*>(out + (v >> 1) * a.d + c + (v & 1) * 4) = sums4[(4 * i + v) * kTall + tid];
     }
 }
 
@@ -380,7 +455,7 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_dx_kernel(const Layernor
                 s[1] = fmaf(v[j] * g[j], (x[j] - mean) * rstd, s[1]);
             }
         }
-        row_sum<kWide, 2, kWide>(s, red[turn]);
+        row_sum<kWide, 2, kWide>(s, red[turn], CtaBarrier());
         const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
         for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8], x[8], g[8], r[8] = {};
@@ -436,37 +511,51 @@ int pow2_at_least(int v) {
 // threads of a row: vectors of 8 columns, `vpt` a thread
 int row_threads(int d, int vpt) { return pow2_at_least((d / 8 + vpt - 1) / vpt); }
 
-constexpr int kForwardVpt = 4, kBackwardVpt = 2;
-constexpr int kForwardMax = 1024 * 8 * kForwardVpt, kBackwardMax = 1024 * 8 * kBackwardVpt;
+constexpr int kForwardMax = 1024 * 8 * 4;
+constexpr int kBackwardMax = 1024 * 8, kTallMax = 1024 * 8 * 2;
 
-template <bool XB>
-cudaError_t forward(const LayernormArgs& a, int sm_count, cudaStream_t s) {
+template <bool XB, int R>
+void forward_rows(const LayernormArgs& a, int sm_count, cudaStream_t s) {
     auto go = [&](auto tpr) {
-        constexpr int kTpr = decltype(tpr)::value, kCta = cta_threads(kTpr, 128), kRows = kCta / kTpr;
+        constexpr int kTpr = decltype(tpr)::value, kCta = cta_threads(kTpr, 128), kRows = kCta / kTpr * R;
         const int grid = std::min((a.T + kRows - 1) / kRows, sm_count * (2048 / kCta));
-        layernorm_kernel<XB, kTpr, kForwardVpt><<<grid, kCta, 0, s>>>(a);
+        layernorm_kernel<XB, kTpr, 4, R><<<grid, kCta, 0, s>>>(a);
     };
-    if (a.d > kForwardMax) {
-        layernorm_wide_kernel<XB><<<std::min(a.T, sm_count), kWide, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    switch (row_threads(a.d, kForwardVpt)) {
+    switch (row_threads(a.d, 4)) {
         case 8: go(std::integral_constant<int, 8>()); break;
         case 16: go(std::integral_constant<int, 16>()); break;
         case 32: go(std::integral_constant<int, 32>()); break;
         case 64: go(std::integral_constant<int, 64>()); break;
         case 128: go(std::integral_constant<int, 128>()); break;
         case 256: go(std::integral_constant<int, 256>()); break;
-        case 512: go(std::integral_constant<int, 512>()); break;
-        default: go(std::integral_constant<int, 1024>()); break;
+        default:
+            if constexpr (R == 1) {
+                if (a.d <= kForwardMax / 2) go(std::integral_constant<int, 512>());
+                else go(std::integral_constant<int, 1024>());
+            }
+    }
+}
+
+template <bool XB>
+cudaError_t forward(const LayernormArgs& a, int sm_count, cudaStream_t s) {
+    const int tpr = row_threads(a.d, 4);
+    if (a.d > kForwardMax) {
+        layernorm_wide_kernel<XB><<<std::min(a.T, sm_count), kWide, 0, s>>>(a);
+    } else if (tpr <= 256 && a.T > sm_count * (1024 / tpr)) {
+        forward_rows<XB, 2>(a, sm_count, s);
+    } else {
+        // few rows: one at a time, on as many SMs as there are; and rows of 512 threads and more, of
+        // which two at a time leave too few on an SM (8192 x 12000 bf16: 98 us with one, 113 with two)
+        forward_rows<XB, 1>(a, sm_count, s);
     }
     return cudaGetLastError();
 }
 
-// CTAs of the backward kernel: resident all at once (three, two or one an SM by its registers)
-int backward_parts(int T, int d, bool x_bf16, int sm_count) {
-    const int tpr = row_threads(d, kBackwardVpt), cta = cta_threads(tpr, 256), rows = cta / tpr;
-    return std::min((T + rows - 1) / rows, sm_count * (cta > 256 ? 1 : x_bf16 ? 3 : 2));
+// CTAs of the backward kernel, all resident at once, and their partial sums
+int backward_parts(int T, int d, int sm_count) {
+    if (d > kBackwardMax) return std::min(T, sm_count);
+    const int tpr = row_threads(d, 1), cta = back_cta(tpr), rows = cta / tpr;
+    return std::min((T + rows - 1) / rows, sm_count * (1024 / cta));
 }
 
 cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
@@ -482,24 +571,38 @@ cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, layernorm_join_kernel, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
 }
 
+// Launches a kernel whose shared memory may be over the default limit of 48 KB, the static part included;
+// `ready`: the devices (by bit) where its limit is raised.
+template <class Kernel>
+cudaError_t launch_big(Kernel kernel, const LayernormBackwardArgs& a, int grid, int cta, size_t smem,
+                       std::atomic<unsigned long long>& ready, cudaStream_t s) {
+    const unsigned long long bit = a.device < 64 ? 1ull << a.device : 0;
+    if (smem > 32 * 1024 && !(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    kernel<<<grid, cta, smem, s>>>(a);
+    return cudaSuccess;
+}
+
 template <bool DYB, bool XB>
 cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t s) {
-    if (a.d > kBackwardMax) {
+    if (a.d > kTallMax) {
         layernorm_wide_dx_kernel<DYB, XB><<<std::min(a.T, sm_count), kWide, 0, s>>>(a);
         if (a.dgamma || a.dbeta) layernorm_wide_dweight_kernel<DYB, XB><<<(a.d + 31) / 32, 256, 0, s>>>(a);
         return cudaGetLastError();
     }
-    const int parts = backward_parts(a.T, a.d, XB, sm_count);
+    const int parts = backward_parts(a.T, a.d, sm_count);
     cudaError_t e = cudaSuccess;
     auto go = [&](auto tpr) {
-        constexpr int kTpr = decltype(tpr)::value;
-        using B = Back<kTpr, XB>;
-        auto kernel = layernorm_backward_kernel<DYB, XB, kTpr, kBackwardVpt>;
-        const size_t smem = B::kShared ? (size_t)kTpr * kBackwardVpt * 8 * 2 * 4 : B::kRows > 1 ? (size_t)B::kCta * kBackwardVpt * 8 * 2 * 4 : 0;
-        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) kernel<<<parts, B::kCta, smem, s>>>(a);
+        using B = Back<decltype(tpr)::value>;
+        static std::atomic<unsigned long long> ready{0};
+        e = launch_big(layernorm_backward_kernel<DYB, XB, decltype(tpr)::value>, a, parts, B::kCta, B::kSmem, ready, s);
     };
-    switch (row_threads(a.d, kBackwardVpt)) {
+    static std::atomic<unsigned long long> tall_ready{0};
+    if (a.d > kBackwardMax) e = launch_big(layernorm_tall_kernel<DYB, XB>, a, parts, kTall, kTallSmem, tall_ready, s);
+    else switch (row_threads(a.d, 1)) {
         case 8: go(std::integral_constant<int, 8>()); break;
         case 16: go(std::integral_constant<int, 16>()); break;
         case 32: go(std::integral_constant<int, 32>()); break;
@@ -521,8 +624,8 @@ cudaError_t launch_layernorm(const LayernormArgs& a, int sm_count, cudaStream_t 
 }
 
 size_t layernorm_backward_scratch_bytes(int T, int d, int sm_count) {
-    if (d > kBackwardMax || T == 0) return 256;
-    return (size_t)backward_parts(T, d, true, sm_count) * 2 * d * sizeof(float);
+    if (d > kTallMax || T == 0) return 256;
+    return (size_t)backward_parts(T, d, sm_count) * 2 * d * sizeof(float);
 }
 
 cudaError_t launch_layernorm_backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t stream) {

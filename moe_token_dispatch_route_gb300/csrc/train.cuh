@@ -48,6 +48,7 @@ struct LayernormBackwardArgs {
     float* dbeta;        // [d] or null
     float* partial;      // scratch: partial sums of dgamma and dbeta
     int T, d;
+    int device;
 };
 size_t layernorm_backward_scratch_bytes(int T, int d, int sm_count);
 cudaError_t launch_layernorm_backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t stream);

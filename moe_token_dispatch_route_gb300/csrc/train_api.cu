@@ -83,7 +83,7 @@ moe_status_t moe_layernorm_backward(moe_plan_t plan, const void* dy, int32_t dy_
     DeviceScope scope(v.device);
     if (!scope.ok) return MOE_ERR_CUDA;
     LayernormBackwardArgs a{dy, dy_dtype == MOE_OUT_BF16, x, x_dtype == MOE_OUT_BF16, gamma, mean, rstd, dres, dx,
-                            dgamma, dbeta, static_cast<float*>(scratch), v.T, v.d};
+                            dgamma, dbeta, static_cast<float*>(scratch), v.T, v.d, v.device};
     return launched(launch_layernorm_backward(a, v.sm_count, s));
 }
 
