@@ -28,6 +28,7 @@ template <bool BF16>
 struct Raw {
     uint4 a;
     __device__ void load(const void* base, size_t i) { a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i)); }
+    __device__ void take(const uint8_t* row, int c) { a = *reinterpret_cast<const uint4*>(row + c * 2); }  // from shared memory
     __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
     __device__ float get(int j) const {
         const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
@@ -41,6 +42,10 @@ struct Raw<false> {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
         a = __ldcs(p);
         b = __ldcs(p + 1);
+    }
+    __device__ void take(const uint8_t* row, int c) {
+        a = *reinterpret_cast<const float4*>(row + c * 4);
+        b = *reinterpret_cast<const float4*>(row + c * 4 + 16);
     }
     __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ float get(int j) const {
@@ -213,17 +218,16 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_kernel(const LayernormAr
 
 // ------------------------------------------------------------------ backward
 
-// A thread has one vector of 8 columns, so its sums and the row's xh and v are 40 registers and 1024
-// threads an SM fit: it is their number that hides the round trips of a row (measured on 8192 x
-// 4096, bf16 x and fp32 dy: rows of two vectors a thread in 80 registers 65 us; the next rows on
-// their way in shared memory by cp.async, 512 threads, 71 us).
-__host__ __device__ constexpr int back_cta(int tpr) { return tpr >= 256 ? tpr : tpr == 64 ? 512 : 1024; }
+// Rows of at most 128 threads (d <= 1024).  A thread has one vector of 8 columns, so its sums and the
+// row's xh and v are 40 registers and 1024 threads an SM fit: it is their number that hides the
+// round trips of a row.
+__host__ __device__ constexpr int back_cta(int tpr) { return tpr == 64 ? 512 : 1024; }
 
 template <int TPR>
 struct Back {
-    // rows of fewer than 256 threads: one CTA an SM, whose rows' sums are joined in shared memory
-    // before they are written (two CTAs for 64 threads: there are 16 named barriers, one the CTA's);
-    // 32768 x 512: 34 us with CTAs of 256 threads, 31 with 1024; 16384 x 2048: 62 and 65
+    // one CTA an SM, whose rows' sums are joined in shared memory before they are written (two CTAs for
+    // 64 threads: there are 16 named barriers, one the CTA's); 32768 x 512, bf16 x and fp32 dy: 34 us
+    // with CTAs of 256 threads, 31 with 1024
     static constexpr int kCta = back_cta(TPR);
     static constexpr int kRows = kCta / TPR;
     static constexpr int kCtasPerSm = 1024 / kCta;
@@ -236,6 +240,35 @@ template <int TPR, int CTA>
 __device__ __forceinline__ void group_barrier(int group) {
     if constexpr (TPR == CTA) __syncthreads();
     else if constexpr (TPR > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+
+// A thread's sums of columns c .. c + 7 into a CTA's partial sums [2][d].
+__device__ __forceinline__ void write_sums(const float (&dg)[8], const float (&db)[8], int c, int d, float* out) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<float4*>(out + c + j) = make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
+        *reinterpret_cast<float4*>(out + d + c + j) = make_float4(db[j], db[j + 1], db[j + 2], db[j + 3]);
+    }
+}
+
+// The sums of a CTA's row groups, added in shared memory ([group][2][COLS]) in the groups' order.
+template <int ROWS, int COLS, int CTA>
+__device__ __forceinline__ void join_rows(float* joined, const float (&dg)[8], const float (&db)[8], int group, int c, int d, float* out) {
+    float* own = joined + group * 2 * COLS + c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        own[j] = dg[j];
+        own[COLS + j] = db[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * COLS; i += CTA) {
+        const int col = i % COLS, half = i / COLS;
+        if (col >= d) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int g = 0; g < ROWS; ++g) v += joined[g * 2 * COLS + i];
+        out[half * d + col] = v;
+    }
 }
 
 template <bool DYB, bool XB, int TPR>
@@ -293,29 +326,135 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
     if (!a.dgamma && !a.dbeta) return;
     asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
     float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
-    if constexpr (B::kRows > 1) {  // the CTA's rows first
-        float* own = joined + group * 2 * B::kCols + c;
+    join_rows<B::kRows, B::kCols, B::kCta>(joined, dg, db, group, c, a.d, out);
+}
+
+// 1024 < d <= 8192: a CTA holds one row, the same way, and its next rows are on their way in shared
+// memory: one thread copies whole rows of x, dy and dres (cp.async.bulk; 192 KB an SM, two to four
+// rows ahead), so a row's round trip is behind the arithmetic of the rows before it.
+// Measured, with the joining kernel, against the rows loaded into registers when they are needed: 8192 x 4096 bf16
+// x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86; 20000 x 992 the other way, 33 -> 43.
+template <bool DYB, bool XB, int TPR>
+struct Ahead {
+    static constexpr int kCta = TPR;
+    static constexpr int kCtasPerSm = 1024 / kCta;
+    static constexpr int kCols = TPR * 8;
+    static constexpr int kXBytes = kCols * (XB ? 2 : 4), kDBytes = kCols * (DYB ? 2 : 4);
+    static constexpr int kSlot = 2 * kXBytes + kDBytes;  // x, dy, dres of one row
+    static constexpr int kStages = 24576 / (kSlot / TPR * 128);  // 192 bytes a thread
+    static constexpr size_t kSmem = (size_t)kStages * kSlot;
+    static_assert(kStages >= 2, "rows ahead");
+};
+
+__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Bounded wait; a copy of memory that is there completes, so running out means a broken context.
+__device__ __forceinline__ bool row_landed(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < (1 << 22); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
+template <bool DYB, bool XB, int TPR>
+__global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>::kCtasPerSm)
+    layernorm_ahead_kernel(const LayernormBackwardArgs a) {
+    using B = Ahead<DYB, XB, TPR>;
+    __shared__ float red[2][2][B::kCta / 32];
+    __shared__ uint64_t full[B::kStages];
+    extern __shared__ __align__(128) uint8_t slots[];  // [stage]{x, dy, dres}
+    const int c = threadIdx.x * 8;
+    const float inv_d = 1.f / (float)a.d;
+    const bool mine = c < a.d;  // this thread's columns exist
+    const long long step = gridDim.x, first = blockIdx.x;
+    const uint32_t slots_at = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+    const uint32_t bars = static_cast<uint32_t>(__cvta_generic_to_shared(full));
+    auto fetch = [&](long long t, int stage) {  // one thread
+        if (t >= a.T) return;
+        const uint32_t xb = (uint32_t)a.d * (XB ? 2 : 4), db = (uint32_t)a.d * (DYB ? 2 : 4);
+        const uint32_t dst = slots_at + stage * B::kSlot, bar = bars + 8 * stage;
+        const size_t row = (size_t)t * a.d;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((a.dres ? 2 : 1) * xb + db) : "memory");
+        copy_row(dst, static_cast<const uint8_t*>(a.x) + row * (XB ? 2 : 4), xb, bar);
+        copy_row(dst + B::kXBytes, static_cast<const uint8_t*>(a.dy) + row * (DYB ? 2 : 4), db, bar);
+        if (a.dres) copy_row(dst + B::kXBytes + B::kDBytes, static_cast<const uint8_t*>(a.dres) + row * (XB ? 2 : 4), xb, bar);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < B::kStages; ++s)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * s) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int s = 0; s < B::kStages; ++s) fetch(first + s * step, s);
+    }
+    float dg[8], db[8], gamma[8];
+    weights8(mine ? a.gamma : nullptr, c, 1.f, gamma);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            own[j] = dg[j];
-            own[B::kCols + j] = db[j];
+    for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.f;
+    auto stats = [&](long long t) { return t < a.T ? make_float2(__ldg(a.mean + t), __ldg(a.rstd + t)) : make_float2(0.f, 0.f); };
+    float2 next = stats(first);
+    __syncthreads();
+    int turn = 0, stage = 0;
+    uint32_t phase = 0;
+    bool landed = true;
+    for (long long t = first; t < a.T; t += step, turn ^= 1) {
+        float mean = next.x;
+        const float rstd = next.y;
+        next = stats(t + step);
+        if (!row_landed(bars + 8 * stage, phase)) {
+            landed = false;
+            mean = __uint_as_float(0x7FC00000u);  // the row's result is NaN, not what was there before
         }
-        __syncthreads();
-        for (int i = tid; i < 2 * B::kCols; i += B::kCta) {
-            const int col = i % B::kCols, half = i / B::kCols;
-            if (col >= a.d) continue;
-            float v = 0.f;
+        // xh and v = dy gamma stay in registers between the two halves
+        const uint8_t* slot = slots + stage * B::kSlot;
+        float xh[8], v[8], s[2] = {0.f, 0.f};
+        Raw<XB> res;
+        res.zero();
+        if (mine) {
+            Raw<XB> x;
+            Raw<DYB> dy;
+            x.take(slot, c);
+            dy.take(slot + B::kXBytes, c);
+            if (a.dres) res.take(slot + B::kXBytes + B::kDBytes, c);
 #pragma unroll
-            for (int g = 0; g < B::kRows; ++g) v += joined[g * 2 * B::kCols + i];
-            out[half * a.d + col] = v;
+            for (int j = 0; j < 8; ++j) {
+                const float w = dy.get(j);
+                xh[j] = (x.get(j) - mean) * rstd;
+                v[j] = w * gamma[j];
+                s[0] += v[j];
+                s[1] = fmaf(v[j], xh[j], s[1]);
+                dg[j] = fmaf(w, xh[j], dg[j]);
+                db[j] += w;
+            }
         }
-    } else if (mine) {
+        // the two arrays of `red` alternate, so one barrier a row is enough; after it the CTA has
+        // read the slot
+        row_sum<TPR, 2, B::kCta>(s, red[turn], CtaBarrier());
+        if (threadIdx.x == 0) fetch(t + B::kStages * step, stage);
+        if (mine) {
+            const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            *reinterpret_cast<float4*>(out + c + j) = make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
-            *reinterpret_cast<float4*>(out + a.d + c + j) = make_float4(db[j], db[j + 1], db[j + 2], db[j + 3]);
+            for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[j], m2, v[j] - m1), res.get(j));
+            store8<XB>(a.dx, (size_t)t * a.d + c, v);
+        }
+        if (++stage == B::kStages) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
+    if (!landed)  // give copies that are late another chance to end before the CTA does
+        for (int s = 0; s < B::kStages; ++s) row_landed(bars + 8 * s, phase);
+    if (!a.dgamma && !a.dbeta) return;
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
+    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
+    if (mine) write_sums(dg, db, c, a.d, out);
 }
 
 // 8192 < d <= 16384: 1024 threads leave 64 registers each, so dgamma and dbeta are summed in shared
@@ -409,27 +548,43 @@ __global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const Layernor
     }
 }
 
-// Adds the CTAs' partial sums, [parts][2 d] -> dgamma, dbeta: a CTA per 32 columns, its 16 warps
-// take every 16th part in order, then the warps' sums are added in order.
+// Adds the CTAs' partial sums, [parts][2 d] -> dgamma, dbeta.  A CTA takes 32 columns: 8 lanes read
+// 128 bytes of a part, a warp four parts, the CTA 64; a lane's sums are added over the warp's
+// four parts by shuffles and over the warps in order.
 constexpr int kJoin = 512;
 __global__ void __launch_bounds__(kJoin) layernorm_join_kernel(const float* partial, int parts, int d, float* dgamma, float* dbeta) {
-    __shared__ float sums[kJoin / 32][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    __shared__ float4 sums[kJoin / 32][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 7;
+    const int c = blockIdx.x * 32 + q * 4;  // 2 d is a multiple of 32
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float v = 0.f;
-    if (c < 2 * d) {
-#pragma unroll 8
-        for (int p = warp; p < parts; p += kJoin / 32) v += __ldcg(partial + (size_t)p * 2 * d + c);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5
+    for (int p = warp * 4 + (lane >> 3); p < parts; p += kJoin / 8) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(partial + (size_t)p * 2 * d + c));
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
     }
-    sums[warp][lane] = v;
+#pragma unroll
+    for (int o = 8; o < 32; o *= 2) {
+        v.x += __shfl_xor_sync(kFull, v.x, o);
+        v.y += __shfl_xor_sync(kFull, v.y, o);
+        v.z += __shfl_xor_sync(kFull, v.z, o);
+        v.w += __shfl_xor_sync(kFull, v.w, o);
+    }
+    if (lane < 8) sums[warp][q] = v;
     __syncthreads();
-    if (warp == 0 && c < 2 * d) {
-        for (int w = 1; w < kJoin / 32; ++w) v += sums[w][lane];
-        if (c < d) {
-            if (dgamma) dgamma[c] = v;
+    if (threadIdx.x < 32) {
+        const float* col = reinterpret_cast<const float*>(sums) + threadIdx.x;
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoin / 32; ++w) t += col[w * 32];
+        const int at = blockIdx.x * 32 + threadIdx.x;
+        if (at < d) {
+            if (dgamma) dgamma[at] = t;
         } else if (dbeta) {
-            dbeta[c - d] = v;
+            dbeta[at - d] = t;
         }
     }
 }
@@ -513,6 +668,7 @@ int row_threads(int d, int vpt) { return pow2_at_least((d / 8 + vpt - 1) / vpt);
 
 constexpr int kForwardMax = 1024 * 8 * 4;
 constexpr int kBackwardMax = 1024 * 8, kTallMax = 1024 * 8 * 2;
+constexpr int kAheadMin = 256;  // threads of a row from which the next rows are copied ahead
 
 template <bool XB, int R>
 void forward_rows(const LayernormArgs& a, int sm_count, cudaStream_t s) {
@@ -551,10 +707,10 @@ cudaError_t forward(const LayernormArgs& a, int sm_count, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// CTAs of the backward kernel, all resident at once, and their partial sums
+// CTAs of the backward kernels, all resident at once, and their partial sums
 int backward_parts(int T, int d, int sm_count) {
     if (d > kBackwardMax) return std::min(T, sm_count);
-    const int tpr = row_threads(d, 1), cta = back_cta(tpr), rows = cta / tpr;
+    const int tpr = row_threads(d, 1), cta = tpr >= kAheadMin ? tpr : back_cta(tpr), rows = cta / tpr;
     return std::min((T + rows - 1) / rows, sm_count * (1024 / cta));
 }
 
@@ -563,7 +719,7 @@ cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((2 * a.d + 31) / 32);
+    cfg.gridDim = dim3(2 * a.d / 32);
     cfg.blockDim = dim3(kJoin);
     cfg.stream = s;
     cfg.attrs = &at;
@@ -596,9 +752,15 @@ cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t 
     const int parts = backward_parts(a.T, a.d, sm_count);
     cudaError_t e = cudaSuccess;
     auto go = [&](auto tpr) {
-        using B = Back<decltype(tpr)::value>;
+        constexpr int kTpr = decltype(tpr)::value;
         static std::atomic<unsigned long long> ready{0};
-        e = launch_big(layernorm_backward_kernel<DYB, XB, decltype(tpr)::value>, a, parts, B::kCta, B::kSmem, ready, s);
+        if constexpr (kTpr >= kAheadMin) {
+            using B = Ahead<DYB, XB, kTpr>;
+            e = launch_big(layernorm_ahead_kernel<DYB, XB, kTpr>, a, parts, B::kCta, B::kSmem, ready, s);
+        } else {
+            using B = Back<kTpr>;
+            e = launch_big(layernorm_backward_kernel<DYB, XB, kTpr>, a, parts, B::kCta, B::kSmem, ready, s);
+        }
     };
     static std::atomic<unsigned long long> tall_ready{0};
     if (a.d > kBackwardMax) e = launch_big(layernorm_tall_kernel<DYB, XB>, a, parts, kTall, kTallSmem, tall_ready, s);
