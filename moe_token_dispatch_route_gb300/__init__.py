@@ -2,6 +2,7 @@
 
 The compute path lives in the CUDA shared library built from ``csrc/``; the
 Python module ``binding`` only marshals arguments into its C ABI (see
-``include/moe.h``).  ``workloads`` draws the seeded synthetic inputs.
+``include/moe.h``).  ``training`` runs a layer forward and backward on it;
+``workloads`` draws the seeded synthetic inputs.
 """
-__all__ = ["binding", "workloads"]
+__all__ = ["binding", "training", "workloads"]

@@ -1,0 +1,87 @@
+"""One MoE layer, forward and backward, on the library's calls:
+
+    out = x + combine(down(swiglu(up(dispatch(layernorm(x))))))
+
+with Mixtral-style gates (softmax over the k chosen logits).  Between the two passes it keeps the
+dispatched rows, the up projection's outputs in 8 bits, the experts' outputs and the routing; H is
+computed again from the 8-bit values.  The router's own two products ([T, d] by [d, E]) and the
+gates' softmax over k values are PyTorch's.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as b
+
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
+class MoeTrainLayer:
+    """Plans and device buffers of a layer of T tokens of width d, E experts of hidden width F, k
+    experts a token; d and F are multiples of 16.  x: fp32 [T, d].  Weights: W_r bf16 [d, E], W1 bf16
+    [E, d, 2F] (gate columns, then up), W2 bf16 [E, F, d], gamma and beta fp32 [d]; their gradients
+    are fp32."""
+
+    def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0):
+        self.T, self.d, self.F, self.E, self.k, self.eps = T, d, F, E, k, eps
+        dev = torch.device("cuda", device)
+        S = T * k
+        self.up = b.moe_plan(T, d, E, k, 2 * F, route_flags=b.MOE_ROUTE_RENORM, out_dtype=b.MOE_OUT_BF16, device=device)
+        self.down = b.moe_plan(T, F, E, k, d, out_dtype=b.MOE_OUT_BF16, device=device)
+        self.bufs = b.MoeBuffers(self.up, dev)             # routing, dispatched rows, GU, workspace, status
+        self.down_ws = torch.zeros(self.down.workspace_bytes, dtype=torch.uint8, device=dev)
+        self.scratch = b.backward_scratch(self.up)
+
+        def new(*shape, dtype=_BF16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+        # kept from the forward pass
+        self.y, self.mean, self.rstd = new(T, d), new(T, dtype=_F32), new(T, dtype=_F32)
+        self.codes = new(S, 2 * F, dtype=torch.int8)
+        self.scales = new(S, 2 * b.checkpoint_blocks(F), dtype=_F32)
+        self.Y = new(S, d)
+        # passing through
+        self.logits, self.out = new(T, E, dtype=_F32), new(T, d, dtype=_F32)
+        self.H, self.dH, self.dY, self.dA = new(S, F), new(S, F), new(S, d), new(S, d)
+        self.dw, self.dy = new(T, k, dtype=_F32), new(T, d, dtype=_F32)
+        self.ones = torch.ones(T, k, dtype=_F32, device=dev)
+
+    def forward(self, x, gamma, beta, W_r, W1, W2, stream=None):
+        u, r = self.up, self.bufs
+        b.moe_layernorm(u, x, gamma, beta, self.eps, self.y, self.mean, self.rstd, stream)
+        b.moe_router_logits(u, self.y, W_r, None, self.logits, stream)
+        b.route(u, self.logits, r, stream)
+        b.dispatch_gemm(u, self.y, W1, r, stream)                                  # GU in r.Y
+        b.moe_swiglu_checkpoint(u, r.Y, self.H, self.codes, self.scales, stream)
+        b.moe_grouped_gemm(self.down, self.H, r.offsets, W2, self.Y, self.down_ws, r.status, stream)
+        b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out, stream)
+        return self.out.add_(x)
+
+    def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
+        """dout fp32 [T, d].  Writes grads["W1"], ["W2"] (or adds to them), ["W_r"], ["gamma"] and
+        ["beta"], fp32, and returns the gradient of x."""
+        u, dn, r = self.up, self.down, self.bufs
+        b.moe_combine_backward(dn, dout, self.Y, r.topk_w, r.dest, self.dY, self.dw, stream)
+        b.moe_grouped_gemm_dgrad(dn, self.dY, r.offsets, W2, self.dH, self.down_ws, r.status, stream)
+        dGU = r.Y                                                                  # GU's buffer: its values are in the codes
+        b.moe_swiglu_checkpoint_backward(u, self.dH, self.codes, self.scales, self.H, dGU, stream)
+        b.moe_grouped_gemm_wgrad(dn, self.H, self.dY, r.offsets, grads["W2"], self.down_ws, r.status, accumulate, stream)
+        b.moe_grouped_gemm_wgrad(u, r.recv[0], dGU, r.offsets, grads["W1"], r.workspace, r.status, accumulate, stream)
+        b.moe_grouped_gemm_dgrad(u, dGU, r.offsets, W1, self.dA, r.workspace, r.status, stream)
+        b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy, stream)             # the dispatch's gradient
+        # the gates: softmax over the chosen logits
+        w = r.topk_w
+        dlogits = torch.zeros_like(self.logits).scatter_(
+            1, r.topk_idx.long(), w * (self.dw - (w * self.dw).sum(1, keepdim=True)))
+        torch.mm(self.y.float().T, dlogits, out=grads["W_r"])
+        self.dy.addmm_(dlogits, W_r.float().T)
+        dx = torch.empty_like(x)
+        b.moe_layernorm_backward(u, self.dy, x, gamma, self.mean, self.rstd, dout, dx, grads["gamma"], grads["beta"],
+                                 self.scratch, stream)
+        return dx
+
+    def kept_bytes(self) -> int:
+        """What the layer holds between its forward and backward pass."""
+        r = self.bufs
+        kept = [self.y, self.mean, self.rstd, self.codes, self.scales, self.Y, r.recv[0], r.topk_idx, r.topk_w,
+                r.offsets, r.perm, r.dest]
+        return sum(t.numel() * t.element_size() for t in kept)
