@@ -57,8 +57,15 @@ struct Cfg {
     static constexpr int kWarpRows = kRowTile / 2;             // output rows of an epilogue warp
 };
 
+// A tile as the roles take it from the ring: the scheduler has worked out what they need, since a
+// tile's change costs the MMA thread's time (500 cycles of it when each role worked it out itself).
 struct GradTile {
-    int e, c, r, pad;  // expert (-1: no more), column tile, row tile
+    int e, c, r;  // expert (-1: no more), column tile, row tile
+    int seg0;     // expert's first row
+    int nkb;      // k-blocks
+    int rows;     // valid output rows
+    int last;     // of the last k-block: MMA steps | rows to keep when they end inside a step << 8 | half of the MMA's N << 16
+    int boxes;    // weight gradient: rows of P's boxes | of Q's << 8 | Q's chunks are paired << 16
 };
 
 struct GradCtl {
@@ -115,40 +122,41 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Wa
     return mbar_try_wait_cluster(bar, parity) || bar_wait_slow(bar, parity, w, where, honor_abort);
 }
 
-// What a tile asks of every role.
+// The unpacked fields of a tile.
 struct Shape {
-    int seg0;    // expert's first row
-    int nkb;     // k-blocks
+    int seg0, nkb, rows;
     int ksteps;  // MMA steps of 16 in the last k-block
     int half;    // Q rows (columns) per CTA: half of the MMA's N
     int fix;     // rows of the last k-block that are the expert's, when they end inside a step; else 0
-    int rows;    // valid output rows
     // weight gradient, last k-block: rows of its boxes (a last block of one or two steps is loaded in
     // boxes of 16 or 32 rows where the columns are paired: an expert of a few rows costs few bytes)
     int p_box, q_box;
     bool q_paired;
+    __device__ explicit Shape(const GradTile& t)
+        : seg0(t.seg0), nkb(t.nkb), rows(t.rows), ksteps(t.last & 0xFF), half(t.last >> 16), fix(t.last >> 8 & 0xFF),
+          p_box(t.boxes & 0xFF), q_box(t.boxes >> 8 & 0xFF), q_paired(t.boxes >> 16 != 0) {}
 };
 
 template <Form F>
-__device__ __forceinline__ Shape shape_of(const GradParams& p, const int* off, const GradTile& t) {
+__device__ void fill_shape(const GradParams& p, const int* off, GradTile& t) {
     constexpr bool WG = Cfg<F>::kWeight;
     constexpr int kRow = Cfg<F>::kRowTile;
-    Shape s;
-    s.seg0 = off[t.e];
-    const int cnt = off[t.e + 1] - s.seg0;
+    t.seg0 = off[t.e];
+    const int cnt = off[t.e + 1] - t.seg0;
     const int K = WG ? cnt : p.a.N;
-    s.rows = min(kRow, (WG ? p.a.d : cnt) - kRow * t.r);
-    s.half = ((s.rows + 31) & ~31) / 2;
-    s.nkb = (K + kTileK - 1) / kTileK;
-    const int last = K - kTileK * (s.nkb - 1);
-    s.ksteps = (last + kUmmaK - 1) / kUmmaK;
-    s.fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
+    t.rows = min(kRow, (WG ? p.a.d : cnt) - kRow * t.r);
+    const int half = ((t.rows + 31) & ~31) / 2;
+    t.nkb = (K + kTileK - 1) / kTileK;
+    const int last = K - kTileK * (t.nkb - 1);
+    const int ksteps = (last + kUmmaK - 1) / kUmmaK;
+    const int fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
+    t.last = ksteps | fix << 8 | half << 16;
+    t.boxes = 0;
     if (WG) {
-        s.q_paired = p.q_paired && s.half % 64 == 0;  // the peer's first column starts a chunk
-        s.p_box = p.p_paired && s.ksteps <= 2 ? kUmmaK * s.ksteps : kTileK;
-        s.q_box = s.q_paired && s.ksteps <= 2 ? kUmmaK * s.ksteps : kTileK;
+        const bool paired = p.q_paired && half % 64 == 0;  // the peer's first column starts a chunk
+        t.boxes = (p.p_paired && ksteps <= 2 ? kUmmaK * ksteps : kTileK) |
+                  (paired && ksteps <= 2 ? kUmmaK * ksteps : kTileK) << 8 | (paired ? 1 : 0) << 16;
     }
-    return s;
 }
 
 // the next slot of the schedule ring
@@ -202,11 +210,11 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
 // Peer CTA's warp 1, one thread: claims the tiles after a pair's first (which is its own number) and
 // writes them into both CTAs' rings.
 template <Form F>
-__device__ GradTile tile_at(const GradParams& p, const int* base, const short* order, uint32_t i) {
+__device__ GradTile tile_at(const GradParams& p, const int* off, const int* base, const short* order, uint32_t i) {
     constexpr bool WG = Cfg<F>::kWeight;
     const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 1u;
     const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
-    GradTile t{-1, 0, 0, 0};
+    GradTile t{-1, 0, 0, 0, 0, 0, 0, 0};
     if (i >= total) return t;
     int local, rt;
     if (WG) {
@@ -232,11 +240,12 @@ __device__ GradTile tile_at(const GradParams& p, const int* base, const short* o
     const int j = local - band * kBand * p.c_tiles;
     t.c = j / nr;
     t.r = band * kBand + j % nr;
+    fill_shape<F>(p, off, t);
     return t;
 }
 
 template <Form F>
-__device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, const short* order, const Wait& w,
+__device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* off, const int* base, const short* order, const Wait& w,
                           uint32_t lead) {
     Ring ring;
     const uint32_t pairs = gridDim.x / 2;
@@ -244,12 +253,14 @@ __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* base, co
     ring.next();  // the first tile was put into both rings before the roles began
     while (more) {
         if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
-        const GradTile t = tile_at<F>(p, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u));
+        const GradTile t = tile_at<F>(p, off, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u));
         ctl->ring[ring.slot] = t;
         const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), lead);
         const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), lead);
         st_async_v2(dst, (uint32_t)t.e, (uint32_t)t.c, bar);
-        st_async_v2(dst + 8, (uint32_t)t.r, 0u, bar);
+        st_async_v2(dst + 8, (uint32_t)t.r, (uint32_t)t.seg0, bar);
+        st_async_v2(dst + 16, (uint32_t)t.nkb, (uint32_t)t.rows, bar);
+        st_async_v2(dst + 24, (uint32_t)t.last, (uint32_t)t.boxes, bar);
         mbar_arrive(smem_addr(&ctl->sfull[ring.slot]));
         more = t.e >= 0;
         ring.next();
@@ -287,7 +298,7 @@ __device__ __forceinline__ uint32_t q_bytes(const Shape& s, int box) {
 
 // Warp 0, one thread: this CTA's half of P, and the stage barriers' expected bytes.
 template <Form F>
-__device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, const Wait& w, bool leader,
+__device__ void producer_p(const GradParams& p, GradCtl* ctl, uint8_t* sP, const Wait& w, bool leader,
                            uint32_t peer, uint32_t lead, uint32_t rank) {
     using C = Cfg<F>;
     constexpr bool WG = C::kWeight;
@@ -304,7 +315,7 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, ui
         if (leader && !first)  // the description comes from the peer's scheduler
             mbar_arrive_expect_tx(smem_addr(&ctl->sfull[ring.slot]), (uint32_t)sizeof(GradTile));
         if (!take<false>(ctl, ring, t, w, 52, leader, peer) || t.e < 0) break;
-        const Shape s = shape_of<F>(p, off, t);
+        const Shape s(t);
         const int c0 = 256 * t.c + side;
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
         const int row0 = WG ? s.seg0 : t.e * p.a.d + c0;
@@ -351,7 +362,7 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, const int* off, ui
 
 // Warp 2, one thread: this CTA's half of Q.
 template <Form F>
-__device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sQ, const Wait& w, bool leader,
+__device__ void producer_q(const GradParams& p, GradCtl* ctl, uint8_t* sQ, const Wait& w, bool leader,
                            uint32_t peer, uint32_t lead, uint32_t rank) {
     using C = Cfg<F>;
     constexpr bool WG = C::kWeight;
@@ -362,7 +373,7 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, ui
     GradTile t;
     for (;;) {
         if (!take<false>(ctl, ring, t, w, 56, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<F>(p, off, t);
+        const Shape s(t);
         const int r0 = C::kRowTile * t.r + s.half * (int)(rank & 1u);
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
         const int chunks = s.half > 64 ? 2 : 1;
@@ -385,7 +396,7 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, const int* off, ui
 
 // Warp 3 (weight gradient): zeroes the rows of a last k-block that are not the expert's, up to
 // the end of its last step of 16, in both operands.
-__device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, const Wait& w,
+__device__ void zero_rows(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t* sQ, const Wait& w,
                           bool leader, uint32_t peer, uint32_t lead) {
     using C = Cfg<Form::kWeight>;
     const int lane = threadIdx.x & 31;
@@ -395,7 +406,7 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
     GradTile t;
     for (;;) {
         if (!take<true>(ctl, ring, t, w, 58, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<Form::kWeight>(p, off, t);
+        const Shape s(t);
         if (s.fix) {
             Stage<C::kStages> at = st;
             at.skip(s.nkb - 1);
@@ -424,7 +435,7 @@ __device__ void zero_rows(const GradParams& p, GradCtl* ctl, const int* off, uin
 }
 
 template <Form F>
-__device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint8_t* sP, uint8_t* sQ, uint32_t tmem,
+__device__ void mma_role(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t* sQ, uint32_t tmem,
                          const Wait& w, uint32_t peer) {
     using C = Cfg<F>;
     constexpr bool WG = C::kWeight;
@@ -441,8 +452,17 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
     GradTile t;
     bool ok = true;
     while (ok) {
-        if (!take<false>(ctl, ring, t, w, 61, true, peer) || t.e < 0) break;
-        const Shape s = shape_of<F>(p, off, t);
+        // the slot is handed back after the tile's first sum is issued, off the path from tile to tile
+        if (!bar_wait(smem_addr(&ctl->sfull[ring.slot]), ring.phase, w, 61)) break;
+        t = ctl->ring[ring.slot];
+        const uint32_t taken = mapa_shared(smem_addr(&ctl->sempty[ring.slot]), peer);
+        ring.next();
+        if (t.e < 0 || t.nkb == 0) {
+            mbar_arrive_remote(taken);
+            if (t.e < 0) break;
+            continue;
+        }
+        const Shape s(t);
         const uint32_t idesc = kDesc | ((uint32_t)(2 * s.half) >> 3) << 17;
         for (int kb0 = 0; ok && kb0 < s.nkb; kb0 += p.chunk_kb) {
             if (!(ok = bar_wait(smem_addr(&ctl->tempty[acc]), aphase ^ 1u, w, 62))) break;
@@ -482,6 +502,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, const int* off, uint
                 st.next();
             }
             umma_commit_pair_mc(smem_addr(&ctl->tfull[acc]), 0x3);
+            if (kb0 == 0) mbar_arrive_remote(taken);
             if ((acc ^= 1) == 0) aphase ^= 1u;
         }
     }
@@ -513,7 +534,7 @@ __device__ __forceinline__ void walk_rows(uint8_t* at, size_t pitch, int n, Visi
 // up to 128 r, are in registers before the first store, so the accumulator is handed
 // back while the stores are still leaving.
 template <Form F>
-__device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off, uint32_t tmem, const Wait& w,
+__device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, const Wait& w,
                               bool leader, uint32_t peer, uint32_t lead, uint32_t rank) {
     using C = Cfg<F>;
     constexpr bool WG = C::kWeight;
@@ -526,7 +547,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, const int* off,
     GradTile t;
     for (;;) {
         if (!take<true>(ctl, ring, t, w, 66, leader, peer) || t.e < 0) return;
-        const Shape s = shape_of<F>(p, off, t);
+        const Shape s(t);
         const int cols = min(kRows, s.rows - kRows * h);  // this warp's valid rows, may be <= 0
         const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
         const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + (size_t)(C::kRowTile * t.r + kRows * h);
@@ -673,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     if (bad && tid == 0) report_error(p.a.status, kStDevice, -2, off[E], 0);
     __syncthreads();
     if (tid == 0) {  // a pair's first tile is its own number: both CTAs know it without a claim
-        ctl->ring[0] = tile_at<F>(p, base, order, blockIdx.x / 2);
+        ctl->ring[0] = tile_at<F>(p, off, base, order, blockIdx.x / 2);
         mbar_arrive(smem_addr(&ctl->sfull[0]));
     }
     tc_fence_before();
@@ -689,22 +710,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (!bad) {
             if (warp == 0) {
-                if (lane == 0) producer_p<F>(p, ctl, off, sP, w, leader, sched, lead, rank);
+                if (lane == 0) producer_p<F>(p, ctl, sP, w, leader, sched, lead, rank);
             } else if (warp == 1) {
                 if (lane == 0) {
-                    if (leader) mma_role<F>(p, ctl, off, sP, sQ, tmem, w, sched);
-                    else scheduler<F>(p, ctl, base, order, w, lead);
+                    if (leader) mma_role<F>(p, ctl, sP, sQ, tmem, w, sched);
+                    else scheduler<F>(p, ctl, off, base, order, w, lead);
                 }
             } else if (warp == 2) {
-                if (lane == 0) producer_q<F>(p, ctl, off, sQ, w, leader, sched, lead, rank);
+                if (lane == 0) producer_q<F>(p, ctl, sQ, w, leader, sched, lead, rank);
             } else if (WG) {
-                zero_rows(p, ctl, off, sP, sQ, w, leader, sched, lead);
+                zero_rows(p, ctl, sP, sQ, w, leader, sched, lead);
             }
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if (!bad) epilogue_role<F>(p, ctl, off, tmem, w, leader, sched, lead, rank);
+        if (!bad) epilogue_role<F>(p, ctl, tmem, w, leader, sched, lead, rank);
     }
 
     tc_fence_before();
@@ -732,7 +753,7 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<Form::kInput>() <= 232448 && smem_bytes<Form::kNarrow>() <= 232448, "more than 227 KB of shared memory per CTA");
 static_assert(Cfg<Form::kInput>::kStages <= kMaxStages && Cfg<Form::kNarrow>::kStages <= kMaxStages, "stages");
-static_assert(sizeof(GradTile) == 16, "a tile travels as two 8-byte stores");
+static_assert(sizeof(GradTile) == 32, "a tile travels as four 8-byte stores");
 
 // Pairs of CTAs that are resident together on the current device; the kernel's attributes are set once per device.
 template <Form F>
