@@ -510,21 +510,23 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t
     bar_wait(smem_addr(&ctl->mma_done), 0u, w, 65, false);
 }
 
-// visit(address, i, i < n) for i = 0, STEP, ... below ROWS, addresses `pitch` bytes apart for each step.  The
+// visit(address, i, rows left) for i = 0, STEP, ... below ROWS, addresses `pitch` bytes apart for each
+// step; n - i rows are left, or STEP where a lane of the warp has all of its rows.  The
 // address is stepped, not multiplied out: 128 products in flight spilled, and the whole epilogue
-// ran at 2.6 TB/s.  A warp whose lanes all have their rows skips the bounds.
+// ran at 2.6 TB/s.
 template <int ROWS, int STEP, class Visit>
 __device__ __forceinline__ void walk_rows(uint8_t* at, size_t pitch, int n, Visit visit) {
-    if (__all_sync(kFull, n > ROWS - STEP)) {
+    constexpr int kAll = STEP == 4 ? ROWS - 2 : ROWS;  // (of four rows a lane stores two)
+    if (__all_sync(kFull, n >= kAll)) {
 #pragma unroll
         for (int i = 0; i < ROWS; i += STEP) {
-            visit(at, i, true);
+            visit(at, i, STEP);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS; i += STEP) {
-            visit(at, i, i < n);
+            visit(at, i, n - i);
             asm volatile("add.u64 %0, %0, %1;" : "+l"(at) : "l"(pitch));
         }
     }
@@ -555,29 +557,37 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
         const int mine = c < p.c_size ? cols : 0;  // this lane's valid rows
         const bool add = WG && p.a.accumulate;
         if (add && s.nkb == 0) continue;  // nothing to add
-        float sum[kRows];
+        uint32_t sum[kRows / 32][32];  // fp32 bits
         if (add) {  // what is there already, read while the MMAs run
-            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
-                         [&](uint8_t* at, int i, bool in) { sum[i] = in ? __ldcs(reinterpret_cast<float*>(at)) : 0.f; });
+            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine, [&](uint8_t* at, int i, int n) {
+                sum[i / 32][i % 32] = n > 0 ? __ldcs(reinterpret_cast<uint32_t*>(at)) : 0u;
+            });
         } else if (s.nkb == 0) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
+            for (int i = 0; i < kRows; ++i) sum[i / 32][i % 32] = 0u;
         }
         for (int kb = 0; kb < s.nkb; kb += p.chunk_kb) {
             const bool ready = bar_wait(smem_addr(&ctl->tfull[acc]), aphase, w, 67);
             if (!__all_sync(kFull, ready)) return;
             tc_fence_after();
-            const bool first = kb == 0 && !add;
             const uint32_t base = tmem + (uint32_t)(acc * 256 + kRows * h) + ((uint32_t)(32 * q) << 16);
+            if (kb == 0 && !add) {  // the first sum is loaded where it stays, all of it in flight
 #pragma unroll
-            for (int g = 0; g < kRows / 32; ++g) {
-                if (32 * g < cols) {
-                    uint32_t v[32];
-                    tmem_ld_32x32(base + 32 * g, v);
-                    tmem_ld_wait(v);
+                for (int g = 0; g < kRows / 32; ++g)
+                    if (32 * g < cols) tmem_ld_32x32(base + 32 * g, sum[g]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        sum[32 * g + i] = first ? __uint_as_float(v[i]) : sum[32 * g + i] + __uint_as_float(v[i]);
+                for (int g = 0; g < kRows / 32; ++g) tmem_ld_wait(sum[g]);
+            } else {
+#pragma unroll
+                for (int g = 0; g < kRows / 32; ++g) {
+                    if (32 * g < cols) {
+                        uint32_t v[32];
+                        tmem_ld_32x32(base + 32 * g, v);
+                        tmem_ld_wait(v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sum[g][i] = __float_as_uint(__uint_as_float(sum[g][i]) + __uint_as_float(v[i]));
+                    }
                 }
             }
             tc_fence_before();
@@ -590,17 +600,23 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
             if ((acc ^= 1) == 0) aphase ^= 1u;
         }
         if (p.a.out_bf16) {
-            // two rows at a time: even lanes store columns c, c + 1 of the first, odd lanes of the second
+            // Four rows at a time: even lanes store columns c, c + 1 of the first two, odd lanes c - 1, c
+            // of the last two.  A lane rounds and packs two rows of its column, so one exchange serves four
+            // rows; the exchanges share a pipe with the stores.
             const int odd = lane & 1;
-            walk_rows<kRows, 2>(static_cast<uint8_t*>(p.a.out) + ((row0 + odd) * ld + (c - odd)) * 2, ld * 4, mine - odd,
-                         [&](uint8_t* at, int i, bool in) {
-                const float other = __shfl_xor_sync(kFull, odd ? sum[i] : sum[i + 1], 1);
-                const uint32_t v = odd ? bf16x2(other, sum[i + 1]) : bf16x2(sum[i], other);
-                if (in) __stcs(reinterpret_cast<uint32_t*>(at), v);
+            const uint32_t lo = odd ? 0x1054u : 0x5410u, hi = odd ? 0x3276u : 0x7632u;  // (mine, other) or (other, mine)
+            walk_rows<kRows, 4>(static_cast<uint8_t*>(p.a.out) + ((row0 + 2 * odd) * ld + (c - odd)) * 2, ld * 8, mine - 2 * odd,
+                                [&](uint8_t* at, int i, int n) {
+                const uint32_t a = bf16x2(__uint_as_float(sum[i / 32][i % 32]), __uint_as_float(sum[i / 32][i % 32 + 1]));
+                const uint32_t b = bf16x2(__uint_as_float(sum[i / 32][i % 32 + 2]), __uint_as_float(sum[i / 32][i % 32 + 3]));
+                const uint32_t other = __shfl_xor_sync(kFull, odd ? a : b, 1), own = odd ? b : a;
+                if (n > 0) __stcs(reinterpret_cast<uint32_t*>(at), __byte_perm(own, other, lo));
+                if (n > 1) __stcs(reinterpret_cast<uint32_t*>(at + ld * 2), __byte_perm(own, other, hi));
             });
         } else {
-            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine,
-                         [&](uint8_t* at, int i, bool in) { if (in) __stcs(reinterpret_cast<float*>(at), sum[i]); });
+            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine, [&](uint8_t* at, int i, int n) {
+                if (n > 0) __stcs(reinterpret_cast<uint32_t*>(at), sum[i / 32][i % 32]);
+            });
         }
     }
 }
