@@ -23,6 +23,10 @@
 // (claims and tails inside their loop cost 250 cycles more, and the weight gradient waited for
 // loads 35% of the time).
 //
+// Few tiles and a long reduction (more than 32 or 64 k-blocks): it is cut into pieces of at least 16, at
+// most two for each pair of CTAs, whose sums go to the workspace; a second kernel adds
+// them in order (2 experts, 192 x 13808, 166 rows: 67 us whole, 19 in pieces).
+//
 // fp32 outputs: the tensor cores' running sum rounds towards zero at every step of 16 products,
 // which over a long reduction is a bias (relative error 1e-6 at 1024 products, 1.6e-5 at 14336).
 // So a sum runs in TMEM over 768 products (7e-7) and the epilogue adds these in registers; the two
@@ -55,6 +59,12 @@ struct Cfg {
     static constexpr int kQBytes = kRowTile / 2 * kTileK * 2;  // one CTA's half of Q
     static constexpr int kStages = F == Form::kNarrow ? 10 : 6;
     static constexpr int kWarpRows = kRowTile / 2;             // output rows of an epilogue warp
+    // Splitting a reduction costs about as much as this many k-blocks (a second kernel) and as many
+    // more for each piece; reductions of up to kMinSplit blocks stay whole (16 tiles of 41 blocks: 20 us
+    // whole, 28 in two pieces).
+    static constexpr int kSplitCost = F == Form::kNarrow ? 14 : 24;
+    static constexpr int kPieceCost = F == Form::kNarrow ? 2 : 4;
+    static constexpr int kMinSplit = F == Form::kNarrow ? 32 : 64;
 };
 
 // A tile as the roles take it from the ring: the scheduler has worked out what they need, since a
@@ -66,6 +76,23 @@ struct GradTile {
     int rows;     // valid output rows
     int last;     // of the last k-block: MMA steps | rows to keep when they end inside a step << 8 | half of the MMA's N << 16
     int boxes;    // weight gradient: rows of P's boxes | of Q's << 8 | Q's chunks are paired << 16
+    int kbeg;     // first k-block
+    int slot;     // >= 0: a piece of a tile's reduction, whose sums go there
+};
+
+// A tile whose reduction is cut into pieces, for the joining kernel: its pieces are in slots
+// slot0, slot0 + stride, ... (n of them).
+struct SplitTile {
+    long long out_row;  // of the tile's first row
+    int c0, rows;
+    int slot0, n, stride, pad;
+};
+constexpr int kMaxSplit = 256;    // split tiles: at most one for each pair of CTAs
+constexpr int kMinPieceKb = 16;   // shortest piece, in k-blocks
+// The split area of a workspace: the number of split tiles, their list, the slots.
+struct SplitArea {
+    int count, pad[7];
+    SplitTile tile[kMaxSplit];
 };
 
 struct GradCtl {
@@ -81,6 +108,12 @@ struct GradCtl {
     GradTile ring[kGradRing];
     uint32_t tmem_base;
     int abort;
+    // Pieces of at most `limit` k-blocks.  Input gradient: every tile has `pieces`; weight gradient, where
+    // no piece is longer than a pair's share of all the work: the first `split_experts` of
+    // `order` have, expert k's from piece split_base[k] of an output tile on.
+    int limit, pieces, split_experts, split_items;
+    int total_kb;  // weight gradient: k-blocks of all experts
+    int split_base[kMaxSplit + 1];
 };
 
 struct GradParams {
@@ -94,6 +127,8 @@ struct GradParams {
     int c_tiles, r_tiles;          // r_tiles: weight gradient only
     int chunk_kb;
     int c_size;                    // extent of c: d or N
+    SplitArea* split;              // null: no tile is split
+    float* slots;
 };
 
 struct Wait {
@@ -137,8 +172,20 @@ struct Shape {
           p_box(t.boxes & 0xFF), q_box(t.boxes >> 8 & 0xFF), q_paired(t.boxes >> 16 != 0) {}
 };
 
+// k-blocks of a reduction, and of each of its pieces
 template <Form F>
-__device__ void fill_shape(const GradParams& p, const int* off, GradTile& t) {
+__device__ __forceinline__ int blocks_of(const GradParams& p, int rows) {
+    return ((Cfg<F>::kWeight ? rows : p.a.N) + kTileK - 1) / kTileK;
+}
+template <Form F>
+__device__ __forceinline__ int piece_blocks(int nkb, int limit) {
+    if (nkb <= limit || nkb <= Cfg<F>::kMinSplit) return nkb;
+    const int n = (nkb + limit - 1) / limit;
+    return (nkb + n - 1) / n;
+}
+
+template <Form F>
+__device__ void fill_shape(const GradParams& p, const int* off, GradTile& t, int piece, int limit) {
     constexpr bool WG = Cfg<F>::kWeight;
     constexpr int kRow = Cfg<F>::kRowTile;
     t.seg0 = off[t.e];
@@ -146,8 +193,10 @@ __device__ void fill_shape(const GradParams& p, const int* off, GradTile& t) {
     const int K = WG ? cnt : p.a.N;
     t.rows = min(kRow, (WG ? p.a.d : cnt) - kRow * t.r);
     const int half = ((t.rows + 31) & ~31) / 2;
-    t.nkb = (K + kTileK - 1) / kTileK;
-    const int last = K - kTileK * (t.nkb - 1);
+    const int nkb = blocks_of<F>(p, cnt), len = piece_blocks<F>(nkb, limit);
+    t.kbeg = piece * len;
+    t.nkb = min(len, nkb - t.kbeg);
+    const int last = t.kbeg + t.nkb == nkb ? K - kTileK * (nkb - 1) : kTileK;
     const int ksteps = (last + kUmmaK - 1) / kUmmaK;
     const int fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
     t.last = ksteps | fix << 8 | half << 16;
@@ -207,22 +256,40 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
     return true;
 }
 
-// Peer CTA's warp 1, one thread: claims the tiles after a pair's first (which is its own number) and
-// writes them into both CTAs' rings.
+// Work item i: a tile, or a piece of one.  `note`: the first piece of a tile enters it in the list of split tiles.
 template <Form F>
-__device__ GradTile tile_at(const GradParams& p, const int* off, const int* base, const short* order, uint32_t i) {
+__device__ GradTile item_at(const GradParams& p, const GradCtl* ctl, const int* off, const int* base, const short* order,
+                            uint32_t i, bool note) {
     constexpr bool WG = Cfg<F>::kWeight;
-    const uint32_t per_expert = WG ? (uint32_t)p.c_tiles * (uint32_t)p.r_tiles : 1u;
-    const uint32_t total = WG ? (uint32_t)p.a.E * per_expert : (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles;
-    GradTile t{-1, 0, 0, 0, 0, 0, 0, 0};
-    if (i >= total) return t;
-    int local, rt;
+    GradTile t{-1, 0, 0, 0, 0, 0, 0, 0, 0, -1};
+    int local, rt, piece = 0, n = 1, stride = 1, ordinal;
     if (WG) {
-        t.e = order[i / per_expert];
-        local = (int)(i % per_expert);
+        const uint32_t per_expert = (uint32_t)p.c_tiles * (uint32_t)p.r_tiles;
         rt = p.r_tiles;
+        if (i < (uint32_t)ctl->split_items) {
+            int k = 0;
+            while ((uint32_t)ctl->split_base[k + 1] * per_expert <= i) ++k;
+            const uint32_t j = i - (uint32_t)ctl->split_base[k] * per_expert;
+            t.e = order[k];
+            piece = (int)(j / per_expert);
+            local = (int)(j % per_expert);
+            n = ctl->split_base[k + 1] - ctl->split_base[k];
+            stride = (int)per_expert;
+            ordinal = k * (int)per_expert + local;
+        } else {
+            const uint32_t j = i - (uint32_t)ctl->split_items;
+            if (j >= (uint32_t)(p.a.E - ctl->split_experts) * per_expert) return t;
+            t.e = order[ctl->split_experts + j / per_expert];
+            local = (int)(j % per_expert);
+            ordinal = 0;
+        }
     } else {
-        const int u = (int)(i / (uint32_t)p.c_tiles);
+        n = ctl->pieces;
+        const uint32_t tile = i / (uint32_t)n;
+        if (tile >= (uint32_t)base[p.a.E] * (uint32_t)p.c_tiles) return t;
+        piece = (int)(i % (uint32_t)n);
+        ordinal = (int)tile;
+        const int u = (int)(tile / (uint32_t)p.c_tiles);
         int lo = 0, hi = p.a.E;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -230,7 +297,7 @@ __device__ GradTile tile_at(const GradParams& p, const int* off, const int* base
             else hi = mid;
         }
         t.e = lo;
-        local = (int)(i - (uint32_t)base[lo] * (uint32_t)p.c_tiles);
+        local = (int)(tile - (uint32_t)base[lo] * (uint32_t)p.c_tiles);
         rt = base[lo + 1] - base[lo];
     }
     // bands of kBand row tiles, all column tiles of a band together: about as many row as column
@@ -240,20 +307,74 @@ __device__ GradTile tile_at(const GradParams& p, const int* off, const int* base
     const int j = local - band * kBand * p.c_tiles;
     t.c = j / nr;
     t.r = band * kBand + j % nr;
-    fill_shape<F>(p, off, t);
+    fill_shape<F>(p, off, t, piece, ctl->limit);
+    if (n > 1) {
+        t.slot = (int)i;
+        if (note && piece == 0 && ordinal < kMaxSplit) {
+            const long long row = (WG ? (long long)t.e * p.a.d : (long long)t.seg0) + (long long)Cfg<F>::kRowTile * t.r;
+            p.split->tile[ordinal] = SplitTile{row, 256 * t.c, t.rows, t.slot, n, stride, 0};
+        }
+    }
     return t;
 }
 
+// How the reductions are cut, by one thread: see GradCtl.
+template <Form F>
+__device__ void plan_pieces(const GradParams& p, GradCtl* ctl, const int* off, const int* base, const short* order, bool write) {
+    using C = Cfg<F>;
+    constexpr bool WG = Cfg<F>::kWeight;
+    ctl->limit = 1 << 30;
+    ctl->pieces = 1;
+    ctl->split_experts = ctl->split_items = 0;
+    if (!p.split) return;
+    const int pairs = (int)(gridDim.x / 2);
+    const long long per_expert = (long long)p.c_tiles * p.r_tiles;
+    int split = 0;
+    if (WG) {
+        const long long total = ctl->total_kb * per_expert;
+        const int limit = (int)min((long long)(1 << 30), max((long long)kMinPieceKb, (total + pairs - 1) / pairs));
+        ctl->limit = limit;
+        int k = 0, run = 0;
+        for (; k < p.a.E && k < kMaxSplit; ++k) {  // most rows first
+            const int nkb = blocks_of<F>(p, off[order[k] + 1] - off[order[k]]), len = piece_blocks<F>(nkb, limit);
+            if (len == nkb) break;
+            ctl->split_base[k] = run;
+            run += (nkb + len - 1) / len;
+        }
+        ctl->split_base[k] = run;
+        ctl->split_experts = k;
+        ctl->split_items = (int)(run * per_expert);
+        split = (int)(k * per_expert);
+    } else {
+        // all tiles have the same reduction: the number of pieces whose rounds of pairs end first
+        const int nkb = blocks_of<F>(p, 0), tiles = base[p.a.E] * p.c_tiles;
+        int best = (tiles + pairs - 1) / pairs * nkb;
+        for (int n = 2; nkb > C::kMinSplit && tiles * n <= 2 * pairs && n * kMinPieceKb <= nkb; ++n) {
+            const int len = (nkb + n - 1) / n, cost = (tiles * n + pairs - 1) / pairs * len + C::kSplitCost + C::kPieceCost * n;
+            if (cost < best) {
+                best = cost;
+                ctl->limit = len;
+            }
+        }
+        const int len = piece_blocks<F>(nkb, ctl->limit);
+        ctl->pieces = (nkb + len - 1) / len;
+        if (ctl->pieces > 1) split = tiles;
+    }
+    if (write) p.split->count = split;
+}
+
+// Peer CTA's warp 1, one thread: claims the items after a pair's first (which is its own number) and
+// writes them into both CTAs' rings.
 template <Form F>
 __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* off, const int* base, const short* order, const Wait& w,
                           uint32_t lead) {
     Ring ring;
     const uint32_t pairs = gridDim.x / 2;
     bool more = ctl->ring[0].e >= 0;
-    ring.next();  // the first tile was put into both rings before the roles began
+    ring.next();  // the first item was put into both rings before the roles began
     while (more) {
         if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
-        const GradTile t = tile_at<F>(p, off, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u));
+        const GradTile t = item_at<F>(p, ctl, off, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u), true);
         ctl->ring[ring.slot] = t;
         const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), lead);
         const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), lead);
@@ -261,6 +382,7 @@ __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* off, con
         st_async_v2(dst + 8, (uint32_t)t.r, (uint32_t)t.seg0, bar);
         st_async_v2(dst + 16, (uint32_t)t.nkb, (uint32_t)t.rows, bar);
         st_async_v2(dst + 24, (uint32_t)t.last, (uint32_t)t.boxes, bar);
+        st_async_v2(dst + 32, (uint32_t)t.kbeg, (uint32_t)t.slot, bar);
         mbar_arrive(smem_addr(&ctl->sfull[ring.slot]));
         more = t.e >= 0;
         ring.next();
@@ -318,14 +440,14 @@ __device__ void producer_p(const GradParams& p, GradCtl* ctl, uint8_t* sP, const
         const Shape s(t);
         const int c0 = 256 * t.c + side;
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
-        const int row0 = WG ? s.seg0 : t.e * p.a.d + c0;
+        const int row0 = WG ? s.seg0 + t.kbeg * kTileK : t.e * p.a.d + c0, k0 = t.kbeg * kTileK;
         const uint32_t bytes = 2 * (kOpBytes + q_bytes<F>(s, kTileK));
         for (int kb = 0; kb < whole; ++kb) {
             if (!(ok = bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 53))) break;
             if (leader) mbar_arrive_expect_tx(full0 + 8 * st.s, bytes);
             if (WG) load_mnmajor(dst0 + st.s * kOpBytes, &p.p_map, p.p_pair, p.p_paired, full_lead + 8 * st.s, c0,
                                  row0 + kb * kTileK, 2, kTileK);
-            else tma_load_2d_pair(dst0 + st.s * kOpBytes, &p.p_map, full_lead + 8 * st.s, kb * kTileK, row0);
+            else tma_load_2d_pair(dst0 + st.s * kOpBytes, &p.p_map, full_lead + 8 * st.s, k0 + kb * kTileK, row0);
             st.next();
             ++uses;
         }
@@ -377,18 +499,19 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, uint8_t* sQ, const
         const int r0 = C::kRowTile * t.r + s.half * (int)(rank & 1u);
         const int whole = WG && s.nkb > 0 ? s.nkb - 1 : s.nkb;
         const int chunks = s.half > 64 ? 2 : 1;
+        const int k0 = t.kbeg * kTileK;
         for (int kb = 0; kb < whole; ++kb) {
             if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
             if (WG) load_mnmajor(dst0 + st.s * C::kQBytes, &p.q_map, p.q_pair, s.q_paired, full_lead + 8 * st.s, r0,
-                                 s.seg0 + kb * kTileK, chunks, kTileK);
-            else load_kmajor(dst0 + st.s * C::kQBytes, &p.q_map, &p.q_tail, full_lead + 8 * st.s, kb * kTileK, s.seg0 + r0, s.half, C::kRowTile / 2);
+                                 s.seg0 + k0 + kb * kTileK, chunks, kTileK);
+            else load_kmajor(dst0 + st.s * C::kQBytes, &p.q_map, &p.q_tail, full_lead + 8 * st.s, k0 + kb * kTileK, s.seg0 + r0, s.half, C::kRowTile / 2);
             st.next();
         }
         if (whole < s.nkb) {
             if (!bar_wait(empty0 + 8 * st.s, st.phase ^ 1u, w, 57)) return;
             load_mnmajor(dst0 + st.s * C::kQBytes, &p.q_map, p.q_pair, s.q_paired,
                          s.fix ? mapa_shared(smem_addr(&ctl->tail[st.s]), rank) : full_lead + 8 * st.s, r0,
-                         s.seg0 + whole * kTileK, chunks, s.q_box);
+                         s.seg0 + k0 + whole * kTileK, chunks, s.q_box);
             st.next();
         }
     }
@@ -552,14 +675,30 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
         const Shape s(t);
         const int cols = min(kRows, s.rows - kRows * h);  // this warp's valid rows, may be <= 0
         const int c = 256 * t.c + 128 * (int)(rank & 1u) + 32 * q + lane;
-        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + (size_t)(C::kRowTile * t.r + kRows * h);
-        const size_t ld = (size_t)p.c_size;
         const int mine = c < p.c_size ? cols : 0;  // this lane's valid rows
-        const bool add = WG && p.a.accumulate;
+        // This lane's first result and the bytes from row to row.  A piece's sums go to [slot][row][256
+        // columns].  bf16: even lanes store columns c, c + 1 of two rows of four, odd lanes c - 1, c of the
+        // other two.
+        const int odd = lane & 1;
+        const bool low = p.a.out_bf16 && t.slot < 0;
+        const size_t row0 = (WG ? (size_t)t.e * p.a.d : (size_t)s.seg0) + (size_t)(C::kRowTile * t.r + kRows * h);
+        uint8_t* at;
+        size_t pitch;
+        if (t.slot >= 0) {
+            at = reinterpret_cast<uint8_t*>(p.slots + ((size_t)t.slot * C::kRowTile + kRows * h) * 256 + (c & 255));
+            pitch = 1024;
+        } else if (low) {
+            at = static_cast<uint8_t*>(p.a.out) + ((row0 + 2 * odd) * p.c_size + (c - odd)) * 2;
+            pitch = (size_t)p.c_size * 2;
+        } else {
+            at = static_cast<uint8_t*>(p.a.out) + (row0 * p.c_size + c) * 4;
+            pitch = (size_t)p.c_size * 4;
+        }
+        const bool add = WG && p.a.accumulate && t.slot < 0;
         if (add && s.nkb == 0) continue;  // nothing to add
         uint32_t sum[kRows / 32][32];  // fp32 bits
         if (add) {  // what is there already, read while the MMAs run
-            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine, [&](uint8_t* at, int i, int n) {
+            walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
                 sum[i / 32][i % 32] = n > 0 ? __ldcs(reinterpret_cast<uint32_t*>(at)) : 0u;
             });
         } else if (s.nkb == 0) {
@@ -599,22 +738,20 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
             }
             if ((acc ^= 1) == 0) aphase ^= 1u;
         }
-        if (p.a.out_bf16) {
-            // Four rows at a time: even lanes store columns c, c + 1 of the first two, odd lanes c - 1, c
-            // of the last two.  A lane rounds and packs two rows of its column, so one exchange serves four
-            // rows; the exchanges share a pipe with the stores.
-            const int odd = lane & 1;
+        if (low) {
+            // Four rows at a time.  A lane rounds and packs two rows of its column, so one exchange serves
+            // four rows; the exchanges share a pipe with the stores (decode-sized weight gradient: 405 us with one
+            // for two rows, 354 with one for four).
             const uint32_t lo = odd ? 0x1054u : 0x5410u, hi = odd ? 0x3276u : 0x7632u;  // (mine, other) or (other, mine)
-            walk_rows<kRows, 4>(static_cast<uint8_t*>(p.a.out) + ((row0 + 2 * odd) * ld + (c - odd)) * 2, ld * 8, mine - 2 * odd,
-                                [&](uint8_t* at, int i, int n) {
+            walk_rows<kRows, 4>(at, 4 * pitch, mine - 2 * odd, [&](uint8_t* at, int i, int n) {
                 const uint32_t a = bf16x2(__uint_as_float(sum[i / 32][i % 32]), __uint_as_float(sum[i / 32][i % 32 + 1]));
                 const uint32_t b = bf16x2(__uint_as_float(sum[i / 32][i % 32 + 2]), __uint_as_float(sum[i / 32][i % 32 + 3]));
                 const uint32_t other = __shfl_xor_sync(kFull, odd ? a : b, 1), own = odd ? b : a;
                 if (n > 0) __stcs(reinterpret_cast<uint32_t*>(at), __byte_perm(own, other, lo));
-                if (n > 1) __stcs(reinterpret_cast<uint32_t*>(at + ld * 2), __byte_perm(own, other, hi));
+                if (n > 1) __stcs(reinterpret_cast<uint32_t*>(at + pitch), __byte_perm(own, other, hi));
             });
         } else {
-            walk_rows<kRows, 1>(static_cast<uint8_t*>(p.a.out) + (row0 * ld + c) * 4, ld * 4, mine, [&](uint8_t* at, int i, int n) {
+            walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
                 if (n > 0) __stcs(reinterpret_cast<uint32_t*>(at), sum[i / 32][i % 32]);
             });
         }
@@ -659,6 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
         mbar_init(smem_addr(&ctl->mma_done), 1);
         ctl->abort = 0;
+        ctl->total_kb = 0;
         mbar_fence_init();
     }
     if (warp == 2) {
@@ -683,6 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         // longest reductions first, so that none is left for the end
         for (int e = tid; e < E; e += kGradThreads) {
             const int cnt = off[e + 1] - off[e];
+            if (cnt > 0) atomicAdd(&ctl->total_kb, blocks_of<F>(p, cnt));
             int before = 0, prev = off[0];
             for (int f = 0; f < E; ++f) {
                 const int nx = off[f + 1], n = nx - prev;
@@ -709,8 +848,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     }
     if (bad && tid == 0) report_error(p.a.status, kStDevice, -2, off[E], 0);
     __syncthreads();
-    if (tid == 0) {  // a pair's first tile is its own number: both CTAs know it without a claim
-        ctl->ring[0] = tile_at<F>(p, off, base, order, blockIdx.x / 2);
+    if (tid == 0) {  // a pair's first item is its own number: both CTAs know it without a claim
+        plan_pieces<F>(p, ctl, off, base, order, blockIdx.x == 0 && !bad);
+        if (bad && p.split && blockIdx.x == 0) p.split->count = 0;
+        if (!bad) ctl->ring[0] = item_at<F>(p, ctl, off, base, order, blockIdx.x / 2, leader);
         mbar_arrive(smem_addr(&ctl->sfull[0]));
     }
     tc_fence_before();
@@ -763,13 +904,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     }
 }
 
+// Adds the pieces of the split tiles in their order and stores (or adds) the results: 64 threads a
+// row of 256 columns, four rows a CTA at a time.
+constexpr int kJoinThreads = 256;
+template <Form F>
+__global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitArea* split, const float* slots, void* out,
+                                                                   int c_size, int out_bf16, int accumulate) {
+    constexpr int kRow = Cfg<F>::kRowTile;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = min(__ldcg(&split->count), kMaxSplit);
+    const int c = (threadIdx.x & 63) * 4;
+    for (int u = blockIdx.x; u < count * (kRow / 4); u += gridDim.x) {
+        const SplitTile* t = split->tile + u / (kRow / 4);
+        const int row = u % (kRow / 4) * 4 + (threadIdx.x >> 6);
+        const int col = __ldcg(&t->c0) + c;
+        if (row >= __ldcg(&t->rows) || col >= c_size) continue;  // c_size % 16 == 0
+        const int n = __ldcg(&t->n);
+        const size_t step = (size_t)__ldcg(&t->stride) * kRow * 256;
+        const float* at = slots + ((size_t)__ldcg(&t->slot0) * kRow + row) * 256 + c;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(at + i * step));
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        const size_t o = (size_t)(__ldcg(&t->out_row) + row) * c_size + col;
+        if (out_bf16) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+        } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+            if (accumulate) {
+                const float4 x = *dst;
+                v = make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w);
+            }
+            *dst = v;
+        }
+    }
+}
+
 template <Form F>
 constexpr size_t smem_bytes() {
     return 1024 + (size_t)Cfg<F>::kStages * (kOpBytes + Cfg<F>::kQBytes) + sizeof(GradCtl) + 2 * sizeof(int) * (kMaxE + 1);
 }
 static_assert(smem_bytes<Form::kInput>() <= 232448 && smem_bytes<Form::kNarrow>() <= 232448, "more than 227 KB of shared memory per CTA");
 static_assert(Cfg<Form::kInput>::kStages <= kMaxStages && Cfg<Form::kNarrow>::kStages <= kMaxStages, "stages");
-static_assert(sizeof(GradTile) == 32, "a tile travels as four 8-byte stores");
+static_assert(sizeof(GradTile) == 40, "a tile travels as five 8-byte stores");
 
 // Pairs of CTAs that are resident together on the current device; the kernel's attributes are set once per device.
 template <Form F>
@@ -797,28 +979,56 @@ cudaError_t resident_pairs(int device, int* pairs) {
     return cudaSuccess;
 }
 
-template <Form F>
-cudaError_t launch(GradParams& p, const GroupedGradArgs& a, int device, long long max_tiles, cudaStream_t stream) {
-    p.a = a;
-    p.chunk_kb = a.out_bf16 ? 1 << 30 : kChunkKb;
-    int pairs = 0;
-    const cudaError_t e = resident_pairs<F>(device, &pairs);
-    if (e != cudaSuccess) return e;
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;  // the kernel waits by itself for the one before it, after its own set-up
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(pairs, max_tiles));
-    cfg.blockDim = dim3(kGradThreads);
-    cfg.dynamicSmemBytes = smem_bytes<F>();
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, grouped_grad_kernel<F>, (const GradParams&)p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <Form F>
-cudaError_t dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
+cudaError_t launch(GradParams& p, const GroupedGradArgs& a, bool may_split, int device, int sm_count, long long max_tiles,
+                   cudaStream_t stream) {
+    p.a = a;
+    p.chunk_kb = a.out_bf16 ? 1 << 30 : kChunkKb;
+    int pairs = 0;
+    cudaError_t e = resident_pairs<F>(device, &pairs);
+    if (e != cudaSuccess) return e;
+    if (may_split && a.split) {
+        p.split = static_cast<SplitArea*>(a.split);
+        p.slots = reinterpret_cast<float*>(p.split + 1);
+    } else {
+        pairs = (int)std::min<long long>(pairs, max_tiles);
+    }
+    e = launch_after(grouped_grad_kernel<F>, 2u * pairs, kGradThreads, smem_bytes<F>(), stream, (const GradParams&)p);
+    if (e == cudaSuccess && p.split)
+        e = launch_after(join_pieces_kernel<F>, (unsigned)sm_count, kJoinThreads, 0, stream, (const SplitArea*)p.split,
+                         (const float*)p.slots, a.out, p.c_size, a.out_bf16, a.accumulate);
+    return e;
+}
+
+// Whether an input (weight) gradient of this shape may have fewer tiles than pairs of CTAs and a reduction long
+// enough to be split.
+bool narrow_rows(long long S, int E) { return S <= 64LL * E; }
+bool dgrad_may_split(long long S, int d, int E, int N, int sm_count) {
+    const long long rows = narrow_rows(S, E) ? 64 : 256, tiles = (S + rows - 1) / rows * ((d + 255) / 256);
+    return N > (narrow_rows(S, E) ? Cfg<Form::kNarrow>::kMinSplit : Cfg<Form::kInput>::kMinSplit) * kTileK && tiles < sm_count / 2;
+}
+bool wgrad_may_split(long long S, int d, int N, int sm_count) {
+    const long long tiles = (long long)((d + 255) / 256) * ((N + 255) / 256);
+    return S > Cfg<Form::kWeight>::kMinSplit * kTileK && tiles < sm_count / 2;
+}
+
+template <Form F>
+cudaError_t dgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream) {
     GradParams p = {};
     p.c_size = a.d;
     p.c_tiles = (a.d + 255) / 256;
@@ -826,17 +1036,26 @@ cudaError_t dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
     if (!map_bf16_2d(&p.p_map, a.W, wrows, N, kTileK, kTileM) ||
         !map_bf16_2d(&p.q_map, a.dY, S, N, kTileK, Cfg<F>::kRowTile / 2) || !map_bf16_2d(&p.q_tail, a.dY, S, N, kTileK, 16))
         return cudaErrorInvalidValue;
-    return launch<F>(p, a, device, ((long long)a.S / Cfg<F>::kRowTile + a.E) * p.c_tiles, stream);
+    return launch<F>(p, a, dgrad_may_split(a.S, a.d, a.E, a.N, sm_count), device, sm_count,
+                     ((long long)a.S / Cfg<F>::kRowTile + a.E) * p.c_tiles, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
-    const bool narrow = a.S <= 64LL * a.E;
-    return narrow ? dgrad<Form::kNarrow>(a, device, stream) : dgrad<Form::kInput>(a, device, stream);
+// Workspace bytes for the pieces of split reductions: no piece is longer than a pair's share of all the work, so
+// there are at most two for each pair of CTAs.
+size_t grouped_grad_split_bytes(long long S, int d, int E, int N, int sm_count) {
+    size_t tile = 0;
+    if (dgrad_may_split(S, d, E, N, sm_count)) tile = narrow_rows(S, E) ? 64 : 256;
+    if (wgrad_may_split(S, d, N, sm_count)) tile = 256;
+    return tile == 0 ? 0 : sizeof(SplitArea) + (size_t)sm_count * tile * 256 * 4;
 }
 
-cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStream_t stream) {
+cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream) {
+    return narrow_rows(a.S, a.E) ? dgrad<Form::kNarrow>(a, device, sm_count, stream) : dgrad<Form::kInput>(a, device, sm_count, stream);
+}
+
+cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream) {
     GradParams p = {};
     p.c_size = a.N;
     p.c_tiles = (a.N + 255) / 256;
@@ -851,7 +1070,7 @@ cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStrea
     }
     const long long tiles = (long long)a.E * p.c_tiles * p.r_tiles;
     if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
-    return launch<Form::kWeight>(p, a, device, tiles, stream);
+    return launch<Form::kWeight>(p, a, wgrad_may_split(a.S, a.d, a.N, sm_count), device, sm_count, tiles, stream);
 }
 
 }  // namespace moe

@@ -168,7 +168,7 @@ bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
 bool plan_view(moe_plan_t plan, PlanView* v) {
     if (!plan) return false;
     *v = PlanView{plan->T, plan->d, plan->E, plan->k, plan->N, plan->S, plan->shape.out_dtype == MOE_OUT_BF16,
-                  plan->device, plan->sm_count, plan->timeout_ns};
+                  plan->device, plan->sm_count, plan->timeout_ns, plan->ws.split_off};
     return true;
 }
 }  // namespace moe
@@ -314,6 +314,11 @@ moe_status_t moe_plan(const moe_shape_t* shape, int device, moe_plan_t* plan, si
     off = round_up(off + (size_t)p->max_mtiles * 4, 256);
     p->ws.cflags_off = off;
     off = round_up(off + (size_t)p->max_mtiles * ((p->N + kTileM - 1) / kTileM) * 2 * 4, 256);
+    const size_t split = grouped_grad_split_bytes(p->S, p->d, p->E, p->N, sms);
+    if (split > 0) {
+        p->ws.split_off = off;
+        off = round_up(off + split, 256);
+    }
     p->ws.total = off;
 
     if ((!p->pair && dispatch_gemm_prepare_attributes(p->tile_n, p->stages, p->smem) != cudaSuccess) ||

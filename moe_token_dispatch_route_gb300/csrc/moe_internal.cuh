@@ -49,6 +49,7 @@ struct WorkspaceLayout {
     size_t flags_off;       // u32 [max_mtiles]
     size_t chunk_cnt_off;   // u32 [max_mtiles]
     size_t cflags_off;      // u32 [max_mtiles][ceil(N / 128)][2] combine completion words (epoch-tagged)
+    size_t split_off;       // pieces of the grouped gradients' split reductions; 0: none
     size_t total;
 };
 

@@ -18,6 +18,7 @@ struct PlanView {
     int out_bf16;     // element type of the plan's Y
     int device, sm_count;
     long long timeout_ns;
+    size_t split_off;  // offset in the workspace of the area for split reductions; 0: none
 };
 bool plan_view(moe_plan_t plan, PlanView* v);
 
@@ -103,11 +104,13 @@ struct GroupedGradArgs {
     int accumulate;          // weight gradient, fp32: out += instead of out =
     int32_t* status;
     uint32_t* hdr;           // workspace header
+    void* split;             // workspace of split reductions, or null
     long long timeout_ns;
     int S, d, E, N;
 };
-cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, cudaStream_t stream);
-cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, cudaStream_t stream);
+cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream);
+cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream);
+size_t grouped_grad_split_bytes(long long S, int d, int E, int N, int sm_count);
 
 // bf16 [rows][cols], 128-byte swizzle, and the same as 64-column chunks loaded two at a time
 // (false where cols % 64 != 0)

@@ -37,6 +37,10 @@ moe_status_t launched(cudaError_t e) {
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+void* split_area(const PlanView& v, void* workspace) {
+    return v.split_off ? static_cast<uint8_t*>(workspace) + v.split_off : nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -137,8 +141,8 @@ moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY, const i
     DeviceScope scope(v.device);
     if (!scope.ok) return MOE_ERR_CUDA;
     GroupedGradArgs a{nullptr, dY, W, offsets, dA, da_dtype == MOE_OUT_BF16, 0, dev_status,
-                      static_cast<uint32_t*>(workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
-    return launched(launch_grouped_dgrad(a, v.device, as_stream(stream)));
+                      static_cast<uint32_t*>(workspace), split_area(v, workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
+    return launched(launch_grouped_dgrad(a, v.device, v.sm_count, as_stream(stream)));
 }
 
 moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const uint16_t* dY, const int32_t* offsets,
@@ -159,8 +163,8 @@ moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const ui
     }
     if (!need(A, 16) || !need(dY, 16) || !need(offsets, 4)) return MOE_ERR_INVALID_ARG;
     GroupedGradArgs a{A, dY, nullptr, offsets, dW, dw_dtype == MOE_OUT_BF16, accumulate, dev_status,
-                      static_cast<uint32_t*>(workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
-    return launched(launch_grouped_wgrad(a, v.device, s));
+                      static_cast<uint32_t*>(workspace), split_area(v, workspace), v.timeout_ns, (int)v.S, v.d, v.E, v.N};
+    return launched(launch_grouped_wgrad(a, v.device, v.sm_count, s));
 }
 
 }  // extern "C"

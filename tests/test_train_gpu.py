@@ -441,6 +441,11 @@ GRAD_CASES = [
     ([2000, 5, 0, 300], 80, 592),
     ([701, 1003, 77, 1], 272, 336),   # long odd reductions before another expert's rows
     ([513] * 5 + [449], 528, 512),
+    # few tiles and a long reduction, which is split: over the rows, over N, with other experts beside it
+    ([5000], 64, 80),
+    ([4501, 70, 0, 6213], 80, 144),
+    ([5], 272, 2608),
+    ([130, 0, 3], 528, 4624),
     ([2] * 64, 256, 512),
     ([0] * 31 + [100], 128, 256),
 ]
@@ -579,6 +584,32 @@ def test_grouped_gradients_repeat_share_a_workspace_and_run_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dA, first[0][0]) and torch.equal(dW, first[0][1])
+    assert binding.moe_read_status(st)[0] == 0
+
+
+def test_split_reductions_repeat_and_share_a_workspace():
+    """Pieces of a reduction are added in their order whichever is done first, and offsets that split nothing
+    leave nothing of an earlier call behind."""
+    counts, d, N = [9001, 9, 130], 272, 4624
+    S = sum(counts)
+    plan, ws, st, off, A, dY, W = grad_setup(counts, d, N)
+    even = torch.tensor([0, 3050, 6100, S], dtype=torch.int32, device=DEV)
+    outs = []
+    for _ in range(3):
+        dA, dW = nan((S, d), BF16), nan((3, d, N))
+        binding.moe_grouped_gemm_dgrad(plan, dY, off, W, dA, ws, st)
+        binding.moe_grouped_gemm_wgrad(plan, A, dY, off, dW, ws, st)
+        dW2 = nan((3, d, N))
+        binding.moe_grouped_gemm_wgrad(plan, A, dY, even, dW2, ws, st)
+        torch.cuda.synchronize()
+        outs.append((dA, dW, dW2))
+    for o in outs[1:]:
+        for a, b in zip(outs[0], o):
+            assert torch.equal(a, b)
+    ref, mag = wgrad_ref(counts, A, dY)
+    check(outs[0][1], ref, mag, mma_rounds(max(counts)))
+    ref, mag = wgrad_ref([3050, 3050, S - 6100], A, dY)
+    check(outs[0][2], ref, mag, mma_rounds(3050))
     assert binding.moe_read_status(st)[0] == 0
 
 
