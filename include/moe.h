@@ -447,9 +447,9 @@ MOE_API moe_status_t moe_route_noalloc(moe_plan_t plan, const float* logits,
 
 /*
  * moe_backward_scratch -- bytes of device scratch that moe_layernorm_backward of
- * this plan needs.  The caller allocates it, 256-byte aligned, and fills it
- * with zeros ONCE before the first call, as for moe_plan's workspace.  Calls that
- * share one scratch must be ordered on one stream.  Host only.
+ * this plan needs for dgamma and dbeta.  The caller allocates it, 256-byte
+ * aligned; what it holds does not matter, and nothing is kept in it from call to
+ * call.  Calls that share one scratch must be ordered on one stream.  Host only.
  */
 MOE_API moe_status_t moe_backward_scratch(moe_plan_t plan, size_t* bytes);
 
@@ -484,7 +484,8 @@ MOE_API moe_status_t moe_layernorm(moe_plan_t plan, const void* x, int32_t x_dty
  *   dgamma, dbeta out: fp32 [d], each may be NULL.
  *   scratch in/out: moe_backward_scratch; may be NULL when dgamma and dbeta are.
  *                MOE_ERR_WORKSPACE if it is missing or misaligned.
- * T = 0 writes zeros to dgamma and dbeta.
+ * T = 0 writes zeros to dgamma and dbeta.  Launches one kernel for dx alone and a
+ * second one where dgamma or dbeta is wanted.
  */
 MOE_API moe_status_t moe_layernorm_backward(moe_plan_t plan, const void* dy, int32_t dy_dtype, const void* x,
                                             int32_t x_dtype, const float* gamma, const float* mean,
@@ -553,6 +554,9 @@ MOE_API moe_status_t moe_combine_backward(moe_plan_t plan, const void* dout, int
  *   dA      out: [S][d] of da_dtype, fp32 sums.
  * Workspace and status as for moe_grouped_gemm.  Offsets that are not an
  * ascending list from 0 to S write MOE_ERR_DEVICE to dev_status and nothing to dA.
+ * Launches one kernel, and a second one where the shape has so few output tiles
+ * beside so long a sum that sums may be cut into pieces; these lie in the workspace
+ * (moe_plan's workspace_bytes holds up to 40 MB more for such a shape).
  */
 MOE_API moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY, const int32_t* offsets,
                                             const uint16_t* W, void* dA, int32_t da_dtype, void* workspace,
@@ -567,8 +571,8 @@ MOE_API moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY,
  *   offsets in:  int32 [E+1] from moe_route.
  *   dW      out: [E][d][N] of dw_dtype.  An expert without rows gets zeros.
  *   accumulate in: 1: dW += (fp32 only, MOE_ERR_UNSUPPORTED otherwise); 0: dW =.
- * T = 0 writes zeros (accumulate: nothing).  Workspace, status and invalid
- * offsets as for moe_grouped_gemm_dgrad.
+ * T = 0 writes zeros (accumulate: nothing).  Workspace, status, invalid offsets
+ * and launches as for moe_grouped_gemm_dgrad.
  */
 MOE_API moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, const uint16_t* dY,
                                             const int32_t* offsets, void* dW, int32_t dw_dtype,

@@ -634,9 +634,9 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t
 }
 
 // visit(address, i, rows left) for i = 0, STEP, ... below ROWS, addresses `pitch` bytes apart for each
-// step; n - i rows are left, or STEP where a lane of the warp has all of its rows.  The
-// address is stepped, not multiplied out: 128 products in flight spilled, and the whole epilogue
-// ran at 2.6 TB/s.
+// step.  n of the lane's rows are to be visited: n - i are left, and where every lane of the warp has all of
+// its rows STEP is passed, a constant, so that the visits' tests vanish.  The address is stepped, not multiplied
+// out: 128 products in flight spilled, and the whole epilogue ran at 2.6 TB/s.
 template <int ROWS, int STEP, class Visit>
 __device__ __forceinline__ void walk_rows(uint8_t* at, size_t pitch, int n, Visit visit) {
     constexpr int kAll = STEP == 4 ? ROWS - 2 : ROWS;  // (of four rows a lane stores two)
@@ -1015,9 +1015,12 @@ cudaError_t launch(GradParams& p, const GroupedGradArgs& a, bool may_split, int 
     return e;
 }
 
+// Row tiles of 64 where that is an expert's mean or more: the ten stages in flight read the weights faster (64
+// experts of 2048 x 2048 with 64 rows each: 92 us, 94 in tiles of 256; with 8 rows 86 and 89), and with more rows
+// they are read twice (80 rows: 118 and 96).
+bool narrow_rows(long long S, int E) { return S <= 64LL * E; }
 // Whether an input (weight) gradient of this shape may have fewer tiles than pairs of CTAs and a reduction long
 // enough to be split.
-bool narrow_rows(long long S, int E) { return S <= 64LL * E; }
 bool dgrad_may_split(long long S, int d, int E, int N, int sm_count) {
     const long long rows = narrow_rows(S, E) ? 64 : 256, tiles = (S + rows - 1) / rows * ((d + 255) / 256);
     return N > (narrow_rows(S, E) ? Cfg<Form::kNarrow>::kMinSplit : Cfg<Form::kInput>::kMinSplit) * kTileK && tiles < sm_count / 2;

@@ -364,6 +364,17 @@ def test_combine_backward(T, k, N, y_dtype, dout_dtype):
     check(dw, rw, mw, rounds(N), "dw")
 
 
+@pytest.mark.parametrize("k,N", [(3, 1408), (8, 1040), (11, 528), (1, 2032)])
+@pytest.mark.parametrize("y_dtype,dout_dtype", [(F32, BF16), (BF16, F32)])
+def test_combine_backward_many_tokens(k, N, y_dtype, dout_dtype):
+    """A warp a token, with rows of several passes and more tokens than warps at once."""
+    T = 10 * torch.cuda.get_device_properties(0).multi_processor_count * 8 // 3 + 5
+    dout, Y, w, dest, dY, dw = cb_run(T, k, N, y_dtype, dout_dtype)
+    rY, rw, mw = cb_ref(dout, Y, w, dest)
+    check(dY, rY, rY.abs(), 2, "dY")
+    check(dw, rw, mw, rounds(N), "dw")
+
+
 def test_combine_backward_skips_slots_outside_the_rows():
     T, k, N = 6, 2, 272
     dest = torch.randperm(T * k, generator=_gen(1), device=DEV).to(torch.int32)
