@@ -237,6 +237,14 @@ struct Stage {
     }
 };
 
+// True, once every word of the tile is in a register.  A slot may be handed back only then: a load of shared memory
+// queues behind its warp's stores to global memory, microseconds of them in the epilogue, but an arrival on a
+// barrier does not, and the scheduler's next tile would be read in the slot's place.  (No field but -1
+// is negative, so the words' OR is never the lowest integer.)
+__device__ __forceinline__ bool loaded(const GradTile& t) {
+    return (t.e | t.c | t.r | t.seg0 | t.nkb | t.rows | t.last | t.boxes | t.kbeg | t.slot) != (int)0x80000000;
+}
+
 // Takes the next tile from the ring and hands the slot back to the scheduler in the peer CTA;
 // called by one thread, or (WARP) by all lanes of a warp, which arrives once.
 template <bool WARP>
@@ -246,8 +254,9 @@ __device__ __forceinline__ bool take(GradCtl* ctl, Ring& ring, GradTile& t, cons
     if (WARP) got = __all_sync(kFull, got);
     if (!got) return false;
     t = ctl->ring[ring.slot];
-    if (WARP) __syncwarp();  // every lane has read it
-    if (!WARP || (threadIdx.x & 31) == 0) {
+    bool read = loaded(t);
+    if (WARP) read = __all_sync(kFull, read);
+    if (read && (!WARP || (threadIdx.x & 31) == 0)) {
         const uint32_t se = smem_addr(&ctl->sempty[ring.slot]);
         if (leader) mbar_arrive_remote(mapa_shared(se, sched));
         else mbar_arrive(se);
@@ -580,8 +589,9 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t
         t = ctl->ring[ring.slot];
         const uint32_t taken = mapa_shared(smem_addr(&ctl->sempty[ring.slot]), peer);
         ring.next();
+        const bool read = loaded(t);
         if (t.e < 0 || t.nkb == 0) {
-            mbar_arrive_remote(taken);
+            if (read) mbar_arrive_remote(taken);
             if (t.e < 0) break;
             continue;
         }
@@ -625,7 +635,7 @@ __device__ void mma_role(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t
                 st.next();
             }
             umma_commit_pair_mc(smem_addr(&ctl->tfull[acc]), 0x3);
-            if (kb0 == 0) mbar_arrive_remote(taken);
+            if (kb0 == 0 && read) mbar_arrive_remote(taken);
             if ((acc ^= 1) == 0) aphase ^= 1u;
         }
     }

@@ -598,6 +598,23 @@ def test_grouped_gradients_repeat_share_a_workspace_and_run_in_a_graph():
     assert binding.moe_read_status(st)[0] == 0
 
 
+def test_grouped_wgrad_adds_up_exactly_over_many_calls():
+    """Few rows an expert: the epilogue's loads and stores of the accumulated sums are the whole work, and every
+    role runs as far ahead of it as the rings let it.  Whole numbers: each sum is exact, a tile that is missed, done
+    twice or done with another's rows shows."""
+    counts, d, N, calls = [64, 0, 17, 64] * 12, 2048, 1536, 150
+    plan, ws, st, off, A, dY, _ = grad_setup(counts, d, N)
+    dY.fill_(1)
+    A.copy_((torch.arange(sum(counts), device=DEV) % 3 + 1)[:, None])
+    want = torch.stack([A[r0:r1, 0].double().sum() for _, r0, r1 in segments(counts)])
+    dW = torch.zeros(len(counts), d, N, device=DEV)
+    for i in range(calls):
+        binding.moe_grouped_gemm_wgrad(plan, A, dY, off, dW, ws, st, accumulate=True)
+    assert binding.moe_read_status(st)[0] == 0
+    for e in range(len(counts)):
+        assert (dW[e] == float(want[e]) * calls).all(), e
+
+
 def test_split_reductions_repeat_and_share_a_workspace():
     """Pieces of a reduction are added in their order whichever is done first, and offsets that split nothing
     leave nothing of an earlier call behind."""
