@@ -30,6 +30,7 @@ struct Raw {
     __device__ void load(const void* base, size_t i) { a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i)); }
     __device__ void take(const uint8_t* row, int c) { a = *reinterpret_cast<const uint4*>(row + c * 2); }  // from shared memory
     __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ uint32_t bits() const { return a.x | a.y | a.z | a.w; }
     __device__ float get(int j) const {
         const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
         return j & 1 ? bf16_hi(w) : bf16_lo(w);
@@ -48,6 +49,10 @@ struct Raw<false> {
         b = *reinterpret_cast<const float4*>(row + c * 4 + 16);
     }
     __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ uint32_t bits() const {
+        return __float_as_uint(a.x) | __float_as_uint(a.y) | __float_as_uint(a.z) | __float_as_uint(a.w) |
+               __float_as_uint(b.x) | __float_as_uint(b.y) | __float_as_uint(b.z) | __float_as_uint(b.w);
+    }
     __device__ float get(int j) const {
         return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
     }
@@ -94,6 +99,13 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32], B
 
 struct CtaBarrier {
     __device__ void operator()() const { __syncthreads(); }
+};
+
+// The same, passed once the words that `bits` is made of are in registers: a load of shared memory queues behind
+// global stores, and a barrier alone does not wait for it to be done.
+struct ReadBarrier {
+    uint32_t bits;
+    __device__ void operator()() const { __syncthreads_or(bits == 1u); }
 };
 
 // ------------------------------------------------------------------ forward
@@ -435,8 +447,8 @@ __global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>
             }
         }
         // the two arrays of `red` alternate, so one barrier a row is enough; after it the CTA has
-        // read the slot
-        row_sum<TPR, 2, B::kCta>(s, red[turn], CtaBarrier());
+        // read the slot (the sums need all of x and dy)
+        row_sum<TPR, 2, B::kCta>(s, red[turn], ReadBarrier{res.bits()});
         if (threadIdx.x == 0) fetch(t + B::kStages * step, stage);
         if (mine) {
             const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
