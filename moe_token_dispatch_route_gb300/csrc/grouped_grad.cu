@@ -707,11 +707,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
         const bool add = WG && p.a.accumulate && t.slot < 0;
         if (add && s.nkb == 0) continue;  // nothing to add
         uint32_t sum[kRows / 32][32];  // fp32 bits
-        if (add) {  // what is there already, read while the MMAs run
-            walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
-                sum[i / 32][i % 32] = n > 0 ? __ldcs(reinterpret_cast<uint32_t*>(at)) : 0u;
-            });
-        } else if (s.nkb == 0) {
+        if (s.nkb == 0) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) sum[i / 32][i % 32] = 0u;
         }
@@ -720,7 +716,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
             if (!__all_sync(kFull, ready)) return;
             tc_fence_after();
             const uint32_t base = tmem + (uint32_t)(acc * 256 + kRows * h) + ((uint32_t)(32 * q) << 16);
-            if (kb == 0 && !add) {  // the first sum is loaded where it stays, all of it in flight
+            if (kb == 0) {  // the first sum is loaded where it stays, all of it in flight
 #pragma unroll
                 for (int g = 0; g < kRows / 32; ++g)
                     if (32 * g < cols) tmem_ld_32x32(base + 32 * g, sum[g]);
@@ -759,6 +755,13 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
                 const uint32_t other = __shfl_xor_sync(kFull, odd ? a : b, 1), own = odd ? b : a;
                 if (n > 0) __stcs(reinterpret_cast<uint32_t*>(at), __byte_perm(own, other, lo));
                 if (n > 1) __stcs(reinterpret_cast<uint32_t*>(at + pitch), __byte_perm(own, other, hi));
+            });
+        } else if (add) {
+            // Added in L2, once for each element, so in no order that could change: to read the sums first takes these
+            // warps a round trip a tile (64 experts of 64 rows, 4096 x 1536: 693 us, 596 added in L2; 2048
+            // rows, 4096 x 14336: 1376 and 1321).
+            walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
+                if (n > 0) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at), "f"(__uint_as_float(sum[i / 32][i % 32])) : "memory");
             });
         } else {
             walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
