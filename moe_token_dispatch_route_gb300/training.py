@@ -20,11 +20,11 @@ class MoeTrainLayer:
     """Plans and device buffers of a layer of T tokens of width d, E experts of hidden width F, k
     experts a token; d and F are multiples of 16.  x: fp32 [T, d].  Weights: W_r bf16 [d, E], W1 bf16
     [E, d, 2F] (gate columns, then up), W2 bf16 [E, F, d], gamma and beta fp32 [d]; their gradients
-    are fp32."""
+    are fp32.  `stream`: a torch stream or a raw handle; None is the current one."""
 
     def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0):
         self.T, self.d, self.F, self.E, self.k, self.eps = T, d, F, E, k, eps
-        dev = torch.device("cuda", device)
+        dev = self.device = torch.device("cuda", device)
         S = T * k
         self.up = b.moe_plan(T, d, E, k, 2 * F, route_flags=b.MOE_ROUTE_RENORM, out_dtype=b.MOE_OUT_BF16, device=device)
         self.down = b.moe_plan(T, F, E, k, d, out_dtype=b.MOE_OUT_BF16, device=device)
@@ -45,29 +45,41 @@ class MoeTrainLayer:
         self.dw, self.dy = new(T, k, dtype=_F32), new(T, d, dtype=_F32)
         self.ones = torch.ones(T, k, dtype=_F32, device=dev)
 
+    def _on(self, stream):
+        """Makes `stream` the current one, for the library's calls and for PyTorch's."""
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
+
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None):
+        with self._on(stream):
+            return self._forward(x, gamma, beta, W_r, W1, W2)
+
+    def _forward(self, x, gamma, beta, W_r, W1, W2):
         u, r = self.up, self.bufs
-        b.moe_layernorm(u, x, gamma, beta, self.eps, self.y, self.mean, self.rstd, stream)
-        b.moe_router_logits(u, self.y, W_r, None, self.logits, stream)
-        b.route(u, self.logits, r, stream)
-        b.dispatch_gemm(u, self.y, W1, r, stream)                                  # GU in r.Y
-        b.moe_swiglu_checkpoint(u, r.Y, self.H, self.codes, self.scales, stream)
-        b.moe_grouped_gemm(self.down, self.H, r.offsets, W2, self.Y, self.down_ws, r.status, stream)
-        b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out, stream)
+        b.moe_layernorm(u, x, gamma, beta, self.eps, self.y, self.mean, self.rstd)
+        b.moe_router_logits(u, self.y, W_r, None, self.logits)
+        b.route(u, self.logits, r)
+        b.dispatch_gemm(u, self.y, W1, r)                                          # GU in r.Y
+        b.moe_swiglu_checkpoint(u, r.Y, self.H, self.codes, self.scales)
+        b.moe_grouped_gemm(self.down, self.H, r.offsets, W2, self.Y, self.down_ws, r.status)
+        b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out)
         return self.out.add_(x)
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
         """dout fp32 [T, d].  Writes grads["W1"], ["W2"] (or adds to them), ["W_r"], ["gamma"] and
         ["beta"], fp32, and returns the gradient of x."""
+        with self._on(stream):
+            return self._backward(dout, x, gamma, W_r, W1, W2, grads, accumulate)
+
+    def _backward(self, dout, x, gamma, W_r, W1, W2, grads, accumulate):
         u, dn, r = self.up, self.down, self.bufs
-        b.moe_combine_backward(dn, dout, self.Y, r.topk_w, r.dest, self.dY, self.dw, stream)
-        b.moe_grouped_gemm_dgrad(dn, self.dY, r.offsets, W2, self.dH, self.down_ws, r.status, stream)
+        b.moe_combine_backward(dn, dout, self.Y, r.topk_w, r.dest, self.dY, self.dw)
+        b.moe_grouped_gemm_dgrad(dn, self.dY, r.offsets, W2, self.dH, self.down_ws, r.status)
         dGU = r.Y                                                                  # GU's buffer: its values are in the codes
-        b.moe_swiglu_checkpoint_backward(u, self.dH, self.codes, self.scales, self.H, dGU, stream)
-        b.moe_grouped_gemm_wgrad(dn, self.H, self.dY, r.offsets, grads["W2"], self.down_ws, r.status, accumulate, stream)
-        b.moe_grouped_gemm_wgrad(u, r.recv[0], dGU, r.offsets, grads["W1"], r.workspace, r.status, accumulate, stream)
-        b.moe_grouped_gemm_dgrad(u, dGU, r.offsets, W1, self.dA, r.workspace, r.status, stream)
-        b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy, stream)             # the dispatch's gradient
+        b.moe_swiglu_checkpoint_backward(u, self.dH, self.codes, self.scales, self.H, dGU)
+        b.moe_grouped_gemm_wgrad(dn, self.H, self.dY, r.offsets, grads["W2"], self.down_ws, r.status, accumulate)
+        b.moe_grouped_gemm_wgrad(u, r.recv[0], dGU, r.offsets, grads["W1"], r.workspace, r.status, accumulate)
+        b.moe_grouped_gemm_dgrad(u, dGU, r.offsets, W1, self.dA, r.workspace, r.status)
+        b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy)                     # the dispatch's gradient
         # the gates: softmax over the chosen logits
         w = r.topk_w
         dlogits = torch.zeros_like(self.logits).scatter_(
@@ -76,7 +88,7 @@ class MoeTrainLayer:
         self.dy.addmm_(dlogits, W_r.float().T)
         dx = torch.empty_like(x)
         b.moe_layernorm_backward(u, self.dy, x, gamma, self.mean, self.rstd, dout, dx, grads["gamma"], grads["beta"],
-                                 self.scratch, stream)
+                                 self.scratch)
         return dx
 
     def kept_bytes(self) -> int:

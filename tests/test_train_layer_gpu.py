@@ -76,3 +76,31 @@ def test_training_lowers_the_loss(example):
     # between the passes the up projection's outputs take 1 byte a value and 8 bytes a block pair
     S, F = 512, 208
     assert layer.codes.numel() + layer.scales.numel() * 4 == S * (2 * F + 2 * 2 * 4)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_layer_on_another_stream(example, raw):
+    """The pass waits behind what its stream has to do, PyTorch's operations of it included."""
+    T, d, F, E, k = 200, 256, 208, 8, 2
+    p = {n: v.bfloat16() if n.startswith("W") else v for n, v in example.weights(d, F, E, 3).items()}
+    x, dout = torch.randn(T, d, device="cuda"), torch.randn(T, d, device="cuda")
+    results = []
+    side = torch.cuda.Stream()
+    for s in (None, side):
+        layer = MoeTrainLayer(T, d, F, E, k)
+        grads = {n: torch.full(v.shape, float("nan"), device="cuda") for n, v in p.items()}
+        torch.cuda.synchronize()
+        if s is not None:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(20_000_000)
+        handle = s.cuda_stream if raw and s is not None else s
+        out = layer.forward(x, **p, stream=handle)
+        with torch.cuda.stream(s):
+            out = out.clone()
+            if s is not None:
+                torch.cuda._sleep(20_000_000)
+        dx = layer.backward(dout, x, p["gamma"], p["W_r"], p["W1"], p["W2"], grads, stream=handle)
+        torch.cuda.synchronize()
+        results.append([out, dx] + [grads[n] for n in sorted(grads)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
