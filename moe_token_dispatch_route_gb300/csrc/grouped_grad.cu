@@ -49,15 +49,20 @@ constexpr int kEpiFirst = 4, kEpiWarps = 8;
 constexpr int kBand = 8;       // row tiles per schedule band
 constexpr int kChunkKb = 12;   // k-blocks (of 64) per TMEM sum of an fp32 output
 
-// The three forms of the kernel.  kNarrow is the input gradient for experts of few rows: row tiles
-// of 64, whose smaller Q leaves shared memory for ten stages of loads in flight.
-enum class Form { kInput, kNarrow, kWeight };
+// The forms of the kernel.  kNarrow is the input gradient for experts of few rows: row tiles
+// of 64, whose smaller Q leaves shared memory for ten stages of loads in flight.  The seventh stage of the
+// others fills the shared memory to the last KB, where the offsets of some 250 experts fit beside it: with more
+// experts (the Many forms) there are six.  Stages are what hides the loads' latency (us with seven and six; fp32
+// outputs): 64 experts of 512 rows, 4096 x 1536, input gradient 296 and 306, weight gradient 358 and 371; 8 experts of 2048
+// rows, 4096 x 14336, weight gradient 1212 and 1244 (five: 4% more again, four: 12%).  bf16 weight gradients of few
+// rows lose 2% by the smaller L1.
+enum class Form { kInput, kInputMany, kNarrow, kWeight, kWeightMany };
 template <Form F>
 struct Cfg {
-    static constexpr bool kWeight = F == Form::kWeight;
+    static constexpr bool kWeight = F == Form::kWeight || F == Form::kWeightMany;
     static constexpr int kRowTile = F == Form::kNarrow ? 64 : 256;
     static constexpr int kQBytes = kRowTile / 2 * kTileK * 2;  // one CTA's half of Q
-    static constexpr int kStages = F == Form::kNarrow ? 10 : 6;
+    static constexpr int kStages = F == Form::kNarrow ? 10 : F == Form::kInput || F == Form::kWeight ? 7 : 6;
     static constexpr int kWarpRows = kRowTile / 2;             // output rows of an epilogue warp
     // Splitting a reduction costs about as much as this many k-blocks (a second kernel) and as many
     // more for each piece; reductions of up to kMinSplit blocks stay whole (16 tiles of 41 blocks: 20 us
@@ -88,6 +93,7 @@ struct SplitTile {
     int slot0, n, stride, pad;
 };
 constexpr int kMaxSplit = 256;    // split tiles: at most one for each pair of CTAs
+constexpr int kMaxSplitExperts = 160;  // each has more than a pair's share of all the work: fewer than pairs
 constexpr int kMinPieceKb = 16;   // shortest piece, in k-blocks
 // The split area of a workspace: the number of split tiles, their list, the slots.
 struct SplitArea {
@@ -113,7 +119,7 @@ struct GradCtl {
     // `order` have, expert k's from piece split_base[k] of an output tile on.
     int limit, pieces, split_experts, split_items;
     int total_kb;  // weight gradient: k-blocks of all experts
-    int split_base[kMaxSplit + 1];
+    short split_base[kMaxSplitExperts + 1];
 };
 
 struct GradParams {
@@ -344,13 +350,13 @@ __device__ void plan_pieces(const GradParams& p, GradCtl* ctl, const int* off, c
         const int limit = (int)min((long long)(1 << 30), max((long long)kMinPieceKb, (total + pairs - 1) / pairs));
         ctl->limit = limit;
         int k = 0, run = 0;
-        for (; k < p.a.E && k < kMaxSplit; ++k) {  // most rows first
+        for (; k < p.a.E && k < kMaxSplitExperts; ++k) {  // most rows first
             const int nkb = blocks_of<F>(p, off[order[k] + 1] - off[order[k]]), len = piece_blocks<F>(nkb, limit);
             if (len == nkb) break;
-            ctl->split_base[k] = run;
+            ctl->split_base[k] = (short)run;
             run += (nkb + len - 1) / len;
         }
-        ctl->split_base[k] = run;
+        ctl->split_base[k] = (short)run;
         ctl->split_experts = k;
         ctl->split_items = (int)(run * per_expert);
         split = (int)(k * per_expert);
@@ -528,9 +534,10 @@ __device__ void producer_q(const GradParams& p, GradCtl* ctl, uint8_t* sQ, const
 
 // Warp 3 (weight gradient): zeroes the rows of a last k-block that are not the expert's, up to
 // the end of its last step of 16, in both operands.
+template <Form F>
 __device__ void zero_rows(const GradParams& p, GradCtl* ctl, uint8_t* sP, uint8_t* sQ, const Wait& w,
                           bool leader, uint32_t peer, uint32_t lead) {
-    using C = Cfg<Form::kWeight>;
+    using C = Cfg<F>;
     const int lane = threadIdx.x & 31;
     Ring ring;
     Stage<C::kStages> st;
@@ -771,19 +778,45 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
     }
 }
 
+constexpr uint32_t kSmemMax = 232448;  // 227 KB
+template <Form F>
+__host__ __device__ constexpr uint32_t smem_bytes(int E) {
+    return (uint32_t)(Cfg<F>::kStages * (kOpBytes + Cfg<F>::kQBytes) + (int)sizeof(GradCtl) +
+                      (Cfg<F>::kWeight ? 4 * (E + 1) + 2 * E : 8 * (E + 1)));
+}
+static_assert(smem_bytes<Form::kInputMany>(kMaxE) <= kSmemMax && smem_bytes<Form::kWeightMany>(kMaxE) <= kSmemMax &&
+                  smem_bytes<Form::kNarrow>(kMaxE) <= kSmemMax,
+              "more than 227 KB of shared memory per CTA");
+static_assert(smem_bytes<Form::kInput>(256) <= kSmemMax && smem_bytes<Form::kWeight>(256) <= kSmemMax, "seven stages");
+static_assert(Cfg<Form::kInput>::kStages <= kMaxStages && Cfg<Form::kNarrow>::kStages <= kMaxStages, "stages");
+static_assert(sizeof(GradTile) == 40, "a tile travels as five 8-byte stores");
+
+__device__ __forceinline__ uint32_t dynamic_smem_size() {
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
+}
+
 template <Form F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grouped_grad_kernel(const __grid_constant__ GradParams p) {
     using C = Cfg<F>;
     constexpr bool WG = C::kWeight;
     constexpr int kStages = C::kStages;
+    // The swizzled stages need 1024 bytes' alignment.  Shared memory starts with that, and nothing is left to
+    // align it with, so a start that has not is refused.  (Declared with the alignment, it compiles to a
+    // kernel that takes 10% longer.)
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    uint8_t* sP = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t raw = smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
+    if (pad + smem_bytes<F>(p.a.E) > dynamic_smem_size()) {
+        if (threadIdx.x == 0) report_error(p.a.status, kStDevice, -3, (int)raw, 0);
+        return;
+    }
+    uint8_t* sP = smem_raw + pad;
     uint8_t* sQ = sP + kStages * kOpBytes;
     GradCtl* ctl = reinterpret_cast<GradCtl*>(sQ + kStages * C::kQBytes);
     int* off = reinterpret_cast<int*>(ctl + 1);        // [E+1]
-    int* base = off + kMaxE + 1;                       // [E+1] row tiles before expert e (input gradient)
+    int* base = off + p.a.E + 1;                       // [E+1] row tiles before expert e (input gradient)
     short* order = reinterpret_cast<short*>(base);     // [E] experts, most rows first (weight gradient)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -889,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             } else if (warp == 2) {
                 if (lane == 0) producer_q<F>(p, ctl, sQ, w, leader, sched, lead, rank);
             } else if (WG) {
-                zero_rows(p, ctl, sP, sQ, w, leader, sched, lead);
+                zero_rows<F>(p, ctl, sP, sQ, w, leader, sched, lead);
             }
             __syncwarp();
         }
@@ -958,14 +991,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitAr
     }
 }
 
-template <Form F>
-constexpr size_t smem_bytes() {
-    return 1024 + (size_t)Cfg<F>::kStages * (kOpBytes + Cfg<F>::kQBytes) + sizeof(GradCtl) + 2 * sizeof(int) * (kMaxE + 1);
-}
-static_assert(smem_bytes<Form::kInput>() <= 232448 && smem_bytes<Form::kNarrow>() <= 232448, "more than 227 KB of shared memory per CTA");
-static_assert(Cfg<Form::kInput>::kStages <= kMaxStages && Cfg<Form::kNarrow>::kStages <= kMaxStages, "stages");
-static_assert(sizeof(GradTile) == 40, "a tile travels as five 8-byte stores");
-
 // Pairs of CTAs that are resident together on the current device; the kernel's attributes are set once per device.
 template <Form F>
 cudaError_t resident_pairs(int device, int* pairs) {
@@ -973,7 +998,7 @@ cudaError_t resident_pairs(int device, int* pairs) {
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     *pairs = known[device].load(std::memory_order_acquire);
     if (*pairs > 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(grouped_grad_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<F>());
+    cudaError_t e = cudaFuncSetAttribute(grouped_grad_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
@@ -982,7 +1007,7 @@ cudaError_t resident_pairs(int device, int* pairs) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kGradThreads);
-    cfg.dynamicSmemBytes = smem_bytes<F>();
+    cfg.dynamicSmemBytes = kSmemMax;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(pairs, grouped_grad_kernel<F>, &cfg);
@@ -1021,7 +1046,7 @@ cudaError_t launch(GradParams& p, const GroupedGradArgs& a, bool may_split, int 
     } else {
         pairs = (int)std::min<long long>(pairs, max_tiles);
     }
-    e = launch_after(grouped_grad_kernel<F>, 2u * pairs, kGradThreads, smem_bytes<F>(), stream, (const GradParams&)p);
+    e = launch_after(grouped_grad_kernel<F>, 2u * pairs, kGradThreads, smem_bytes<F>(a.E), stream, (const GradParams&)p);
     if (e == cudaSuccess && p.split)
         e = launch_after(join_pieces_kernel<F>, (unsigned)sm_count, kJoinThreads, 0, stream, (const SplitArea*)p.split,
                          (const float*)p.slots, a.out, p.c_size, a.out_bf16, a.accumulate);
@@ -1068,7 +1093,9 @@ size_t grouped_grad_split_bytes(long long S, int d, int E, int N, int sm_count) 
 }
 
 cudaError_t launch_grouped_dgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream) {
-    return narrow_rows(a.S, a.E) ? dgrad<Form::kNarrow>(a, device, sm_count, stream) : dgrad<Form::kInput>(a, device, sm_count, stream);
+    if (narrow_rows(a.S, a.E)) return dgrad<Form::kNarrow>(a, device, sm_count, stream);
+    return smem_bytes<Form::kInput>(a.E) <= kSmemMax ? dgrad<Form::kInput>(a, device, sm_count, stream)
+                                                     : dgrad<Form::kInputMany>(a, device, sm_count, stream);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, int sm_count, cudaStream_t stream) {
@@ -1086,7 +1113,9 @@ cudaError_t launch_grouped_wgrad(const GroupedGradArgs& a, int device, int sm_co
     }
     const long long tiles = (long long)a.E * p.c_tiles * p.r_tiles;
     if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
-    return launch<Form::kWeight>(p, a, wgrad_may_split(a.S, a.d, a.N, sm_count), device, sm_count, tiles, stream);
+    const bool split = wgrad_may_split(a.S, a.d, a.N, sm_count);
+    return smem_bytes<Form::kWeight>(a.E) <= kSmemMax ? launch<Form::kWeight>(p, a, split, device, sm_count, tiles, stream)
+                                                      : launch<Form::kWeightMany>(p, a, split, device, sm_count, tiles, stream);
 }
 
 }  // namespace moe

@@ -459,6 +459,10 @@ GRAD_CASES = [
     ([130, 0, 3], 528, 4624),
     ([2] * 64, 256, 512),
     ([0] * 31 + [100], 128, 256),
+    # experts whose offsets just fit beside seven stages of loads, and more
+    ([66] * 255 + [400], 48, 80),
+    ([66] * 299 + [700], 272, 80),
+    ([65] * 1023 + [90], 16, 32),
 ]
 
 
