@@ -31,6 +31,11 @@
 // which over a long reduction is a bias (relative error 1e-6 at 1024 products, 1.6e-5 at 14336).
 // So a sum runs in TMEM over 768 products (7e-7) and the epilogue adds these in registers; the two
 // accumulators alternate, so the MMAs do not wait.  bf16 outputs (2e-3 apart) take one sum.
+//
+// Measured.  16384 rows of 8 experts, 4096 x 14336: input gradient bf16 1.12 ms (1.72 PFLOP/s), weight gradient bf16
+// 1.11 and fp32 1.21 ms; after seconds at the power limit 1.29 and (fp32) 1.28.  65536 rows of 64 experts (Zipf),
+// 2048 x 1408: weight gradient fp32 0.30 ms, with its 738 MB of stores.  512 rows of 128 experts, 4096 x 1536: input
+// gradient 203 us, 7.0 TB/s of weights.
 #include <algorithm>
 #include <atomic>
 
