@@ -168,6 +168,7 @@ class Plan:
         self.workspace_bytes = workspace_bytes
         self.shape = shape
         self.device = device
+        self.T, self.d, self.E, self.N, self.S = shape.T, shape.d, shape.E, shape.N, shape.T * shape.k
         info = PlanInfo()
         _check(load_library().moe_plan_info(handle, ctypes.byref(info)), "moe_plan_info")
         self.info = info.as_dict()
@@ -307,12 +308,14 @@ def moe_combine(plan: Plan, Y, topk_w, dest, out, stream=None) -> None:
 _DTYPES = {torch.float32: MOE_OUT_F32, torch.bfloat16: MOE_OUT_BF16}
 
 
-def _arg(call: str, plan: Plan, name: str, t, numel: int, *dtypes, optional: bool = False) -> int | None:
+_F32, _BF16 = torch.float32, torch.bfloat16
+_IS_F32, _IS_BF16, _IS_EITHER, _IS_I32, _IS_I8 = (_F32,), (_BF16,), (_BF16, _F32), (torch.int32,), (torch.int8,)
+
+
+def _arg(call: str, plan: Plan, name: str, t, numel: int, dtypes: tuple) -> int:
     """Device pointer of a dense tensor on the plan's device with `numel` elements and one of
     `dtypes`; the C ABI sees addresses alone, so a tensor it would misread is refused here."""
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{call}: {name} is missing")
     if t.dtype in dtypes and t.numel() == numel and t.get_device() == plan.device and t.is_contiguous():
         return t.data_ptr()
@@ -324,7 +327,12 @@ def _arg(call: str, plan: Plan, name: str, t, numel: int, *dtypes, optional: boo
     raise ValueError(f"{call}: {name} is on {t.device}, the plan on cuda:{plan.device}")
 
 
-_F32, _BF16 = torch.float32, torch.bfloat16
+def _opt(call: str, plan: Plan, name: str, t, numel: int, dtypes: tuple) -> int | None:
+    if t is None:
+        return None
+    if t.dtype in dtypes and t.numel() == numel and t.get_device() == plan.device and t.is_contiguous():
+        return t.data_ptr()
+    return _arg(call, plan, name, t, numel, dtypes)
 
 
 def backward_scratch(plan: Plan, device=None) -> torch.Tensor:
@@ -337,31 +345,33 @@ def backward_scratch(plan: Plan, device=None) -> torch.Tensor:
 def moe_layernorm(plan: Plan, x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
     """y = (x - mean) rstd gamma + beta over the plan's T rows of width d; gamma, beta, mean and
     rstd may be None."""
-    s, c = plan.shape, "moe_layernorm"
-    n = s.T * s.d
+    c = "moe_layernorm"
+    d, T = plan.d, plan.T
+    n = T * d
     _check(load_library().moe_layernorm(
-        plan.handle, _arg(c, plan, "x", x, n, _BF16, _F32), _DTYPES[x.dtype],
-        _arg(c, plan, "gamma", gamma, s.d, _F32, optional=True), _arg(c, plan, "beta", beta, s.d, _F32, optional=True),
-        eps, _arg(c, plan, "y", y, n, _BF16), _arg(c, plan, "mean", mean, s.T, _F32, optional=True),
-        _arg(c, plan, "rstd", rstd, s.T, _F32, optional=True), _stream(stream, plan.device)), c)
+        plan.handle, _arg(c, plan, "x", x, n, _IS_EITHER), _DTYPES[x.dtype],
+        _opt(c, plan, "gamma", gamma, d, _IS_F32), _opt(c, plan, "beta", beta, d, _IS_F32),
+        eps, _arg(c, plan, "y", y, n, _IS_BF16), _opt(c, plan, "mean", mean, T, _IS_F32),
+        _opt(c, plan, "rstd", rstd, T, _IS_F32), _stream(stream, plan.device)), c)
 
 
 def moe_layernorm_backward(plan: Plan, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, scratch,
                            stream=None) -> None:
     """Gradient of moe_layernorm; dres (added to dx), gamma, dgamma and dbeta may be None."""
-    s, c = plan.shape, "moe_layernorm_backward"
-    n = s.T * s.d
-    px = _arg(c, plan, "x", x, n, _BF16, _F32)
+    c = "moe_layernorm_backward"
+    d, T = plan.d, plan.T
+    n = T * d
+    px = _arg(c, plan, "x", x, n, _IS_EITHER)
     _check(load_library().moe_layernorm_backward(
-        plan.handle, _arg(c, plan, "dy", dy, n, _BF16, _F32), _DTYPES[dy.dtype], px, _DTYPES[x.dtype],
-        _arg(c, plan, "gamma", gamma, s.d, _F32, optional=True), _arg(c, plan, "mean", mean, s.T, _F32),
-        _arg(c, plan, "rstd", rstd, s.T, _F32), _arg(c, plan, "dres", dres, n, x.dtype, optional=True),
-        _arg(c, plan, "dx", dx, n, x.dtype), _arg(c, plan, "dgamma", dgamma, s.d, _F32, optional=True),
-        _arg(c, plan, "dbeta", dbeta, s.d, _F32, optional=True), _ptr(scratch), _stream(stream, plan.device)), c)
+        plan.handle, _arg(c, plan, "dy", dy, n, _IS_EITHER), _DTYPES[dy.dtype], px, _DTYPES[x.dtype],
+        _opt(c, plan, "gamma", gamma, d, _IS_F32), _arg(c, plan, "mean", mean, T, _IS_F32),
+        _arg(c, plan, "rstd", rstd, T, _IS_F32), _opt(c, plan, "dres", dres, n, (x.dtype,)),
+        _arg(c, plan, "dx", dx, n, (x.dtype,)), _opt(c, plan, "dgamma", dgamma, d, _IS_F32),
+        _opt(c, plan, "dbeta", dbeta, d, _IS_F32), _ptr(scratch), _stream(stream, plan.device)), c)
 
 
 def _out_dtype(plan: Plan):
-    return _BF16 if plan.shape.out_dtype == MOE_OUT_BF16 else _F32
+    return _IS_BF16 if plan.shape.out_dtype == MOE_OUT_BF16 else _IS_F32
 
 
 def checkpoint_blocks(F: int) -> int:
@@ -372,56 +382,56 @@ def checkpoint_blocks(F: int) -> int:
 def moe_swiglu_checkpoint(plan: Plan, GU, H, codes, scales, stream=None) -> None:
     """H = silu(gate) * up (H may be None), and GU in 8 bits: int8 codes [S][2F] and fp32 scales
     [S][2 * checkpoint_blocks(F)]."""
-    s, c = plan.shape, "moe_swiglu_checkpoint"
-    S, F = s.T * s.k, s.N // 2
+    c = "moe_swiglu_checkpoint"
+    S, F = plan.S, plan.N // 2
     _check(load_library().moe_swiglu_checkpoint(
         plan.handle, _arg(c, plan, "GU", GU, S * 2 * F, _out_dtype(plan)),
-        _arg(c, plan, "H", H, S * F, _BF16, optional=True), _arg(c, plan, "codes", codes, S * 2 * F, torch.int8),
-        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _F32), _stream(stream, plan.device)), c)
+        _opt(c, plan, "H", H, S * F, _IS_BF16), _arg(c, plan, "codes", codes, S * 2 * F, _IS_I8),
+        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _IS_F32), _stream(stream, plan.device)), c)
 
 
 def moe_swiglu_checkpoint_backward(plan: Plan, dH, codes, scales, H, dGU, stream=None) -> None:
     """dGU from dH and the 8-bit checkpoint, and the activation H again (H may be None)."""
-    s, c = plan.shape, "moe_swiglu_checkpoint_backward"
-    S, F = s.T * s.k, s.N // 2
+    c = "moe_swiglu_checkpoint_backward"
+    S, F = plan.S, plan.N // 2
     _check(load_library().moe_swiglu_checkpoint_backward(
-        plan.handle, _arg(c, plan, "dH", dH, S * F, _BF16, _F32), _DTYPES[dH.dtype],
-        _arg(c, plan, "codes", codes, S * 2 * F, torch.int8),
-        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _F32),
-        _arg(c, plan, "H", H, S * F, _BF16, optional=True), _arg(c, plan, "dGU", dGU, S * 2 * F, _BF16),
+        plan.handle, _arg(c, plan, "dH", dH, S * F, _IS_EITHER), _DTYPES[dH.dtype],
+        _arg(c, plan, "codes", codes, S * 2 * F, _IS_I8),
+        _arg(c, plan, "scales", scales, S * 2 * checkpoint_blocks(F), _IS_F32),
+        _opt(c, plan, "H", H, S * F, _IS_BF16), _arg(c, plan, "dGU", dGU, S * 2 * F, _IS_BF16),
         _stream(stream, plan.device)), c)
 
 
 def moe_combine_backward(plan: Plan, dout, Y, topk_w, dest, dY, dtopk_w, stream=None) -> None:
     """dY[dest[t,j]] = topk_w[t,j] dout[t] and dtopk_w[t,j] = <dout[t], Y[dest[t,j]]>."""
-    s, c = plan.shape, "moe_combine_backward"
-    S = s.T * s.k
+    c = "moe_combine_backward"
+    S, N = plan.S, plan.N
     _check(load_library().moe_combine_backward(
-        plan.handle, _arg(c, plan, "dout", dout, s.T * s.N, _BF16, _F32), _DTYPES[dout.dtype],
-        _arg(c, plan, "Y", Y, S * s.N, _out_dtype(plan)), _arg(c, plan, "topk_w", topk_w, S, _F32),
-        _arg(c, plan, "dest", dest, S, torch.int32), _arg(c, plan, "dY", dY, S * s.N, _BF16),
-        _arg(c, plan, "dtopk_w", dtopk_w, S, _F32), _stream(stream, plan.device)), c)
+        plan.handle, _arg(c, plan, "dout", dout, plan.T * N, _IS_EITHER), _DTYPES[dout.dtype],
+        _arg(c, plan, "Y", Y, S * N, _out_dtype(plan)), _arg(c, plan, "topk_w", topk_w, S, _IS_F32),
+        _arg(c, plan, "dest", dest, S, _IS_I32), _arg(c, plan, "dY", dY, S * N, _IS_BF16),
+        _arg(c, plan, "dtopk_w", dtopk_w, S, _IS_F32), _stream(stream, plan.device)), c)
 
 
 def moe_grouped_gemm_dgrad(plan: Plan, dY, offsets, W, dA, workspace, dev_status, stream=None) -> None:
     """dA[i] = dY[i] W[e(i)]^T, fp32 or bf16 by dA's type."""
-    s, c = plan.shape, "moe_grouped_gemm_dgrad"
-    S = s.T * s.k
+    c = "moe_grouped_gemm_dgrad"
+    S, N = plan.S, plan.N
     _check(load_library().moe_grouped_gemm_dgrad(
-        plan.handle, _arg(c, plan, "dY", dY, S * s.N, _BF16), _arg(c, plan, "offsets", offsets, s.E + 1, torch.int32),
-        _arg(c, plan, "W", W, s.E * s.d * s.N, _BF16), _arg(c, plan, "dA", dA, S * s.d, _BF16, _F32),
+        plan.handle, _arg(c, plan, "dY", dY, S * N, _IS_BF16), _arg(c, plan, "offsets", offsets, plan.E + 1, _IS_I32),
+        _arg(c, plan, "W", W, plan.E * plan.d * N, _IS_BF16), _arg(c, plan, "dA", dA, S * plan.d, _IS_EITHER),
         _DTYPES[dA.dtype], _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
 
 
 def moe_grouped_gemm_wgrad(plan: Plan, A, dY, offsets, dW, workspace, dev_status, accumulate: bool = False,
                            stream=None) -> None:
     """dW[e] = A_e^T dY_e (accumulate: added to dW, fp32), fp32 or bf16 by dW's type."""
-    s, c = plan.shape, "moe_grouped_gemm_wgrad"
-    S = s.T * s.k
+    c = "moe_grouped_gemm_wgrad"
+    S, N = plan.S, plan.N
     _check(load_library().moe_grouped_gemm_wgrad(
-        plan.handle, _arg(c, plan, "A", A, S * s.d, _BF16), _arg(c, plan, "dY", dY, S * s.N, _BF16),
-        _arg(c, plan, "offsets", offsets, s.E + 1, torch.int32),
-        _arg(c, plan, "dW", dW, s.E * s.d * s.N, _BF16, _F32), _DTYPES[dW.dtype], int(accumulate),
+        plan.handle, _arg(c, plan, "A", A, S * plan.d, _IS_BF16), _arg(c, plan, "dY", dY, S * N, _IS_BF16),
+        _arg(c, plan, "offsets", offsets, plan.E + 1, _IS_I32),
+        _arg(c, plan, "dW", dW, plan.E * plan.d * N, _IS_EITHER), _DTYPES[dW.dtype], int(accumulate),
         _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
 
 
