@@ -87,13 +87,14 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[CTA / 32], B
 #pragma unroll
             for (int i = 0; i < N; ++i) red[i][warp] = v[i];
         barrier();
+        // a lane a warp, not every lane all warps: those loads alone were 15% of a row of 1024 threads (8192 x 8192
+        // bf16, backward: 127 us, 109 so)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = 0.f;
+        for (int i = 0; i < N; ++i) v[i] = red[i][first + (threadIdx.x & 31) % kWarps];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[i][first + w];
-            v[i] = s;
-        }
+        for (int o = kWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
     }
 }
 
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
 // memory: one thread copies whole rows of x, dy and dres (cp.async.bulk; 192 KB an SM, two to four
 // rows ahead), so a row's round trip is behind the arithmetic of the rows before it.
 // Measured, with the joining kernel, against the rows loaded into registers when they are needed: 8192 x 4096 bf16
-// x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86; 20000 x 992 the other way, 33 -> 43.
+// x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86 (60 and 87 with row_sum as it is now); 20000 x 992 the other way, 33 -> 43.
 template <bool DYB, bool XB, int TPR>
 struct Ahead {
     static constexpr int kCta = TPR;

@@ -151,7 +151,7 @@ def ln_back_run(dy, x, gamma, dres, in_place=False):
     return plan, scratch, mean, rstd, dx, dg, db
 
 
-@pytest.mark.parametrize("T,d", LN_SHAPES + [(20000, 48), (5000, 2064)])
+@pytest.mark.parametrize("T,d", LN_SHAPES + [(20000, 48), (5000, 2064), (1500, 4112), (1501, 8192), (600, 12304), (300, 32768)])
 @pytest.mark.parametrize("x_dtype,dy_dtype", [(F32, F32), (BF16, F32), (BF16, BF16), (F32, BF16)])
 def test_layernorm_backward(T, d, x_dtype, dy_dtype):
     x = (randn((T, d), 11) + randn((T, 1), 12)).to(x_dtype)
