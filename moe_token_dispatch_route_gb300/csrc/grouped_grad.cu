@@ -124,6 +124,7 @@ struct GradCtl {
     // `order` have, expert k's from piece split_base[k] of an output tile on.
     int limit, pieces, split_experts, split_items;
     int total_kb;  // weight gradient: k-blocks of all experts
+    int one_round;  // no more items than pairs: nothing is claimed, and the counters stay as they are
     short split_base[kMaxSplitExperts + 1];
 };
 
@@ -209,7 +210,8 @@ __device__ void fill_shape(const GradParams& p, const int* off, GradTile& t, int
     t.nkb = min(len, nkb - t.kbeg);
     const int last = t.kbeg + t.nkb == nkb ? K - kTileK * (nkb - 1) : kTileK;
     const int ksteps = (last + kUmmaK - 1) / kUmmaK;
-    const int fix = (WG && (last & (kUmmaK - 1))) ? last : 0;
+    // (rows past the last one of all are read as zeros)
+    const int fix = (WG && (last & (kUmmaK - 1)) && t.seg0 + cnt < p.a.S) ? last : 0;
     t.last = ksteps | fix << 8 | half << 16;
     t.boxes = 0;
     if (WG) {
@@ -346,9 +348,10 @@ __device__ void plan_pieces(const GradParams& p, GradCtl* ctl, const int* off, c
     ctl->limit = 1 << 30;
     ctl->pieces = 1;
     ctl->split_experts = ctl->split_items = 0;
-    if (!p.split) return;
     const int pairs = (int)(gridDim.x / 2);
     const long long per_expert = (long long)p.c_tiles * p.r_tiles;
+    ctl->one_round = (WG ? p.a.E * per_expert : (long long)base[p.a.E] * p.c_tiles) <= pairs;
+    if (!p.split) return;
     int split = 0;
     if (WG) {
         const long long total = ctl->total_kb * per_expert;
@@ -365,6 +368,7 @@ __device__ void plan_pieces(const GradParams& p, GradCtl* ctl, const int* off, c
         ctl->split_experts = k;
         ctl->split_items = (int)(run * per_expert);
         split = (int)(k * per_expert);
+        ctl->one_round = (p.a.E - k) * per_expert + ctl->split_items <= pairs;
     } else {
         // all tiles have the same reduction: the number of pieces whose rounds of pairs end first
         const int nkb = blocks_of<F>(p, 0), tiles = base[p.a.E] * p.c_tiles;
@@ -379,6 +383,7 @@ __device__ void plan_pieces(const GradParams& p, GradCtl* ctl, const int* off, c
         const int len = piece_blocks<F>(nkb, ctl->limit);
         ctl->pieces = (nkb + len - 1) / len;
         if (ctl->pieces > 1) split = tiles;
+        ctl->one_round = (long long)tiles * ctl->pieces <= pairs;
     }
     if (write) p.split->count = split;
 }
@@ -394,7 +399,8 @@ __device__ void scheduler(const GradParams& p, GradCtl* ctl, const int* off, con
     ring.next();  // the first item was put into both rings before the roles began
     while (more) {
         if (!bar_wait(smem_addr(&ctl->sempty[ring.slot]), ring.phase ^ 1u, w, 51)) return;
-        const GradTile t = item_at<F>(p, ctl, off, base, order, pairs + atomicAdd(p.a.hdr + kHdrTileCtr, 1u), true);
+        const uint32_t next = ctl->one_round ? 0u : atomicAdd(p.a.hdr + kHdrTileCtr, 1u);
+        const GradTile t = item_at<F>(p, ctl, off, base, order, pairs + next, true);
         ctl->ring[ring.slot] = t;
         const uint32_t dst = mapa_shared(smem_addr(&ctl->ring[ring.slot]), lead);
         const uint32_t bar = mapa_shared(smem_addr(&ctl->sfull[ring.slot]), lead);
@@ -943,7 +949,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
-    if (tid == 0) {
+    // (the wait for the last claim's return, 0.7 us, is what a small product's end would otherwise be)
+    if (tid == 0 && !ctl->one_round) {
         __threadfence();
         const uint32_t prev = atomicAdd(p.a.hdr + kHdrDoneCtr, 1u);
         if (prev == gridDim.x - 1) {  // every CTA has finished with the counters
