@@ -15,8 +15,8 @@
 // Both kernels are bound by HBM, and close to it by their instructions.  A thread takes 8 columns of the gate and the
 // same 8 of the up half; the 16 threads of a block find its amax by shuffles.  The row and block of a
 // thread's next unit are stepped, not divided out.
-// bf16, S = 16384, F = 14336: forward 308 us, 6.2 TB/s (0.91 of a plain copy's rate); backward 365 us, 6.5 TB/s (0.95).
-// S = 65536, F = 1408: forward 127 us, both 272 us.
+// bf16, S = 16384, F = 14336: forward 305 us, 6.2 TB/s (0.92 of a plain copy's rate); backward 365 us, 6.5 TB/s (0.95).
+// S = 65536, F = 1408: forward 124 us, both 270 us.
 #include <algorithm>
 
 #include "train.cuh"
@@ -224,11 +224,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluC
     }
 }
 
-// threads of a launch: `per_sm` CTAs on every SM, fewer where there is less to do
+// threads of a launch: four CTAs on every SM of bf16 inputs, three of fp32, fewer where there is less to do.  More loads
+// in flight are slower, not faster (forward, S = 16384, F = 14336, us: bf16 333 with three, 305 with four, 330 with five
+// resident; fp32 468 with two, 428 with three, 451 with four, 511 with five).
 template <class Kernel, class Args>
-cudaError_t go(Kernel kernel, const Args& a, long long threads, int sm_count, cudaStream_t stream) {
+cudaError_t go(Kernel kernel, const Args& a, long long threads, bool bf16, int sm_count, cudaStream_t stream) {
     const long long ctas = (threads + kThreads - 1) / kThreads;
-    kernel<<<(int)std::min<long long>(ctas, (long long)sm_count * 8), kThreads, 0, stream>>>(a);
+    kernel<<<(int)std::min<long long>(ctas, (long long)sm_count * (bf16 ? 4 : 3)), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -236,14 +238,14 @@ cudaError_t go(Kernel kernel, const Args& a, long long threads, int sm_count, cu
 
 cudaError_t launch_swiglu_checkpoint(const SwigluCkptArgs& a, int sm_count, cudaStream_t stream) {
     const long long threads = a.S * ckpt_blocks(a.F) * kLanes;
-    return a.gu_bf16 ? go(swiglu_checkpoint_kernel<true>, a, threads, sm_count, stream)
-                     : go(swiglu_checkpoint_kernel<false>, a, threads, sm_count, stream);
+    return a.gu_bf16 ? go(swiglu_checkpoint_kernel<true>, a, threads, true, sm_count, stream)
+                     : go(swiglu_checkpoint_kernel<false>, a, threads, false, sm_count, stream);
 }
 
 cudaError_t launch_swiglu_checkpoint_backward(const SwigluCkptBackwardArgs& a, int sm_count, cudaStream_t stream) {
     const long long threads = a.S * (a.F / 8);
-    return a.dh_bf16 ? go(swiglu_backward_kernel<true>, a, threads, sm_count, stream)
-                     : go(swiglu_backward_kernel<false>, a, threads, sm_count, stream);
+    return a.dh_bf16 ? go(swiglu_backward_kernel<true>, a, threads, true, sm_count, stream)
+                     : go(swiglu_backward_kernel<false>, a, threads, false, sm_count, stream);
 }
 
 }  // namespace moe
