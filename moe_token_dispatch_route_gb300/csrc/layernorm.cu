@@ -343,10 +343,11 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
 }
 
 // 1024 < d <= 8192: a CTA holds one row, the same way, and its next rows are on their way in shared
-// memory: one thread copies whole rows of x, dy and dres (cp.async.bulk; 192 KB an SM, two to four
-// rows ahead), so a row's round trip is behind the arithmetic of the rows before it.
+// memory: one thread copies whole rows of x, dy and dres (cp.async.bulk, two rows ahead), so a row's
+// round trip is behind the arithmetic of the rows before it.
 // Measured, with the joining kernel, against the rows loaded into registers when they are needed: 8192 x 4096 bf16
-// x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86 (60 and 87 with row_sum as it is now); 20000 x 992 the other way, 33 -> 43.
+// x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86; 20000 x 992 the other way, 33 -> 43.  More rows ahead are slower: 8192 x
+// 4096 bf16 54 us with two, 54.5 with three, 56 with four (fp32 dy 59 with two, 60 with three).
 template <bool DYB, bool XB, int TPR>
 struct Ahead {
     static constexpr int kCta = TPR;
@@ -354,9 +355,8 @@ struct Ahead {
     static constexpr int kCols = TPR * 8;
     static constexpr int kXBytes = kCols * (XB ? 2 : 4), kDBytes = kCols * (DYB ? 2 : 4);
     static constexpr int kSlot = 2 * kXBytes + kDBytes;  // x, dy, dres of one row
-    static constexpr int kStages = 24576 / (kSlot / TPR * 128);  // 192 bytes a thread
+    static constexpr int kStages = 2;
     static constexpr size_t kSmem = (size_t)kStages * kSlot;
-    static_assert(kStages >= 2, "rows ahead");
 };
 
 __device__ __forceinline__ void copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
