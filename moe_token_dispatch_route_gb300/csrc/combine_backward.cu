@@ -48,6 +48,7 @@ struct Row8<false> {
 // registers are what limits the CTAs of an SM.
 template <bool DB, bool YB, int GROUP, int KMAX>
 __global__ void __launch_bounds__(kThreads, KMAX == 8 ? (YB ? 3 : 2) : 4) combine_backward_kernel(const CombineBackwardArgs a) {
+    wait_for_kernel_before();
     __shared__ float red[2][KMAX][kThreads / 32];
     const int sub = threadIdx.x % GROUP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kTokens = kThreads / GROUP;
@@ -108,12 +109,13 @@ __global__ void __launch_bounds__(kThreads, KMAX == 8 ? (YB ? 3 : 2) : 4) combin
 }
 
 template <bool DB, bool YB, int GROUP, int KMAX>
-void go(const CombineBackwardArgs& a, int sm_count, cudaStream_t stream) {
+cudaError_t go(const CombineBackwardArgs& a, int sm_count, cudaStream_t stream) {
     constexpr int kTokens = kThreads / GROUP;
     // 32 CTAs an SM, of few tokens each, rather than as many as are resident: 8192 tokens, k = 8, N = 4096, fp32
     // 251 us, 268 with those
     const long long ctas = ((long long)a.T + kTokens - 1) / kTokens;
-    combine_backward_kernel<DB, YB, GROUP, KMAX><<<(int)std::min<long long>(ctas, (long long)sm_count * 32), kThreads, 0, stream>>>(a);
+    return launch_after(combine_backward_kernel<DB, YB, GROUP, KMAX>, (unsigned)std::min<long long>(ctas, (long long)sm_count * 32), kThreads, 0,
+                        stream, a);
 }
 
 template <bool DB, bool YB>
@@ -123,15 +125,13 @@ cudaError_t launch(const CombineBackwardArgs& a, int sm_count, cudaStream_t stre
     // 1024 66 and 57, 1408 82 and 78; 2048 with 8192 tokens 56 and 57), and slower by its passes over the row before
     // (333 tokens, k = 8, N = 1024: 6.7 and 9.2; N = 512, k = 4: 7.1 and 6.9).
     if (a.N <= 512 || (a.N < 2048 && a.T > 8 * sm_count)) {
-        if (a.k <= 2) go<DB, YB, 32, 2>(a, sm_count, stream);
-        else if (a.k <= 4) go<DB, YB, 32, 4>(a, sm_count, stream);
-        else go<DB, YB, 32, 8>(a, sm_count, stream);
-    } else {
-        if (a.k <= 2) go<DB, YB, 256, 2>(a, sm_count, stream);
-        else if (a.k <= 4) go<DB, YB, 256, 4>(a, sm_count, stream);
-        else go<DB, YB, 256, 8>(a, sm_count, stream);
+        if (a.k <= 2) return go<DB, YB, 32, 2>(a, sm_count, stream);
+        if (a.k <= 4) return go<DB, YB, 32, 4>(a, sm_count, stream);
+        return go<DB, YB, 32, 8>(a, sm_count, stream);
     }
-    return cudaGetLastError();
+    if (a.k <= 2) return go<DB, YB, 256, 2>(a, sm_count, stream);
+    if (a.k <= 4) return go<DB, YB, 256, 4>(a, sm_count, stream);
+    return go<DB, YB, 256, 8>(a, sm_count, stream);
 }
 
 }  // namespace

@@ -864,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         tma_prefetch_map(&p.q_map);
     }
     // what is above runs beside the end of the kernel before this one in the stream
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_kernel_before();
     // offsets have to ascend from 0 to S: they bound every access
     int bad = 0;
     for (int e = tid; e <= E; e += kGradThreads) {
@@ -969,7 +969,7 @@ template <Form F>
 __global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitArea* split, const float* slots, void* out,
                                                                    int c_size, int out_bf16, int accumulate) {
     constexpr int kRow = Cfg<F>::kRowTile;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_kernel_before();
     const int count = min(__ldcg(&split->count), kMaxSplit);
     const int c = (threadIdx.x & 63) * 4;
     for (int u = blockIdx.x; u < count * (kRow / 4); u += gridDim.x) {
@@ -1027,21 +1027,6 @@ cudaError_t resident_pairs(int device, int* pairs) {
     if (*pairs < 1) return cudaErrorLaunchOutOfResources;
     known[device].store(*pairs, std::memory_order_release);
     return cudaSuccess;
-}
-
-template <class Kernel, class... Args>
-cudaError_t launch_after(Kernel kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at;  // the kernel waits by itself for the one before it, after its own set-up
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <Form F>

@@ -122,6 +122,7 @@ __host__ __device__ constexpr int forward_ctas(int cta, bool xb, int rows) {
 // rows, and R rows share each barrier (8192 x 4096: bf16 30 us with one row, 27 with two; fp32 36 and 33).
 template <bool XB, int TPR, int VPT, int R>
 __global__ void __launch_bounds__(cta_threads(TPR, 128), forward_ctas(cta_threads(TPR, 128), XB, R)) layernorm_kernel(const LayernormArgs a) {
+    wait_for_kernel_before();
     constexpr int kCta = cta_threads(TPR, 128), kRows = kCta / TPR * R;
     __shared__ float red_m[R][kCta / 32], red_v[R][kCta / 32];
     const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
     const int tid = threadIdx.x, sub = tid % TPR, group = tid / TPR, c = sub * 8;
     const float inv_d = 1.f / (float)a.d;
     const bool mine = c < a.d;  // this thread's columns exist
+    wait_for_kernel_before();
     float dg[8], db[8], gamma[8];
     weights8(mine ? a.gamma : nullptr, c, 1.f, gamma);
 #pragma unroll
@@ -405,6 +407,9 @@ __global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>
         for (int s = 0; s < B::kStages; ++s)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * s) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_kernel_before();
+    if (threadIdx.x == 0) {
         for (int s = 0; s < B::kStages; ++s) fetch(first + s * step, s);
     }
     float dg[8], db[8], gamma[8];
@@ -477,6 +482,7 @@ constexpr size_t kTallSmem = (size_t)kTall * 2 * 8 * 2 * 4;
 
 template <bool DYB, bool XB>
 __global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const LayernormBackwardArgs a) {
+    wait_for_kernel_before();
     constexpr int VPT = 2;
     __shared__ float red[2][2][kTall / 32];
     extern __shared__ float4 sums4[];
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kJoin) layernorm_join_kernel(const float* part
     __shared__ float4 sums[kJoin / 32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 7;
     const int c = blockIdx.x * 32 + q * 4;  // 2 d is a multiple of 32
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_kernel_before();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 5
     for (int p = warp * 4 + (lane >> 3); p < parts; p += kJoin / 8) {
@@ -688,7 +694,7 @@ void forward_rows(const LayernormArgs& a, int sm_count, cudaStream_t s) {
     auto go = [&](auto tpr) {
         constexpr int kTpr = decltype(tpr)::value, kCta = cta_threads(kTpr, 128), kRows = kCta / kTpr * R;
         const int grid = std::min((a.T + kRows - 1) / kRows, sm_count * (2048 / kCta));
-        layernorm_kernel<XB, kTpr, 4, R><<<grid, kCta, 0, s>>>(a);
+        launch_after(layernorm_kernel<XB, kTpr, 4, R>, grid, kCta, 0, s, a);  // (an error is seen below)
     };
     switch (row_threads(a.d, 4)) {
         case 8: go(std::integral_constant<int, 8>()); break;
@@ -728,16 +734,7 @@ int backward_parts(int T, int d, int sm_count) {
 }
 
 cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * a.d / 32);
-    cfg.blockDim = dim3(kJoin);
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layernorm_join_kernel, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
+    return launch_after(layernorm_join_kernel, 2 * a.d / 32, kJoin, 0, s, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
 }
 
 // Launches a kernel whose shared memory may be over the default limit of 48 KB, the static part included;
@@ -751,8 +748,7 @@ cudaError_t launch_big(Kernel kernel, const LayernormBackwardArgs& a, int grid, 
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    kernel<<<grid, cta, smem, s>>>(a);
-    return cudaSuccess;
+    return launch_after(kernel, grid, cta, smem, s, a);
 }
 
 template <bool DYB, bool XB>

@@ -134,6 +134,7 @@ struct Walk {
 // are issued before this one's arithmetic.
 template <bool GUB>
 __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(const SwigluCkptArgs a) {
+    wait_for_kernel_before();
     const int nb = ckpt_blocks(a.F);
     const int sub = threadIdx.x & (kLanes - 1), part = threadIdx.x / kLanes;
     Walk at((long long)blockIdx.x * (kThreads / kLanes) + part, (long long)gridDim.x * (kThreads / kLanes), nb);
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(const Swigl
 
 template <bool DHB>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluCkptBackwardArgs a) {
+    wait_for_kernel_before();
     const int nb = ckpt_blocks(a.F);
     Walk at((long long)blockIdx.x * kThreads + threadIdx.x, (long long)gridDim.x * kThreads, a.F / 8);
     uint2 qg, qu;
@@ -230,8 +232,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluC
 template <class Kernel, class Args>
 cudaError_t go(Kernel kernel, const Args& a, long long threads, bool bf16, int sm_count, cudaStream_t stream) {
     const long long ctas = (threads + kThreads - 1) / kThreads;
-    kernel<<<(int)std::min<long long>(ctas, (long long)sm_count * (bf16 ? 4 : 3)), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, (unsigned)std::min<long long>(ctas, (long long)sm_count * (bf16 ? 4 : 3)), kThreads, 0, stream, a);
 }
 
 }  // namespace
