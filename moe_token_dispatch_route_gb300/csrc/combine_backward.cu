@@ -5,7 +5,7 @@
 // Bound by HBM: reads T rows of dout and S = T k rows of Y, writes S rows of dY.  A group of
 // threads, a CTA or for narrow rows a warp, takes one token: each of its threads reads 8 columns of
 // dout once and the same columns of up to KMAX of the token's rows of Y, all in flight at once.
-// T = 8192, k = 8, N = 4096, Y bf16 and dout fp32: 184 us, 6.6 TB/s (0.97 of a plain copy's rate).
+// T = 8192, k = 8, N = 4096, Y bf16 and dout fp32: 181 us, 6.7 TB/s (0.98 of a plain copy's rate).
 #include <algorithm>
 
 #include "train.cuh"

@@ -119,7 +119,8 @@ __host__ __device__ constexpr int forward_ctas(int cta, bool xb, int rows) {
 }
 
 // R rows at a time: the weights, 8 bytes a column from L1 where a row has 2 or 4, are read once for R
-// rows, and R rows share each barrier (8192 x 4096: bf16 30 us with one row, 27 with two; fp32 36 and 33).
+// rows, and R rows share each barrier (8192 x 4096: bf16 30 us with one row, 27 with two; fp32 36 and 33; launched while
+// the kernel before ends 24.5, 5.5 TB/s, and 31).
 template <bool XB, int TPR, int VPT, int R>
 __global__ void __launch_bounds__(cta_threads(TPR, 128), forward_ctas(cta_threads(TPR, 128), XB, R)) layernorm_kernel(const LayernormArgs a) {
     wait_for_kernel_before();
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
 // round trip is behind the arithmetic of the rows before it.
 // Measured, with the joining kernel, against the rows loaded into registers when they are needed: 8192 x 4096 bf16
 // x and fp32 dy 66 -> 62 us, fp32 both 93 -> 86; 20000 x 992 the other way, 33 -> 43.  More rows ahead are slower: 8192 x
-// 4096 bf16 54 us with two, 54.5 with three, 56 with four (fp32 dy 59 with two, 60 with three).
+// 4096 bf16 54 us with two, 54.5 with three, 56 with four (fp32 dy 59 with two, 60 with three; launched while the kernel
+// before ends 51.7 and 56.6, 5.9 TB/s).
 template <bool DYB, bool XB, int TPR>
 struct Ahead {
     static constexpr int kCta = TPR;

@@ -16,7 +16,7 @@
 // same 8 of the up half; the 16 threads of a block find its amax by shuffles.  The row and block of a
 // thread's next unit are stepped, not divided out.
 // bf16, S = 16384, F = 14336: forward 305 us, 6.2 TB/s (0.92 of a plain copy's rate); backward 365 us, 6.5 TB/s (0.95).
-// S = 65536, F = 1408: forward 124 us, both 270 us.
+// S = 65536, F = 1408: forward 123 us, both 265 us.
 #include <algorithm>
 
 #include "train.cuh"
