@@ -645,6 +645,54 @@ def test_split_reductions_repeat_and_share_a_workspace():
     assert binding.moe_read_status(st)[0] == 0
 
 
+def test_calls_wait_for_their_stream_and_for_events_of_others():
+    """Launched while the kernel before them ends, the calls still see all that their stream has been told to wait
+    for: a kernel, a copy and a fill before them, and another stream's work through an event."""
+    T, d, k, N = 512, 1040, 2, 528
+    plan = binding.moe_plan(T, d, 1, 1, 256)
+    cplan = binding.moe_plan(T, 256, 8, k, N, out_dtype=1)
+    x, other = randn((T, d), 90, BF16), randn((T, d), 91, BF16)
+    dout, w = randn((T, N), 92), randn((T, k), 93)
+    Y = randn((T * k, N), 94, BF16)
+    dest = torch.randperm(T * k, generator=_gen(95), device=DEV).to(torch.int32)
+
+    def results(x, dout, stream):
+        y, mean, rstd = nan((T, d), BF16), nan((T,)), nan((T,))
+        dx, dg, db = nan((T, d), BF16), nan((d,)), nan((d,))
+        dY, dw = nan((T * k, N), BF16), nan((T, k))
+        scratch = binding.backward_scratch(plan)
+        torch.cuda.synchronize()
+
+        def run():
+            binding.moe_layernorm(plan, x, None, None, 1e-5, y, mean, rstd, stream)
+            binding.moe_layernorm_backward(plan, y, x, None, mean, rstd, None, dx, dg, db, scratch, stream)
+            binding.moe_combine_backward(cplan, dout, Y, w, dest, dY, dw, stream)
+            return y, mean, rstd, dx, dg, db, dY, dw
+        return run
+
+    want = [t.clone() for t in results(x, dout, None)()]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for how in ("copy", "fill and add", "event"):
+        late_x, late_dout = other.clone(), torch.zeros_like(dout)
+        run = results(late_x, late_dout, b)
+        with torch.cuda.stream(a if how == "event" else b):
+            torch.cuda._sleep(10_000_000)
+            if how == "fill and add":
+                late_x.zero_()
+                late_x.add_(x)
+            else:
+                late_x.copy_(x)
+            late_dout.copy_(dout)
+        if how == "event":
+            binding.moe_layernorm(plan, other, None, None, 1e-5, nan((T, d), BF16), None, None, b)
+            b.wait_stream(a)
+        got = run()
+        torch.cuda.synchronize()
+        for g, r in zip(got, want):
+            assert torch.equal(g, r), how
+
+
 def test_no_rows():
     """T = 0: nothing is read; sums over rows are zero."""
     plan = binding.moe_plan(0, 64, 4, 2, 64)
