@@ -484,8 +484,8 @@ MOE_API moe_status_t moe_layernorm(moe_plan_t plan, const void* x, int32_t x_dty
  *   dgamma, dbeta out: fp32 [d], each may be NULL.
  *   scratch in/out: moe_backward_scratch; may be NULL when dgamma and dbeta are.
  *                MOE_ERR_WORKSPACE if it is missing or misaligned.
- * T = 0 writes zeros to dgamma and dbeta.  Launches one kernel for dx alone and a
- * second one where dgamma or dbeta is wanted.
+ * T = 0 writes zeros to dgamma and dbeta.  Launches one kernel, and a second
+ * one where dgamma or dbeta is wanted of more rows than one CTA takes at a time.
  */
 MOE_API moe_status_t moe_layernorm_backward(moe_plan_t plan, const void* dy, int32_t dy_dtype, const void* x,
                                             int32_t x_dtype, const float* gamma, const float* mean,

@@ -257,18 +257,28 @@ __device__ __forceinline__ void group_barrier(int group) {
     else if constexpr (TPR > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
 }
 
-// A thread's sums of columns c .. c + 7 into a CTA's partial sums [2][d].
-__device__ __forceinline__ void write_sums(const float (&dg)[8], const float (&db)[8], int c, int d, float* out) {
+// Where a CTA's sums go: its partial sums [2][d], or the results themselves where it is the only one.
+struct SumsOut {
+    float *dgamma, *dbeta;
+    __device__ explicit SumsOut(const LayernormBackwardArgs& a) {
+        float* part = a.partial + (size_t)blockIdx.x * 2 * a.d;
+        dgamma = gridDim.x == 1 ? a.dgamma : part;
+        dbeta = gridDim.x == 1 ? a.dbeta : part + a.d;
+    }
+};
+
+// A thread's sums of columns c .. c + 7.
+__device__ __forceinline__ void write_sums(const float (&dg)[8], const float (&db)[8], int c, const SumsOut& out) {
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
-        *reinterpret_cast<float4*>(out + c + j) = make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
-        *reinterpret_cast<float4*>(out + d + c + j) = make_float4(db[j], db[j + 1], db[j + 2], db[j + 3]);
+        if (out.dgamma) *reinterpret_cast<float4*>(out.dgamma + c + j) = make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
+        if (out.dbeta) *reinterpret_cast<float4*>(out.dbeta + c + j) = make_float4(db[j], db[j + 1], db[j + 2], db[j + 3]);
     }
 }
 
 // The sums of a CTA's row groups, added in shared memory ([group][2][COLS]) in the groups' order.
 template <int ROWS, int COLS, int CTA>
-__device__ __forceinline__ void join_rows(float* joined, const float (&dg)[8], const float (&db)[8], int group, int c, int d, float* out) {
+__device__ __forceinline__ void join_rows(float* joined, const float (&dg)[8], const float (&db)[8], int group, int c, int d, const SumsOut& out) {
     float* own = joined + group * 2 * COLS + c;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -278,11 +288,12 @@ __device__ __forceinline__ void join_rows(float* joined, const float (&dg)[8], c
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * COLS; i += CTA) {
         const int col = i % COLS, half = i / COLS;
-        if (col >= d) continue;
+        float* to = half ? out.dbeta : out.dgamma;
+        if (col >= d || !to) continue;
         float v = 0.f;
 #pragma unroll
         for (int g = 0; g < ROWS; ++g) v += joined[g * 2 * COLS + i];
-        out[half * d + col] = v;
+        to[col] = v;
     }
 }
 
@@ -341,8 +352,7 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
     }
     if (!a.dgamma && !a.dbeta) return;
     asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
-    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
-    join_rows<B::kRows, B::kCols, B::kCta>(joined, dg, db, group, c, a.d, out);
+    join_rows<B::kRows, B::kCols, B::kCta>(joined, dg, db, group, c, a.d, SumsOut(a));
 }
 
 // 1024 < d <= 8192: a CTA holds one row, the same way, and its next rows are on their way in shared
@@ -473,8 +483,7 @@ __global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>
         for (int s = 0; s < B::kStages; ++s) row_landed(bars + 8 * s, phase);
     if (!a.dgamma && !a.dbeta) return;
     asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may start; it waits for this one's end
-    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
-    if (mine) write_sums(dg, db, c, a.d, out);
+    if (mine) write_sums(dg, db, c, SumsOut(a));
 }
 
 // 8192 < d <= 16384: 1024 threads leave 64 registers each, so dgamma and dbeta are summed in shared
@@ -558,14 +567,16 @@ __global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const Layernor
     }
     if (!a.dgamma && !a.dbeta) return;
     asm volatile("griddepcontrol.launch_dependents;");
-    float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
+    const SumsOut out(a);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (tid + i * kTall) * 8;
         if (c >= a.d) continue;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-            *reinterpret_cast<float4*>(out + (v >> 1) * a.d + c + (v & 1) * 4) = sums4[(4 * i + v) * kTall + tid];
+        for (int v = 0; v < 4; ++v) {
+            float* to = v >> 1 ? out.dbeta : out.dgamma;
+            if (to) *reinterpret_cast<float4*>(to + c + (v & 1) * 4) = sums4[(4 * i + v) * kTall + tid];
+        }
     }
 }
 
@@ -786,7 +797,7 @@ cudaError_t backward(const LayernormBackwardArgs& a, int sm_count, cudaStream_t 
         default: go(std::integral_constant<int, 1024>()); break;
     }
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e == cudaSuccess && (a.dgamma || a.dbeta)) e = join(a, parts, s);
+    if (e == cudaSuccess && (a.dgamma || a.dbeta) && parts > 1) e = join(a, parts, s);
     return e;
 }
 

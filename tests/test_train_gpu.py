@@ -182,6 +182,23 @@ def test_layernorm_backward_optional_arguments_and_repeats():
         assert torch.equal(db2, db) if want_b else torch.isnan(db2).all()
 
 
+@pytest.mark.parametrize("T,d", [(1, 16), (3, 272), (16, 64), (1, 2064), (1, 9008), (2, 9008), (1, 16400)])
+@pytest.mark.parametrize("want_g,want_b", [(True, True), (True, False), (False, True), (False, False)])
+def test_layernorm_backward_of_few_rows(T, d, want_g, want_b):
+    """One CTA writes the weights' gradients itself, those that are wanted."""
+    x, dy, dres = randn((T, d), 26, BF16), randn((T, d), 27), randn((T, d), 28, BF16)
+    plan, scratch, mean, rstd, dx, dg, db = ln_back_run(dy, x, None, dres)
+    _, _, rdg, mdg, rdb, mdb = ln_back_ref(dy, x, None, mean, rstd, dres)
+    check(dg, rdg, mdg, rounds(T))
+    check(db, rdb, mdb, rounds(T))
+    dx2, dg2, db2 = nan((T, d), BF16), nan((d,)), nan((d,))
+    binding.moe_layernorm_backward(plan, dy, x, None, mean, rstd, dres, dx2, dg2 if want_g else None,
+                                   db2 if want_b else None, scratch if want_g or want_b else None)
+    assert torch.equal(dx2, dx)
+    assert torch.equal(dg2, dg) if want_g else torch.isnan(dg2).all()
+    assert torch.equal(db2, db) if want_b else torch.isnan(db2).all()
+
+
 def test_layernorm_gradient_against_differences():
     T, d = 9, 272
     x, gamma, beta, r = (randn(s, 20 + i) for i, s in enumerate(((T, d), (d,), (d,), (T, d))))
