@@ -97,6 +97,16 @@ struct SmemCtl {
     PieceRec piece[kThreads / 32][kMaxPieceBufs];  // scatter: per-warp ring of staged pieces
 };
 
+// True, once every word of the description is in a register.  A ring slot may be handed back only
+// then: a load of shared memory queues behind its warp's stores to global memory (an epilogue warp has
+// microseconds of them when it takes its next tile), but an arrival on a barrier, of another CTA's above all,
+// does not, and the slot's next description would be read in its place: one tile written twice
+// and another not at all.  (No field is the lowest integer, and the other negative ones
+// have more bits, so the words' OR is never the lowest integer.)
+__device__ __forceinline__ bool taken(const TileInfo& t) {
+    return (t.e | t.m | t.n | t.mtile | t.row0 | t.rows | t.rank | t.arow | t.m128 | t.half) != (int)0x80000000;
+}
+
 static_assert(sizeof(TileInfo) % 8 == 0, "tile descriptions move in 8-byte asynchronous stores");
 static_assert(offsetof(SmemCtl, ring) % 8 == 0, "ring slots must be 8-byte aligned");
 
@@ -1025,7 +1035,7 @@ __device__ void tma_b_role(const DispatchGemmParams& p, SmemCtl* ctl, uint8_t* s
     for (;;) {
         if (!wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 35)) return;
         const TileInfo ti = ctl->ring[slot];
-        mbar_arrive(smem_addr(&ctl->sempty[slot]));
+        if (taken(ti)) mbar_arrive(smem_addr(&ctl->sempty[slot]));
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1063,9 +1073,9 @@ __device__ void mma_role(const DispatchGemmParams& p, SmemCtl* ctl, uint8_t* sA,
     bool ok = true;
     while (ok) {
         if (!wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 4)) break;
-        const int rows = ctl->ring[slot].rows;
-        const uint32_t idesc = ctl->ring[slot].half ? C::kIdescHalf : C::kIdesc;  // N = BN or BN/2
-        mbar_arrive(smem_addr(&ctl->sempty[slot]));
+        const int rows = ctl->ring[slot].rows, half = ctl->ring[slot].half;
+        const uint32_t idesc = half ? C::kIdescHalf : C::kIdesc;  // N = BN or BN/2
+        if ((rows | half) != (int)0x80000000) mbar_arrive(smem_addr(&ctl->sempty[slot]));  // as taken()
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1143,8 +1153,8 @@ __device__ void epilogue_role(const DispatchGemmParams& p, SmemCtl* ctl, uint32_
         const bool got = wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 8);
         if (!__all_sync(kFull, got)) break;
         const TileInfo ti = ctl->ring[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl->sempty[slot]));
+        const bool read = __all_sync(kFull, taken(ti));
+        if (read && lane == 0) mbar_arrive(smem_addr(&ctl->sempty[slot]));
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1207,8 +1217,8 @@ __device__ void gather_a_role(const DispatchGemmParams& p, SmemCtl* ctl, uint8_t
         const bool got = wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 40, true, pair);
         if (!__all_sync(kFull, got)) break;
         const TileInfo ti = ctl->ring[slot];
-        __syncwarp();
-        if (lane == 0) {
+        const bool read = __all_sync(kFull, taken(ti));
+        if (read && lane == 0) {
             const uint32_t se = smem_addr(&ctl->sempty[slot]);
             if (leader) mbar_arrive(se);
             else mbar_arrive_remote(mapa_shared(se, lead));
@@ -1281,7 +1291,7 @@ __device__ void pair_relay_role(const DispatchGemmParams& p, SmemCtl* ctl, const
     for (;;) {
         if (!wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 31, true, true)) return;
         const int e = ctl->ring[slot].e;
-        mbar_arrive_remote(mapa_shared(smem_addr(&ctl->sempty[slot]), lead));
+        if (e != (int)0x80000000) mbar_arrive_remote(mapa_shared(smem_addr(&ctl->sempty[slot]), lead));  // as taken()
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1570,7 +1580,7 @@ __device__ void pair_tma_role(const DispatchGemmParams& p, SmemCtl* ctl, const i
                 return true;  // not published yet
             }
             ti = ctl->ring[slot];
-            mbar_arrive_remote(mapa_shared(smem_addr(&ctl->sempty[slot]), lead));
+            if (taken(ti)) mbar_arrive_remote(mapa_shared(smem_addr(&ctl->sempty[slot]), lead));
         }
         armed = false;
         if (++slot == kRing) {
@@ -1687,8 +1697,10 @@ __device__ void pair_tma_b_role(const DispatchGemmParams& p, SmemCtl* ctl, uint8
         if (!wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 33, true, true)) return;
         const TileInfo ti = ctl->ring[slot];
         const uint32_t se = smem_addr(&ctl->sempty[slot]);
-        if (leader) mbar_arrive(se);
-        else mbar_arrive_remote(mapa_shared(se, lead));
+        if (taken(ti)) {
+            if (leader) mbar_arrive(se);
+            else mbar_arrive_remote(mapa_shared(se, lead));
+        }
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1735,9 +1747,9 @@ __device__ void pair_mma_role(const DispatchGemmParams& p, SmemCtl* ctl, uint8_t
     bool ok = true;
     while (ok) {
         if (!wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 25, true, true)) break;
-        const int e = ctl->ring[slot].e;
-        const uint32_t idesc = ctl->ring[slot].m128 ? C::kIdesc128 : C::kIdesc;
-        mbar_arrive(smem_addr(&ctl->sempty[slot]));
+        const int e = ctl->ring[slot].e, m128 = ctl->ring[slot].m128;
+        const uint32_t idesc = m128 ? C::kIdesc128 : C::kIdesc;
+        if ((e | m128) != (int)0x80000000) mbar_arrive(smem_addr(&ctl->sempty[slot]));  // as taken()
         if (++slot == kRing) {
             slot = 0;
             sphase ^= 1u;
@@ -1820,8 +1832,8 @@ __device__ void pair_epilogue_role(const DispatchGemmParams& p, SmemCtl* ctl, ui
         const bool got = wait_bar(smem_addr(&ctl->sfull[slot]), sphase, w, 29, true, true);
         if (!__all_sync(kFull, got)) break;
         const TileInfo ti = ctl->ring[slot];
-        __syncwarp();
-        if (lane == 0) {
+        const bool read = __all_sync(kFull, taken(ti));
+        if (read && lane == 0) {
             const uint32_t se = smem_addr(&ctl->sempty[slot]);
             if (leader) mbar_arrive(se);
             else mbar_arrive_remote(mapa_shared(se, lead));
