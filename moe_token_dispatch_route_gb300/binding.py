@@ -172,6 +172,9 @@ class Plan:
         info = PlanInfo()
         _check(load_library().moe_plan_info(handle, ctypes.byref(info)), "moe_plan_info")
         self.info = info.as_dict()
+        scratch = ctypes.c_size_t()
+        _check(load_library().moe_backward_scratch(handle, ctypes.byref(scratch)), "moe_backward_scratch")
+        self.scratch_bytes = scratch.value
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -335,11 +338,24 @@ def _opt(call: str, plan: Plan, name: str, t, numel: int, dtypes: tuple) -> int 
     return _arg(call, plan, name, t, numel, dtypes)
 
 
+def _buf(call: str, plan: Plan, name: str, t, nbytes: int) -> int | None:
+    """Device pointer of a buffer that the kernels write without looking at its size: dense, on the plan's device, at
+    least `nbytes` long (one that was made for a smaller plan would be written past its end).  An int is an
+    address that the caller answers for; a missing buffer is the library's to refuse."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.nbytes >= nbytes and t.get_device() == plan.device and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != plan.device:
+        raise ValueError(f"{call}: {name} is on {t.device}, the plan on cuda:{plan.device}")
+    raise ValueError(f"{call}: {name} must be dense with at least {nbytes} bytes, has {t.nbytes}"
+                     f"{'' if t.is_contiguous() else ', strided'}")
+
+
 def backward_scratch(plan: Plan, device=None) -> torch.Tensor:
     """Zeroed scratch of moe_layernorm_backward (the caller keeps it, like the workspace)."""
-    n = ctypes.c_size_t()
-    _check(load_library().moe_backward_scratch(plan.handle, ctypes.byref(n)), "moe_backward_scratch")
-    return torch.zeros(n.value, dtype=torch.uint8, device=torch.device("cuda", plan.device) if device is None else device)
+    return torch.zeros(plan.scratch_bytes, dtype=torch.uint8,
+                       device=torch.device("cuda", plan.device) if device is None else device)
 
 
 def moe_layernorm(plan: Plan, x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
@@ -367,7 +383,9 @@ def moe_layernorm_backward(plan: Plan, dy, x, gamma, mean, rstd, dres, dx, dgamm
         _opt(c, plan, "gamma", gamma, d, _IS_F32), _arg(c, plan, "mean", mean, T, _IS_F32),
         _arg(c, plan, "rstd", rstd, T, _IS_F32), _opt(c, plan, "dres", dres, n, (x.dtype,)),
         _arg(c, plan, "dx", dx, n, (x.dtype,)), _opt(c, plan, "dgamma", dgamma, d, _IS_F32),
-        _opt(c, plan, "dbeta", dbeta, d, _IS_F32), _ptr(scratch), _stream(stream, plan.device)), c)
+        _opt(c, plan, "dbeta", dbeta, d, _IS_F32),
+        None if dgamma is None and dbeta is None else _buf(c, plan, "scratch", scratch, plan.scratch_bytes),
+        _stream(stream, plan.device)), c)
 
 
 def _out_dtype(plan: Plan):
@@ -420,7 +438,8 @@ def moe_grouped_gemm_dgrad(plan: Plan, dY, offsets, W, dA, workspace, dev_status
     _check(load_library().moe_grouped_gemm_dgrad(
         plan.handle, _arg(c, plan, "dY", dY, S * N, _IS_BF16), _arg(c, plan, "offsets", offsets, plan.E + 1, _IS_I32),
         _arg(c, plan, "W", W, plan.E * plan.d * N, _IS_BF16), _arg(c, plan, "dA", dA, S * plan.d, _IS_EITHER),
-        _DTYPES[dA.dtype], _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
+        _DTYPES[dA.dtype], _buf(c, plan, "workspace", workspace, plan.workspace_bytes),
+        _buf(c, plan, "dev_status", dev_status, 16), _stream(stream, plan.device)), c)
 
 
 def moe_grouped_gemm_wgrad(plan: Plan, A, dY, offsets, dW, workspace, dev_status, accumulate: bool = False,
@@ -432,7 +451,8 @@ def moe_grouped_gemm_wgrad(plan: Plan, A, dY, offsets, dW, workspace, dev_status
         plan.handle, _arg(c, plan, "A", A, S * plan.d, _IS_BF16), _arg(c, plan, "dY", dY, S * N, _IS_BF16),
         _arg(c, plan, "offsets", offsets, plan.E + 1, _IS_I32),
         _arg(c, plan, "dW", dW, plan.E * plan.d * N, _IS_EITHER), _DTYPES[dW.dtype], int(accumulate),
-        _ptr(workspace), _ptr(dev_status), _stream(stream, plan.device)), c)
+        _buf(c, plan, "workspace", workspace, plan.workspace_bytes), _buf(c, plan, "dev_status", dev_status, 16),
+        _stream(stream, plan.device)), c)
 
 
 def moe_read_status(dev_status, stream=None) -> tuple[int, list[int]]:
