@@ -65,8 +65,8 @@ class MoeTrainLayer:
         return self.out.add_(x)
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
-        """dout fp32 [T, d].  Writes grads["W1"], ["W2"] (or adds to them), ["W_r"], ["gamma"] and
-        ["beta"], fp32, and returns the gradient of x."""
+        """dout fp32 [T, d].  Writes grads["W1"], ["W2"], ["W_r"], ["gamma"] and ["beta"], fp32, or
+        (accumulate) adds to all of them, and returns the gradient of x."""
         with self._on(stream):
             return self._backward(dout, x, gamma, W_r, W1, W2, grads, accumulate)
 
@@ -84,11 +84,19 @@ class MoeTrainLayer:
         w = r.topk_w
         dlogits = torch.zeros_like(self.logits).scatter_(
             1, r.topk_idx.long(), w * (self.dw - (w * self.dw).sum(1, keepdim=True)))
-        torch.mm(self.y.float().T, dlogits, out=grads["W_r"])
+        if accumulate:
+            grads["W_r"].addmm_(self.y.float().T, dlogits)
+        else:
+            torch.mm(self.y.float().T, dlogits, out=grads["W_r"])
         self.dy.addmm_(dlogits, W_r.float().T)
         dx = torch.empty_like(x)
-        b.moe_layernorm_backward(u, self.dy, x, gamma, self.mean, self.rstd, dout, dx, grads["gamma"], grads["beta"],
-                                 self.scratch)
+        dgamma, dbeta = grads["gamma"], grads["beta"]
+        if accumulate:  # the norm's gradient is written, so it goes through buffers of its own
+            dgamma, dbeta = torch.empty_like(dgamma), torch.empty_like(dbeta)
+        b.moe_layernorm_backward(u, self.dy, x, gamma, self.mean, self.rstd, dout, dx, dgamma, dbeta, self.scratch)
+        if accumulate:
+            grads["gamma"].add_(dgamma)
+            grads["beta"].add_(dbeta)
         return dx
 
     def kept_bytes(self) -> int:

@@ -1,0 +1,52 @@
+"""What a training layer keeps, adds to and hands out from call to call."""
+import pytest
+import torch
+
+from moe_token_dispatch_route_gb300.training import MoeTrainLayer
+
+pytestmark = pytest.mark.gpu
+T, D, F, E, K = 200, 256, 208, 8, 2
+
+
+def weights(seed=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale):
+        return torch.randn(shape, generator=g, device="cuda") * scale
+    return {"W_r": normal(D, E, scale=D ** -0.5).bfloat16(), "W1": normal(E, D, 2 * F, scale=D ** -0.5).bfloat16(),
+            "W2": normal(E, F, D, scale=F ** -0.5).bfloat16(), "gamma": 1 + normal(D, scale=0.1), "beta": normal(D, scale=0.1)}
+
+
+def batch(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(T, D, generator=g, device="cuda"), torch.randn(T, D, generator=g, device="cuda")
+
+
+def empty_grads(p):
+    return {n: torch.full(v.shape, float("nan"), device="cuda") for n, v in p.items()}
+
+
+def backward(layer, dout, x, p, grads, **kw):
+    return layer.backward(dout, x, p["gamma"], p["W_r"], p["W1"], p["W2"], grads, **kw)
+
+
+def test_gradients_of_micro_batches_add_up():
+    """All five gradients of two different batches.  Each is a sum of T or fewer fp32 terms in another order than that of
+    the two alone: off by T u of the terms' magnitudes, which are below sqrt(T) of the sums' norm, 2e-4 in
+    all.  (An overwritten gradient is off by half and more.)"""
+    p, layer = weights(), MoeTrainLayer(T, D, F, E, K)
+    alone = []
+    for seed in (11, 12):
+        x, dout = batch(seed)
+        grads = empty_grads(p)
+        layer.forward(x, **p)
+        backward(layer, dout, x, p, grads)
+        alone.append(grads)
+    both = empty_grads(p)
+    for i, seed in enumerate((11, 12)):
+        x, dout = batch(seed)
+        layer.forward(x, **p)
+        backward(layer, dout, x, p, both, accumulate=i > 0)
+    for n in p:
+        want = alone[0][n] + alone[1][n]
+        assert float((both[n] - want).norm()) <= 2e-4 * float(alone[0][n].norm() + alone[1][n].norm()), n
