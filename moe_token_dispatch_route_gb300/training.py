@@ -20,7 +20,8 @@ class MoeTrainLayer:
     """Plans and device buffers of a layer of T tokens of width d, E experts of hidden width F, k
     experts a token; d and F are multiples of 16.  x: fp32 [T, d].  Weights: W_r bf16 [d, E], W1 bf16
     [E, d, 2F] (gate columns, then up), W2 bf16 [E, F, d], gamma and beta fp32 [d]; their gradients
-    are fp32.  `stream`: a torch stream or a raw handle; None is the current one."""
+    are fp32.  `stream`: a torch stream or a raw handle; None is the current one.  The buffers belong to the
+    stream that is current when the layer is made: keep the layer until its passes on other streams are done."""
 
     def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0):
         self.T, self.d, self.F, self.E, self.k, self.eps = T, d, F, E, k, eps
@@ -44,6 +45,8 @@ class MoeTrainLayer:
         self.H, self.dH, self.dY, self.dA = new(S, F), new(S, F), new(S, d), new(S, d)
         self.dw, self.dy = new(T, k, dtype=_F32), new(T, d, dtype=_F32)
         self.ones = torch.ones(T, k, dtype=_F32, device=dev)
+        # the fills above, and what the memory was used for before, are over before any stream uses it
+        torch.cuda.current_stream(dev).synchronize()
 
     def _on(self, stream):
         """Makes `stream` the current one, for the library's calls and for PyTorch's."""

@@ -50,3 +50,28 @@ def test_gradients_of_micro_batches_add_up():
     for n in p:
         want = alone[0][n] + alone[1][n]
         assert float((both[n] - want).norm()) <= 2e-4 * float(alone[0][n].norm() + alone[1][n].norm()), n
+
+
+def test_a_new_layer_is_ready_for_any_stream():
+    """The constructor's fills are over when it returns: a first pass on another stream waits for nothing of the stream
+    that the layer was made on, and has the workspace's counters at zero."""
+    p = weights()
+    x, dout = batch(21)
+    first = MoeTrainLayer(T, D, F, E, K)
+    want = [first.forward(x, **p).clone()]
+    grads = empty_grads(p)
+    want += [backward(first, dout, x, p, grads)] + [grads[n] for n in sorted(p)]
+    made_on, used_on = torch.cuda.Stream(), torch.cuda.Stream()
+    got = empty_grads(p)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(made_on):
+        torch.cuda._sleep(200_000_000)
+        layer = MoeTrainLayer(T, D, F, E, K)
+        assert made_on.query()
+    out = layer.forward(x, **p, stream=used_on)
+    with torch.cuda.stream(used_on):
+        out = out.clone()
+    dx = backward(layer, dout, x, p, got, stream=used_on)
+    torch.cuda.synchronize()
+    for a, b in zip(want, [out, dx] + [got[n] for n in sorted(p)]):
+        assert torch.equal(a, b)
