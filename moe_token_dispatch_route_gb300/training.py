@@ -50,7 +50,9 @@ class MoeTrainLayer:
 
     def _on(self, stream):
         """Makes `stream` the current one, for the library's calls and for PyTorch's."""
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
+        if isinstance(stream, int):  # (an ExternalStream of handle 0 is a new stream, not the default one)
+            stream = torch.cuda.ExternalStream(stream, self.device) if stream else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
 
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None):
         with self._on(stream):

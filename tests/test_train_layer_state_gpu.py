@@ -75,3 +75,14 @@ def test_a_new_layer_is_ready_for_any_stream():
     torch.cuda.synchronize()
     for a, b in zip(want, [out, dx] + [got[n] for n in sorted(p)]):
         assert torch.equal(a, b)
+
+
+def test_the_default_streams_raw_handle_is_the_default_stream():
+    handle = torch.cuda.default_stream().cuda_stream
+    side = torch.cuda.Stream()
+    layer = MoeTrainLayer(T, D, F, E, K)
+    for given, want in ((handle, handle), (side.cuda_stream, side.cuda_stream), (side, side.cuda_stream)):
+        with layer._on(given):
+            assert torch.cuda.current_stream().cuda_stream == want
+    with torch.cuda.stream(side), layer._on(None):
+        assert torch.cuda.current_stream() == side
