@@ -55,6 +55,8 @@ class MoeTrainLayer:
         return torch.cuda.stream(stream)
 
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None):
+        """The layer's output, a tensor of its own.  The layer keeps one pass: a second forward replaces what the
+        first one's backward would need."""
         with self._on(stream):
             return self._forward(x, gamma, beta, W_r, W1, W2)
 
@@ -67,10 +69,11 @@ class MoeTrainLayer:
         b.moe_swiglu_checkpoint(u, r.Y, self.H, self.codes, self.scales)
         b.moe_grouped_gemm(self.down, self.H, r.offsets, W2, self.Y, self.down_ws, r.status)
         b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out)
-        return self.out.add_(x)
+        return torch.add(self.out, x)
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
-        """dout fp32 [T, d].  Writes grads["W1"], ["W2"], ["W_r"], ["gamma"] and ["beta"], fp32, or
+        """The gradients of the latest forward pass (which may be taken more than once).  x and the weights are that pass's,
+        dout fp32 [T, d].  Writes grads["W1"], ["W2"], ["W_r"], ["gamma"] and ["beta"], fp32, or
         (accumulate) adds to all of them, and returns the gradient of x."""
         with self._on(stream):
             return self._backward(dout, x, gamma, W_r, W1, W2, grads, accumulate)

@@ -86,3 +86,19 @@ def test_the_default_streams_raw_handle_is_the_default_stream():
             assert torch.cuda.current_stream().cuda_stream == want
     with torch.cuda.stream(side), layer._on(None):
         assert torch.cuda.current_stream() == side
+
+
+def test_outputs_outlive_the_next_pass_and_a_backward_repeats():
+    p, layer = weights(), MoeTrainLayer(T, D, F, E, K)
+    (x1, dout), (x2, _) = batch(31), batch(32)
+    out1 = layer.forward(x1, **p)
+    kept = out1.clone()
+    out2 = layer.forward(x2, **p)
+    assert torch.equal(out1, kept) and not torch.equal(out1, out2)
+    results = []
+    for _ in range(2):
+        grads = empty_grads(p)
+        results.append([backward(layer, dout, x2, p, grads)] + [grads[n] for n in sorted(p)])
+    assert torch.equal(out1, kept)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
