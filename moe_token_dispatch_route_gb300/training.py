@@ -5,7 +5,8 @@
 with Mixtral-style gates (softmax over the k chosen logits).  Between the two passes it keeps the
 dispatched rows, the up projection's outputs in 8 bits, the experts' outputs and the routing; H is
 computed again from the 8-bit values.  The router's own two products ([T, d] by [d, E]) and the
-gates' softmax over k values are PyTorch's.
+gates' softmax over k values are PyTorch's.  Nothing is recorded for automatic differentiation: inputs and weights may
+require gradients, results do not.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ class MoeTrainLayer:
     """Plans and device buffers of a layer of T tokens of width d, E experts of hidden width F, k
     experts a token; d and F are multiples of 16.  x: fp32 [T, d].  Weights: W_r bf16 [d, E], W1 bf16
     [E, d, 2F] (gate columns, then up), W2 bf16 [E, F, d], gamma and beta fp32 [d]; their gradients
-    are fp32.  `stream`: a torch stream or a raw handle; None is the current one.  The buffers belong to the
+    are fp32.  `stream`: a torch stream or a raw handle; None is the current one; results belong to it.  The buffers belong to the
     stream that is current when the layer is made: keep the layer until its passes on other streams are done."""
 
     def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0):
@@ -57,7 +58,7 @@ class MoeTrainLayer:
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None):
         """The layer's output, a tensor of its own.  The layer keeps one pass: a second forward replaces what the
         first one's backward would need."""
-        with self._on(stream):
+        with torch.no_grad(), self._on(stream):
             return self._forward(x, gamma, beta, W_r, W1, W2)
 
     def _forward(self, x, gamma, beta, W_r, W1, W2):
@@ -75,7 +76,7 @@ class MoeTrainLayer:
         """The gradients of the latest forward pass (which may be taken more than once).  x and the weights are that pass's,
         dout fp32 [T, d].  Writes grads["W1"], ["W2"], ["W_r"], ["gamma"] and ["beta"], fp32, or
         (accumulate) adds to all of them, and returns the gradient of x."""
-        with self._on(stream):
+        with torch.no_grad(), self._on(stream):
             return self._backward(dout, x, gamma, W_r, W1, W2, grads, accumulate)
 
     def _backward(self, dout, x, gamma, W_r, W1, W2, grads, accumulate):

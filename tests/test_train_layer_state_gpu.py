@@ -102,3 +102,22 @@ def test_outputs_outlive_the_next_pass_and_a_backward_repeats():
     assert torch.equal(out1, kept)
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_inputs_and_weights_that_require_gradients():
+    """Parameters as a model holds them: the results are the same, and nothing is recorded in the layer's buffers."""
+    p, layer = weights(), MoeTrainLayer(T, D, F, E, K)
+    x, dout = batch(41)
+    results = []
+    for wanted in (False, True):
+        q = {n: v.detach().clone().requires_grad_(wanted) for n, v in p.items()}
+        xq = x.clone().requires_grad_(wanted)
+        grads = empty_grads(p)
+        for accumulate in (False, True):
+            out = layer.forward(xq, **q)
+            dx = backward(layer, dout, xq, q, grads, accumulate=accumulate)
+        kept = [v for v in vars(layer).values() if isinstance(v, torch.Tensor)]
+        assert not any(t.requires_grad for t in [out, dx, *grads.values(), *kept])
+        results.append([out, dx] + [grads[n] for n in sorted(p)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
