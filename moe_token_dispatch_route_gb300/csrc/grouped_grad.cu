@@ -97,6 +97,25 @@ struct SplitTile {
     int c0, rows;
     int slot0, n, stride, pad;
 };
+// Whether a listed tile lies inside an output of `out_rows` rows, and its pieces inside `slots` slots.
+// The list is the kernel's own, but one that ended early (a wait ran out, which the status says) leaves entries of
+// an earlier call in it, of another output: the joining kernel passes over what it must not touch.
+__host__ __device__ constexpr bool inside(long long out_row, int c0, int rows, int slot0, int n, int stride,
+                                          long long out_rows, int row_tile, int slots) {
+    return rows > 0 && rows <= row_tile && out_row >= 0 && out_row <= out_rows - rows && c0 >= 0 && n > 0 && n <= slots &&
+           slot0 >= 0 && stride >= 0 && slot0 + (long long)(n - 1) * stride < slots;
+}
+static_assert(inside(0, 0, 256, 0, 2, 76, 256, 256, 152) && inside(744, 512, 256, 75, 2, 76, 1000, 256, 152), "in bounds");
+static_assert(!inside(745, 0, 256, 0, 2, 76, 1000, 256, 152) && !inside(-1, 0, 16, 0, 2, 1, 1000, 256, 152) &&
+                  !inside(1LL << 62, 0, 16, 0, 2, 1, 1000, 256, 152) && !inside(0, -256, 16, 0, 2, 1, 1000, 256, 152),
+              "outside the output");
+static_assert(!inside(0, 0, 0, 0, 2, 1, 1000, 256, 152) && !inside(0, 0, 257, 0, 2, 1, 1000, 256, 152) &&
+                  !inside(0, 0, 65, 0, 2, 1, 1000, 64, 152),
+              "no rows, or more than a tile's");
+static_assert(!inside(0, 0, 16, 76, 2, 76, 1000, 256, 152) && !inside(0, 0, 16, -1, 2, 76, 1000, 256, 152) &&
+                  !inside(0, 0, 16, 0, 153, 0, 1000, 256, 152) && !inside(0, 0, 16, 0, 152, 0x7FFFFFFF, 1000, 256, 152) &&
+                  !inside(0, 0, 16, 0, 2, -1, 1000, 256, 152) && !inside(0, 0, 16, 0, 0, 1, 1000, 256, 152),
+              "outside the slots");
 constexpr int kMaxSplit = 256;    // split tiles: at most one for each pair of CTAs
 constexpr int kMaxSplitExperts = 160;  // each has more than a pair's share of all the work: fewer than pairs
 constexpr int kMinPieceKb = 16;   // shortest piece, in k-blocks
@@ -820,7 +839,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
     if (pad + smem_bytes<F>(p.a.E) > dynamic_smem_size()) {
+        wait_for_kernel_before();
         if (threadIdx.x == 0) report_error(p.a.status, kStDevice, -3, (int)raw, 0);
+        if (threadIdx.x == 0 && blockIdx.x == 0 && p.split) p.split->count = 0;
         return;
     }
     uint8_t* sP = smem_raw + pad;
@@ -967,7 +988,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 constexpr int kJoinThreads = 256;
 template <Form F>
 __global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitArea* split, const float* slots, void* out,
-                                                                   int c_size, int out_bf16, int accumulate) {
+                                                                   long long out_rows, int n_slots, int c_size,
+                                                                   int out_bf16, int accumulate) {
     constexpr int kRow = Cfg<F>::kRowTile;
     wait_for_kernel_before();
     const int count = min(__ldcg(&split->count), kMaxSplit);
@@ -975,11 +997,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitAr
     for (int u = blockIdx.x; u < count * (kRow / 4); u += gridDim.x) {
         const SplitTile* t = split->tile + u / (kRow / 4);
         const int row = u % (kRow / 4) * 4 + (threadIdx.x >> 6);
-        const int col = __ldcg(&t->c0) + c;
-        if (row >= __ldcg(&t->rows) || col >= c_size) continue;  // c_size % 16 == 0
-        const int n = __ldcg(&t->n);
-        const size_t step = (size_t)__ldcg(&t->stride) * kRow * 256;
-        const float* at = slots + ((size_t)__ldcg(&t->slot0) * kRow + row) * 256 + c;
+        const long long out_row = __ldcg(&t->out_row);
+        const int c0 = __ldcg(&t->c0), rows = __ldcg(&t->rows), slot0 = __ldcg(&t->slot0), n = __ldcg(&t->n), stride = __ldcg(&t->stride);
+        if (!inside(out_row, c0, rows, slot0, n, stride, out_rows, kRow, n_slots)) continue;
+        const int col = c0 + c;
+        if (row >= rows || col >= c_size) continue;  // c_size % 16 == 0
+        const size_t step = (size_t)stride * kRow * 256;
+        const float* at = slots + ((size_t)slot0 * kRow + row) * 256 + c;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
@@ -989,7 +1013,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const SplitAr
             v.z += x.z;
             v.w += x.w;
         }
-        const size_t o = (size_t)(__ldcg(&t->out_row) + row) * c_size + col;
+        const size_t o = (size_t)(out_row + row) * c_size + col;
         if (out_bf16) {
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
         } else {
@@ -1046,7 +1070,8 @@ cudaError_t launch(GradParams& p, const GroupedGradArgs& a, bool may_split, int 
     e = launch_after(grouped_grad_kernel<F>, 2u * pairs, kGradThreads, smem_bytes<F>(a.E), stream, (const GradParams&)p);
     if (e == cudaSuccess && p.split)
         e = launch_after(join_pieces_kernel<F>, (unsigned)sm_count, kJoinThreads, 0, stream, (const SplitArea*)p.split,
-                         (const float*)p.slots, a.out, p.c_size, a.out_bf16, a.accumulate);
+                         (const float*)p.slots, a.out, Cfg<F>::kWeight ? (long long)a.E * a.d : (long long)a.S, sm_count,
+                         p.c_size, a.out_bf16, a.accumulate);
     return e;
 }
 
