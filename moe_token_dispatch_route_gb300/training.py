@@ -86,7 +86,7 @@ class MoeTrainLayer:
         dGU = r.Y                                                                  # GU's buffer: its values are in the codes
         b.moe_swiglu_checkpoint_backward(u, self.dH, self.codes, self.scales, self.H, dGU)
         b.moe_grouped_gemm_wgrad(dn, self.H, self.dY, r.offsets, grads["W2"], self.down_ws, r.status, accumulate)
-        b.moe_grouped_gemm_wgrad(u, r.recv[0], dGU, r.offsets, grads["W1"], r.workspace, r.status, accumulate)
+        b.moe_grouped_gemm_wgrad(u, r.recv[0][:u.S], dGU, r.offsets, grads["W1"], r.workspace, r.status, accumulate)
         b.moe_grouped_gemm_dgrad(u, dGU, r.offsets, W1, self.dA, r.workspace, r.status)
         b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy)                     # the dispatch's gradient
         # the gates: softmax over the chosen logits

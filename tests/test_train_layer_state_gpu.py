@@ -121,3 +121,47 @@ def test_inputs_and_weights_that_require_gradients():
         results.append([out, dx] + [grads[n] for n in sorted(p)])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_a_layer_without_tokens():
+    """T = 0: nothing is read, and sums over rows are zero, or add nothing."""
+    p, layer = weights(), MoeTrainLayer(0, D, F, E, K)
+    x = torch.empty(0, D, device="cuda")
+    assert layer.forward(x, **p).shape == (0, D)
+    grads = empty_grads(p)
+    assert backward(layer, x, x, p, grads).shape == (0, D)
+    assert all((g == 0).all() for g in grads.values())
+    for g in grads.values():
+        g.fill_(1.5)
+    layer.forward(x, **p)
+    backward(layer, x, x, p, grads, accumulate=True)
+    assert all((g == 1.5).all() for g in grads.values())
+
+
+def test_a_step_in_a_graph():
+    """A whole step, captured once and replayed on other inputs, gives what the calls give."""
+    p, layer = weights(), MoeTrainLayer(T, D, F, E, K)
+    grads = empty_grads(p)
+    x, dout = batch(51)
+
+    def step():
+        out = layer.forward(x, **p)
+        return [out, backward(layer, dout, x, p, grads)] + [grads[n] for n in sorted(p)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # first uses are outside the capture
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = step()
+    for seed in (52, 53):
+        for to, value in zip((x, dout), batch(seed)):
+            to.copy_(value)
+        for g in grads.values():
+            g.fill_(float("nan"))
+        graph.replay()
+        got = [t.clone() for t in captured]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
