@@ -706,7 +706,7 @@ template <bool XB, int R>
 void forward_rows(const LayernormArgs& a, int sm_count, cudaStream_t s) {
     auto go = [&](auto tpr) {
         constexpr int kTpr = decltype(tpr)::value, kCta = cta_threads(kTpr, 128), kRows = kCta / kTpr * R;
-        const int grid = std::min((a.T + kRows - 1) / kRows, sm_count * (2048 / kCta));
+        const int grid = (int)std::min(((long long)a.T + kRows - 1) / kRows, (long long)sm_count * (2048 / kCta));
         launch_after(layernorm_kernel<XB, kTpr, 4, R>, grid, kCta, 0, s, a);  // (an error is seen below)
     };
     switch (row_threads(a.d, 4)) {
@@ -743,7 +743,7 @@ cudaError_t forward(const LayernormArgs& a, int sm_count, cudaStream_t s) {
 int backward_parts(int T, int d, int sm_count) {
     if (d > kBackwardMax) return std::min(T, sm_count);
     const int tpr = row_threads(d, 1), cta = tpr >= kAheadMin ? tpr : back_cta(tpr), rows = cta / tpr;
-    return std::min((T + rows - 1) / rows, sm_count * (1024 / cta));
+    return (int)std::min(((long long)T + rows - 1) / rows, (long long)sm_count * (1024 / cta));
 }
 
 cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {

@@ -217,3 +217,10 @@ def test_grouped_gradients_beyond_2_31_elements_of_the_rows(d, N):
         one = wgrad_ref([part.stop - part.start], A[part], dY[part])
         ref, mag = one if r == 0 else (ref + one[0], mag + one[1])
     check(dW[3:], ref, mag, mma_rounds(counts[3]), "dW")
+
+
+@pytest.mark.parametrize("d,ctas", [(16, 1), (512, 2), (1040, 4), (8192, 1), (16384, 1)])
+def test_scratch_of_as_many_rows_as_a_plan_takes(sms, d, ctas):
+    """Partial sums of the CTAs that are resident, however many rows there are."""
+    for T in (1 << 20, (1 << 31) - 1):
+        assert binding.moe_plan(T, d, 1, 1, 256).scratch_bytes == sms * ctas * 2 * d * 4
