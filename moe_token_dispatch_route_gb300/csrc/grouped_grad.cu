@@ -203,10 +203,15 @@ struct Shape {
           p_box(t.boxes & 0xFF), q_box(t.boxes >> 8 & 0xFF), q_paired(t.boxes >> 16 != 0) {}
 };
 
+// v / step, rounded up, for every v that an int holds
+__host__ __device__ constexpr int steps_of(int v, int step) { return (int)(((unsigned)v + (unsigned)step - 1u) / (unsigned)step); }
+static_assert(steps_of(0, 64) == 0 && steps_of(64, 64) == 1 && steps_of(65, 64) == 2 && steps_of(0x7FFFFFFF, 256) == 1 << 23,
+              "rounded up");
+
 // k-blocks of a reduction, and of each of its pieces
 template <Form F>
 __device__ __forceinline__ int blocks_of(const GradParams& p, int rows) {
-    return ((Cfg<F>::kWeight ? rows : p.a.N) + kTileK - 1) / kTileK;
+    return steps_of(Cfg<F>::kWeight ? rows : p.a.N, kTileK);
 }
 template <Form F>
 __device__ __forceinline__ int piece_blocks(int nkb, int limit) {
@@ -912,7 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         int run = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < E ? (off[e + 1] - off[e] + C::kRowTile - 1) / C::kRowTile : 0;
+            const int n = e < E ? steps_of(off[e + 1] - off[e], C::kRowTile) : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
