@@ -63,6 +63,10 @@ class MoeTrainLayer:
 
     def _forward(self, x, gamma, beta, W_r, W1, W2):
         u, r = self.up, self.bufs
+        # the forward calls take the weights by address alone: one of another type or size would be misread
+        for name, w, n in (("W_r", W_r, self.d * self.E), ("W1", W1, self.E * self.d * 2 * self.F),
+                           ("W2", W2, self.E * self.F * self.d)):
+            b._arg("MoeTrainLayer.forward", u, name, w, n, b._IS_BF16)
         b.moe_layernorm(u, x, gamma, beta, self.eps, self.y, self.mean, self.rstd)
         b.moe_router_logits(u, self.y, W_r, None, self.logits)
         b.route(u, self.logits, r)
