@@ -571,6 +571,7 @@ MOE_API moe_status_t moe_grouped_gemm_dgrad(moe_plan_t plan, const uint16_t* dY,
  *   offsets in:  int32 [E+1] from moe_route.
  *   dW      out: [E][d][N] of dw_dtype.  An expert without rows gets zeros.
  *   accumulate in: 1: dW += (fp32 only, MOE_ERR_UNSUPPORTED otherwise); 0: dW =.
+ *                The addition may take values below 2^-126 in magnitude, of dW or of the sum, as zeros.
  * T = 0 writes zeros (accumulate: nothing).  Workspace, status, invalid offsets
  * and launches as for moe_grouped_gemm_dgrad.
  */

@@ -801,7 +801,7 @@ __device__ void epilogue_role(const GradParams& p, GradCtl* ctl, uint32_t tmem, 
         } else if (add) {
             // Added in L2, once for each element, so in no order that could change: to read the sums first takes these
             // warps a round trip a tile (64 experts of 64 rows, 4096 x 1536: 693 us, 596 added in L2; 2048
-            // rows, 4096 x 14336: 1376 and 1321).
+            // rows, 4096 x 14336: 1376 and 1321).  The reduction takes subnormal values as zeros.
             walk_rows<kRows, 1>(at, pitch, mine, [&](uint8_t* at, int i, int n) {
                 if (n > 0) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at), "f"(__uint_as_float(sum[i / 32][i % 32])) : "memory");
             });
@@ -1082,7 +1082,8 @@ cudaError_t launch(GradParams& p, const GroupedGradArgs& a, bool may_split, int 
 
 // Row tiles of 64 where that is an expert's mean or more: the ten stages in flight read the weights faster (64
 // experts of 2048 x 2048 with 64 rows each: 92 us, 94 in tiles of 256; with 8 rows 86 and 89), and with more rows
-// they are read twice (80 rows: 118 and 96).
+// they are read twice (80 rows: 118 and 96).  These are equal loads: the mean decides for all experts, and one with more than
+// 64 rows beside many with few reads its weights once for each 64 of them.
 bool narrow_rows(long long S, int E) { return S <= 64LL * E; }
 // Whether an input (weight) gradient of this shape may have fewer tiles than pairs of CTAs and a reduction long
 // enough to be split.

@@ -5,7 +5,9 @@
 //   dx = rstd (v - sum v / d - xh (sum v xh) / d) + dres,
 //   dgamma = sum_t dy xh,  dbeta = sum_t dy.
 // All sums are fp32.  Both directions are bound by HBM: each input is read once and stays in
-// registers between the sums over a row and the row's result.
+// registers between the sums over a row and the row's result.  Wider rows do not fit: above 32768 columns the forward
+// kernel reads a row three times, and above 16384 the backward pass reads x and dy twice for dx and once more
+// for dgamma and dbeta (the repeats within a row come from L2).
 //
 // A row is held by TPR threads (a power of two from 8 to 1024), VPT vectors of 8 columns each, so
 // that the sums are one shuffle tree and, above a warp, one exchange through shared memory.  The

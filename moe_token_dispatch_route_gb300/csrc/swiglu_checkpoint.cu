@@ -30,7 +30,8 @@ constexpr int kLanes = kCkptBlock / 8;      // 16 threads of 8 columns share a b
 constexpr float kMinAmax = 3.7615819e-37f;  // 2^-121: the smallest amax that is stored
 
 // 1 / (1 + e^-g) from e^-|g|, which does not overflow: far negative g keeps its small result.
-// The approximations are within a few units of 2^-24, far below the rounding to bf16 that follows.
+// The exponential is within 2 + 1.173 |g| units in its last place and the quotient within 2: 2e-6 of the result at
+// |g| = 10, 1.2e-5 at 80, below the 2^-9 of the rounding to bf16 that follows.
 __device__ __forceinline__ float sigmoid(float g) {
     const float e = __expf(-fabsf(g));
     return __fdividef(g >= 0.f ? 1.f : e, 1.f + e);
