@@ -4,9 +4,9 @@
 
 with Mixtral-style gates (softmax over the k chosen logits).  Between the two passes it keeps the
 dispatched rows, the up projection's outputs in 8 bits, the experts' outputs and the routing; H is
-computed again from the 8-bit values.  The router's own two products ([T, d] by [d, E]) and the
-gates' softmax over k values are PyTorch's.  Nothing is recorded for automatic differentiation: inputs and weights may
-require gradients, results do not.
+computed again from the 8-bit values.  The router's two gradient products ([T, d] by [d, E]) and the
+gates' softmax gradient over k values are PyTorch's.  Nothing is recorded for automatic differentiation: inputs
+and weights may require gradients, results do not.
 """
 from __future__ import annotations
 
@@ -21,8 +21,9 @@ class MoeTrainLayer:
     """Plans and device buffers of a layer of T tokens of width d, E experts of hidden width F, k
     experts a token; d and F are multiples of 16.  x: fp32 [T, d].  Weights: W_r bf16 [d, E], W1 bf16
     [E, d, 2F] (gate columns, then up), W2 bf16 [E, F, d], gamma and beta fp32 [d]; their gradients
-    are fp32.  `stream`: a torch stream or a raw handle; None is the current one; results belong to it.  The buffers belong to the
-    stream that is current when the layer is made: keep the layer until its passes on other streams are done."""
+    are fp32.  `stream`: a torch stream or a raw handle; None is the current one; results belong to it.
+    The buffers belong to the stream that is current when the layer is made: keep the layer until its
+    passes on other streams are done."""
 
     def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0):
         self.T, self.d, self.F, self.E, self.k, self.eps = T, d, F, E, k, eps
