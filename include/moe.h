@@ -580,6 +580,149 @@ MOE_API moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, 
                                             int32_t accumulate, void* workspace, int32_t* dev_status,
                                             void* stream);
 
+/* ------------------------------------------------------- 8-bit forward pass
+ *
+ * The layer's forward pass with its activations and weights in 8-bit floating point (e4m3), for
+ * serving.  With `up` the plan of the gate and up projections (N = 2F) and `down` the plan of the down
+ * projection (d = F, N = the model's width, out_dtype bf16):
+ *   once      moe_quantize_weights(up, halves 2), moe_quantize_weights(down, halves 1)
+ *   forward   moe_rmsnorm(up) -> h, y, codes;  moe_router_logits(y), moe_route,
+ *             moe_grouped_gemm_fp8_swiglu(up; codes, perm) -> H,
+ *             moe_grouped_gemm_fp8(down; H, perm NULL) -> Y,  moe_combine(down) -> out,
+ *             which the next layer's moe_rmsnorm adds to h.
+ * 8-bit storage.  e4m3 codes (1 byte: sign, 4 exponent and 3 mantissa bits; largest value 448) and
+ * one fp32 scale for each block of 128 columns of a row (of weights: 128 x 128); a stored value is code * scale.
+ * With amax the block's largest magnitude,
+ *   scale = amax / 448,  code = round(x * (448 / amax)),
+ * every operation rounded to fp32, round to the nearest e4m3 value (even on ties).  A block whose amax is below
+ * 2^-117 gets scale 0 and codes 0.  A block that holds an infinity or a NaN gets scale NaN and codes 0: it is
+ * restored as NaN throughout.  The last block of a row may be shorter.
+ * The conventions at the top of this file and of the training operators hold.
+ */
+
+/*
+ * moe_rmsnorm -- the residual's addition and the root-mean-square norm of the plan's T token rows of width d:
+ *   h = x + res,  rstd = 1 / sqrt(sum h^2 / d + eps),  y = h * rstd * gamma.
+ *   x       in:  [T][d] of x_dtype.
+ *   res     in:  [T][d] of h_dtype, or NULL: h = x, and h_dtype must be x_dtype.
+ *   gamma   in:  fp32 [d], or NULL for ones.
+ *   eps     in:  > 0, finite.
+ *   h       out: [T][d] of h_dtype: the sum in fp32, rounded once; the norm is of these values.  Must be there
+ *                with res (and may be res); without res it may be NULL, and is a copy of x otherwise.
+ *   y       out: bf16 [T][d], rounded once; or NULL.
+ *   codes   out: e4m3 [T][d], 16-byte aligned, of y before it is rounded; or NULL (with scales).
+ *   scales  out: fp32 [T][ceil(d / 128)]; or NULL (with codes).  y and codes may not both be NULL.
+ *   rstd    out: fp32 [T], or NULL (inference).
+ * A row that holds an infinity or a NaN gives NaN.  No output may overlap an input or another output (but h may be res).
+ * Launches one kernel.
+ */
+MOE_API moe_status_t moe_rmsnorm(moe_plan_t plan, const void* x, int32_t x_dtype, const void* res, int32_t h_dtype,
+                                 const float* gamma, float eps, void* h, uint16_t* y, uint8_t* codes, float* scales,
+                                 float* rstd, void* stream);
+
+/*
+ * moe_rmsnorm_backward -- the gradient of moe_rmsnorm with respect to h (that of x and of res alike).  With
+ * hh = h * rstd and v = dy * gamma,
+ *   dx = rstd * (v - hh * sum(v * hh) / d) + dres,  dgamma = sum over the rows of dy * hh.
+ *   dy      in:  [T][d] of dy_dtype, the gradient of y.
+ *   h, rstd in:  from the forward call; gamma as there.
+ *   dres    in:  [T][d] of h_dtype: a gradient to add (of the later uses of h), or NULL.  May be dx itself.
+ *   dx      out: [T][d] of h_dtype.  May not overlap dy or h.
+ *   dgamma  out: fp32 [d], or NULL.
+ *   scratch in/out: moe_backward_scratch; may be NULL when dgamma is.  MOE_ERR_WORKSPACE if it is missing or misaligned.
+ * T = 0 writes zeros to dgamma.  Launches as moe_layernorm_backward does.
+ */
+MOE_API moe_status_t moe_rmsnorm_backward(moe_plan_t plan, const void* dy, int32_t dy_dtype, const void* h, int32_t h_dtype,
+                                          const float* gamma, const float* rstd, const void* dres, void* dx, float* dgamma,
+                                          void* scratch, void* stream);
+
+/*
+ * moe_quantize_weights -- the plan's expert weights in 8 bits, transposed for the 8-bit product.
+ *   W       in:  bf16 [E][d][N].
+ *   halves  in:  1; or 2 for a gated up projection, N = 2F: blocks of 128 columns are counted from the first column
+ *                of each half (MOE_ERR_UNSUPPORTED unless N is a multiple of 32).
+ *   codes   out: e4m3 [E][N][d].
+ *   scales  out: fp32 [E][halves * ceil(N / halves / 128)][ceil(d / 128)], one for 128 rows of codes by 128 columns.
+ * Launches one kernel.
+ */
+MOE_API moe_status_t moe_quantize_weights(moe_plan_t plan, const uint16_t* W, int32_t halves, uint8_t* codes, float* scales,
+                                          void* stream);
+
+/*
+ * moe_grouped_gemm_fp8 -- the per-expert product on 8-bit rows and weights:
+ *   Y[i][n] = sum over blocks b of  A_scales[r][b] * W_scales[e(i)][n / 128][b] * (A[r] . W[e(i)][n] over block b),
+ * r = i, or perm[i] / k.  The products of a block are summed in fp32 by the tensor cores, the blocks' sums in fp32.
+ *   A        in:  e4m3 codes: [S][d] in destination order, or [T][d] with perm.
+ *   A_scales in:  fp32 [S or T][ceil(d / 128)].  The product of a row's and a weight block's scale is formed first.
+ *   perm     in:  int32 [S] from moe_route: the rows are gathered from the token rows; or NULL.
+ *   offsets  in:  int32 [E+1] from moe_route.
+ *   W, W_scales in: from moe_quantize_weights with halves 1.
+ *   Y        out: [S][N] in the plan's out_dtype.
+ * Workspace and status as for moe_grouped_gemm.  Offsets that are not an ascending list from 0 to S write
+ * MOE_ERR_DEVICE to dev_status and nothing to Y.  Launches one kernel.
+ */
+MOE_API moe_status_t moe_grouped_gemm_fp8(moe_plan_t plan, const uint8_t* A, const float* A_scales, const int32_t* perm,
+                                          const int32_t* offsets, const uint8_t* W, const float* W_scales, void* Y,
+                                          void* workspace, int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_gemm_fp8_swiglu -- moe_grouped_gemm_fp8 for a gated up projection, its result back in 8 bits: with g and u
+ * the gate and up halves of Y's row, H = silu(g) * u in fp32, stored as e4m3 codes and scales.
+ *   W1, W1_scales in: from moe_quantize_weights with halves 2 (the plan's N = 2F, a multiple of 32:
+ *                 MOE_ERR_UNSUPPORTED otherwise).
+ *   H         out: e4m3 [S][F], 16-byte aligned.
+ *   H_scales  out: fp32 [S][ceil(F / 128)].
+ * Other arguments as for moe_grouped_gemm_fp8 (the plan's out_dtype does not apply).  Launches one kernel.
+ */
+MOE_API moe_status_t moe_grouped_gemm_fp8_swiglu(moe_plan_t plan, const uint8_t* A, const float* A_scales,
+                                                 const int32_t* perm, const int32_t* offsets, const uint8_t* W1,
+                                                 const float* W1_scales, uint8_t* H, float* H_scales, void* workspace,
+                                                 int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------ router's losses
+ *
+ * moe_balance_loss, moe_router_backward -- the auxiliary losses of the router and the gradient of its logits.
+ * The T tokens are cut into G groups (sequences) of seq_len, the last one maybe shorter; seq_len 0 is one group of all.
+ * Tokens whose mask is 0 (padding) count in no sum.  With p[t] a token's scores in sum 1 over all E experts (softmax of
+ * its logits; with MOE_ROUTE_SIGMOID in the plan's route_flags the logistics divided by their sum), n[g] the counted
+ * tokens of group g, load[g][e] how many of its picks are expert e, and N all counted tokens:
+ *   loss[0] = balance / G * sum over g of  E / (k n[g]^2) * sum_e load[g][e] * sum over g's tokens of p[t][e]
+ *             (a group whose load and scores are uniform adds balance / G; one without counted tokens adds 0),
+ *   loss[1] = z / N * sum over the counted tokens of lse[t]^2,  lse = log sum_e exp(logit).
+ * Logits of masked experts may be -infinity or the type's lowest value, but not all of a row's.
+ *
+ * moe_balance_scratch -- bytes of device scratch that moe_balance_loss needs (256-byte aligned; nothing is kept in it
+ * from call to call; calls that share one must be ordered on one stream).  Host only.
+ *
+ * moe_balance_loss
+ *   logits   in:  fp32 [T][E].
+ *   topk_idx in:  int32 [T][k] from moe_route (a token's picks are distinct; one outside [0, E) is not counted).
+ *   mask     in:  uint8 [T], 0: the token does not count; or NULL.
+ *   balance, z in: the losses' coefficients, finite (0: the loss is 0).
+ *   loss     out: fp32 [2].
+ *   load     out: int32 [G][E], the counted picks.
+ *   tokens   out: int32 [G + 1], n[g] and at last N.
+ * Launches one to three kernels.  The same bits on every run.
+ */
+MOE_API moe_status_t moe_balance_scratch(moe_plan_t plan, int32_t seq_len, size_t* bytes);
+MOE_API moe_status_t moe_balance_loss(moe_plan_t plan, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                                      int32_t seq_len, float balance, float z, float* loss, int32_t* load, int32_t* tokens,
+                                      void* scratch, void* stream);
+
+/*
+ * moe_router_backward -- dlogits = the gradient of loss[0] + loss[1] + sum topk_w * dtopk_w, load taken as constant and
+ * topk_w as moe_route computes it under the plan's route_flags.
+ *   dtopk_w  in:  fp32 [T][k] (moe_combine_backward's), of masked tokens too; or NULL: the losses alone.
+ *   load, tokens in: from moe_balance_loss with the same mask and seq_len; load may be NULL when balance is 0, tokens
+ *                when balance and z are.
+ *   dlogits  out: fp32 [T][E].
+ * With SIGMOID | RENORM a token whose chosen logits are all below about -87 gets NaN, as its gates do.
+ * Launches one kernel.
+ */
+MOE_API moe_status_t moe_router_backward(moe_plan_t plan, const float* logits, const int32_t* topk_idx,
+                                         const float* dtopk_w, const uint8_t* mask, int32_t seq_len, float balance, float z,
+                                         const int32_t* load, const int32_t* tokens, float* dlogits, void* stream);
+
 /* Static string naming a status code. */
 MOE_API const char* moe_status_string(moe_status_t status);
 

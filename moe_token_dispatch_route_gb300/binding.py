@@ -71,7 +71,9 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_plan_info", "moe_route", "moe_d
             "moe_grouped_gemm", "moe_gather_gemm", "moe_set_trace", "moe_dispatch_gemm_combine",
             "moe_backward_scratch", "moe_layernorm", "moe_layernorm_backward", "moe_swiglu_checkpoint",
             "moe_swiglu_checkpoint_backward", "moe_combine_backward", "moe_grouped_gemm_dgrad",
-            "moe_grouped_gemm_wgrad")
+            "moe_grouped_gemm_wgrad", "moe_rmsnorm", "moe_rmsnorm_backward", "moe_quantize_weights",
+            "moe_grouped_gemm_fp8", "moe_grouped_gemm_fp8_swiglu", "moe_balance_scratch", "moe_balance_loss",
+            "moe_router_backward")
 
 
 def load_library(path: str = LIB_PATH):
@@ -124,7 +126,15 @@ def load_library(path: str = LIB_PATH):
     lib.moe_combine_backward.argtypes = [VP, VP, I32] + [VP] * 6
     lib.moe_grouped_gemm_dgrad.argtypes = [VP] * 5 + [I32] + [VP] * 3
     lib.moe_grouped_gemm_wgrad.argtypes = [VP] * 5 + [I32, I32] + [VP] * 3
-    for name in EXPORTED[-8:]:  # the training operators
+    lib.moe_rmsnorm.argtypes = [VP, VP, I32, VP, I32, VP, F32] + [VP] * 6
+    lib.moe_rmsnorm_backward.argtypes = [VP, VP, I32, VP, I32] + [VP] * 7
+    lib.moe_quantize_weights.argtypes = [VP, VP, I32, VP, VP, VP]
+    lib.moe_grouped_gemm_fp8.argtypes = [VP] * 11
+    lib.moe_grouped_gemm_fp8_swiglu.argtypes = [VP] * 12
+    lib.moe_balance_scratch.argtypes = [VP, I32, P(ctypes.c_size_t)]
+    lib.moe_balance_loss.argtypes = [VP] * 4 + [I32, F32, F32] + [VP] * 5
+    lib.moe_router_backward.argtypes = [VP] * 5 + [I32, F32, F32] + [VP] * 4
+    for name in EXPORTED[-16:]:  # the training operators, the 8-bit forward pass and the router's losses
         getattr(lib, name).restype = I32
     lib.moe_status_string.argtypes = [I32]
     lib.moe_status_string.restype = ctypes.c_char_p
@@ -453,6 +463,149 @@ def moe_grouped_gemm_wgrad(plan: Plan, A, dY, offsets, dW, workspace, dev_status
         _arg(c, plan, "dW", dW, plan.E * plan.d * N, _IS_EITHER), _DTYPES[dW.dtype], int(accumulate),
         _buf(c, plan, "workspace", workspace, plan.workspace_bytes), _buf(c, plan, "dev_status", dev_status, 16),
         _stream(stream, plan.device)), c)
+
+
+# ---------------------------------------------------------------- 8-bit forward pass
+
+_IS_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def scale_blocks(n: int) -> int:
+    """Scales of n columns stored in 8 bits: blocks of 128."""
+    return (n + 127) // 128
+
+
+def moe_rmsnorm(plan: Plan, x, res, gamma, eps: float, h, y, codes=None, scales=None, rstd=None, stream=None) -> None:
+    """h = x + res, y = h rstd gamma over the plan's T rows of width d; y in bf16 and (or) in 8 bits as e4m3 codes
+    [T][d] and fp32 scales [T][scale_blocks(d)].  res, gamma, y or codes and scales, and rstd may be None; h may be res, and
+    None without one."""
+    c = "moe_rmsnorm"
+    d, T = plan.d, plan.T
+    n = T * d
+    px = _arg(c, plan, "x", x, n, _IS_EITHER)
+    kind = (x.dtype,) if res is None else _IS_EITHER
+    ph = _opt(c, plan, "h", h, n, kind) if res is None else _arg(c, plan, "h", h, n, kind)
+    hd = x.dtype if h is None else h.dtype
+    _check(load_library().moe_rmsnorm(
+        plan.handle, px, _DTYPES[x.dtype], _opt(c, plan, "res", res, n, (hd,)), _DTYPES[hd],
+        _opt(c, plan, "gamma", gamma, d, _IS_F32), eps, ph, _opt(c, plan, "y", y, n, _IS_BF16),
+        _opt(c, plan, "codes", codes, n, _IS_E4M3), _opt(c, plan, "scales", scales, T * scale_blocks(d), _IS_F32),
+        _opt(c, plan, "rstd", rstd, T, _IS_F32), _stream(stream, plan.device)), c)
+
+
+def moe_rmsnorm_backward(plan: Plan, dy, h, gamma, rstd, dres, dx, dgamma, scratch, stream=None) -> None:
+    """Gradient of moe_rmsnorm with respect to h; dres (added to dx), gamma and dgamma may be None."""
+    c = "moe_rmsnorm_backward"
+    d, T = plan.d, plan.T
+    n = T * d
+    ph = _arg(c, plan, "h", h, n, _IS_EITHER)
+    _check(load_library().moe_rmsnorm_backward(
+        plan.handle, _arg(c, plan, "dy", dy, n, _IS_EITHER), _DTYPES[dy.dtype], ph, _DTYPES[h.dtype],
+        _opt(c, plan, "gamma", gamma, d, _IS_F32), _arg(c, plan, "rstd", rstd, T, _IS_F32),
+        _opt(c, plan, "dres", dres, n, (h.dtype,)), _arg(c, plan, "dx", dx, n, (h.dtype,)),
+        _opt(c, plan, "dgamma", dgamma, d, _IS_F32),
+        None if dgamma is None else _buf(c, plan, "scratch", scratch, plan.scratch_bytes), _stream(stream, plan.device)), c)
+
+
+def _weight_scales(plan: Plan, halves: int) -> int:
+    return plan.E * halves * scale_blocks(plan.N // halves) * scale_blocks(plan.d)
+
+
+def moe_quantize_weights(plan: Plan, W, codes, scales, halves: int = 1, stream=None) -> None:
+    """W bf16 [E][d][N] as e4m3 codes [E][N][d] and fp32 scales [E][halves * scale_blocks(N / halves)][scale_blocks(d)];
+    halves is 2 for the gate and up projections of a gated layer."""
+    c = "moe_quantize_weights"
+    n = plan.E * plan.d * plan.N
+    if halves not in (1, 2):
+        raise ValueError(f"{c}: halves is 1 or 2, got {halves}")
+    _check(load_library().moe_quantize_weights(
+        plan.handle, _arg(c, plan, "W", W, n, _IS_BF16), halves, _arg(c, plan, "codes", codes, n, _IS_E4M3),
+        _arg(c, plan, "scales", scales, _weight_scales(plan, halves), _IS_F32), _stream(stream, plan.device)), c)
+
+
+def _fp8_operands(c: str, plan: Plan, A, A_scales, perm, offsets, W, W_scales, halves: int) -> list:
+    rows = plan.S if perm is None else plan.T
+    return [_arg(c, plan, "A", A, rows * plan.d, _IS_E4M3),
+            _arg(c, plan, "A_scales", A_scales, rows * scale_blocks(plan.d), _IS_F32),
+            _opt(c, plan, "perm", perm, plan.S, _IS_I32), _arg(c, plan, "offsets", offsets, plan.E + 1, _IS_I32),
+            _arg(c, plan, "W", W, plan.E * plan.d * plan.N, _IS_E4M3),
+            _arg(c, plan, "W_scales", W_scales, _weight_scales(plan, halves), _IS_F32)]
+
+
+def moe_grouped_gemm_fp8(plan: Plan, A, A_scales, perm, offsets, W, W_scales, Y, workspace, dev_status, stream=None) -> None:
+    """Per-expert product on 8-bit rows and weights: Y[i] = A[r] W[e(i)]^T, r = i or (with perm) the row's token."""
+    c = "moe_grouped_gemm_fp8"
+    _check(load_library().moe_grouped_gemm_fp8(
+        plan.handle, *_fp8_operands(c, plan, A, A_scales, perm, offsets, W, W_scales, 1),
+        _arg(c, plan, "Y", Y, plan.S * plan.N, _out_dtype(plan)),
+        _buf(c, plan, "workspace", workspace, plan.workspace_bytes), _buf(c, plan, "dev_status", dev_status, 16),
+        _stream(stream, plan.device)), c)
+
+
+def moe_grouped_gemm_fp8_swiglu(plan: Plan, A, A_scales, perm, offsets, W1, W1_scales, H, H_scales, workspace, dev_status,
+                                stream=None) -> None:
+    """moe_grouped_gemm_fp8 for gate and up projections: H = silu(gate) * up as e4m3 codes [S][F] and fp32 scales
+    [S][scale_blocks(F)]."""
+    c = "moe_grouped_gemm_fp8_swiglu"
+    F = plan.N // 2
+    _check(load_library().moe_grouped_gemm_fp8_swiglu(
+        plan.handle, *_fp8_operands(c, plan, A, A_scales, perm, offsets, W1, W1_scales, 2),
+        _arg(c, plan, "H", H, plan.S * F, _IS_E4M3), _arg(c, plan, "H_scales", H_scales, plan.S * scale_blocks(F), _IS_F32),
+        _buf(c, plan, "workspace", workspace, plan.workspace_bytes), _buf(c, plan, "dev_status", dev_status, 16),
+        _stream(stream, plan.device)), c)
+
+
+# ---------------------------------------------------------------- router's losses
+
+_IS_MASK = (torch.bool, torch.uint8)
+
+
+def loss_groups(plan: Plan, seq_len: int) -> int:
+    """Groups of tokens that the balance loss is taken over: sequences of seq_len, or (0) all tokens."""
+    if not 0 <= seq_len < 1 << 31:
+        raise ValueError(f"seq_len must be 0 or a number of tokens, got {seq_len}")
+    return max(1, -(-plan.T // seq_len)) if seq_len else 1
+
+
+def _balance_scratch_bytes(plan: Plan, seq_len: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_balance_scratch(plan.handle, seq_len, ctypes.byref(n)), "moe_balance_scratch")
+    return n.value
+
+
+def balance_scratch(plan: Plan, seq_len: int = 0, device=None) -> torch.Tensor:
+    """Scratch of moe_balance_loss (the caller keeps it, like the workspace)."""
+    return torch.zeros(_balance_scratch_bytes(plan, seq_len), dtype=torch.uint8,
+                       device=torch.device("cuda", plan.device) if device is None else device)
+
+
+def moe_balance_loss(plan: Plan, logits, topk_idx, mask, seq_len: int, balance: float, z: float, loss, load, tokens, scratch,
+                     stream=None) -> None:
+    """loss[0], loss[1]: the router's balance loss over sequences of seq_len tokens (0: all in one) and its z loss, times
+    their coefficients; load int32 [groups][E]: counted picks; tokens int32 [groups + 1]: counted tokens, at last all.
+    mask (bool or uint8 [T], 0: the token does not count) may be None."""
+    c = "moe_balance_loss"
+    G = loss_groups(plan, seq_len)
+    _check(load_library().moe_balance_loss(
+        plan.handle, _arg(c, plan, "logits", logits, plan.T * plan.E, _IS_F32),
+        _arg(c, plan, "topk_idx", topk_idx, plan.S, _IS_I32), _opt(c, plan, "mask", mask, plan.T, _IS_MASK), seq_len,
+        balance, z, _arg(c, plan, "loss", loss, 2, _IS_F32), _arg(c, plan, "load", load, G * plan.E, _IS_I32),
+        _arg(c, plan, "tokens", tokens, G + 1, _IS_I32),
+        _buf(c, plan, "scratch", scratch, _balance_scratch_bytes(plan, seq_len)), _stream(stream, plan.device)), c)
+
+
+def moe_router_backward(plan: Plan, logits, topk_idx, dtopk_w, mask, seq_len: int, balance: float, z: float, load, tokens,
+                        dlogits, stream=None) -> None:
+    """dlogits of the losses (load and tokens from moe_balance_loss; None where their coefficients are 0) and, with
+    dtopk_w, of the gates."""
+    c = "moe_router_backward"
+    G = loss_groups(plan, seq_len)
+    n = plan.T * plan.E
+    _check(load_library().moe_router_backward(
+        plan.handle, _arg(c, plan, "logits", logits, n, _IS_F32), _opt(c, plan, "topk_idx", topk_idx, plan.S, _IS_I32),
+        _opt(c, plan, "dtopk_w", dtopk_w, plan.S, _IS_F32), _opt(c, plan, "mask", mask, plan.T, _IS_MASK), seq_len,
+        balance, z, _opt(c, plan, "load", load, G * plan.E, _IS_I32), _opt(c, plan, "tokens", tokens, G + 1, _IS_I32),
+        _arg(c, plan, "dlogits", dlogits, n, _IS_F32), _stream(stream, plan.device)), c)
 
 
 def moe_read_status(dev_status, stream=None) -> tuple[int, list[int]]:

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["moe_api.cu", "route.cu", "dispatch_gemm.cu", "route_noalloc.cu", "combine.cu", "router.cu",
-           "train_api.cu", "layernorm.cu", "swiglu_checkpoint.cu", "combine_backward.cu", "grouped_grad.cu"]
+           "train_api.cu", "layernorm.cu", "swiglu_checkpoint.cu", "combine_backward.cu", "grouped_grad.cu",
+           "serve_api.cu", "rmsnorm.cu", "quantize_weights.cu", "grouped_fp8.cu", "router_losses.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -4,6 +4,7 @@
 // and, with xh = (x - mean) rstd and v = dy gamma,
 //   dx = rstd (v - sum v / d - xh (sum v xh) / d) + dres,
 //   dgamma = sum_t dy xh,  dbeta = sum_t dy.
+// Without a mean (a null pointer in the backward pass) it is the RMS norm's: mean = 0, and the term sum v / d is left out.
 // All sums are fp32.  Both directions are bound by HBM: each input is read once and stays in
 // registers between the sums over a row and the row's result.  Wider rows do not fit: above 32768 columns the forward
 // kernel reads a row three times, and above 16384 the backward pass reads x and dy twice for dx and once more
@@ -265,7 +266,7 @@ struct SumsOut {
     __device__ explicit SumsOut(const LayernormBackwardArgs& a) {
         float* part = a.partial + (size_t)blockIdx.x * 2 * a.d;
         dgamma = gridDim.x == 1 ? a.dgamma : part;
-        dbeta = gridDim.x == 1 ? a.dbeta : part + a.d;
+        dbeta = gridDim.x == 1 || !a.dbeta ? a.dbeta : part + a.d;
     }
 };
 
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
         if (live) {
             x.load(a.x, at);
             dy.load(a.dy, at);
-            mean = __ldg(a.mean + t);
+            mean = a.mean ? __ldg(a.mean + t) : 0.f;
             rstd = __ldg(a.rstd + t);
         } else {
             x.zero();
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(Back<TPR>::kCta, Back<TPR>::kCtasPerSm) layern
         // the two arrays of `red` alternate, so one barrier a row is enough
         row_sum<TPR, 2, B::kCta>(s, red[turn], [&] { group_barrier<TPR, B::kCta>(group); });
         if (!live) continue;
-        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+        const float m1 = a.mean ? s[0] * inv_d : 0.f, m2 = s[1] * inv_d;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[j], m2, v[j] - m1), res.get(j));
         store8<XB>(a.dx, at, v);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>
     weights8(mine ? a.gamma : nullptr, c, 1.f, gamma);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.f;
-    auto stats = [&](long long t) { return t < a.T ? make_float2(__ldg(a.mean + t), __ldg(a.rstd + t)) : make_float2(0.f, 0.f); };
+    auto stats = [&](long long t) { return t < a.T ? make_float2(a.mean ? __ldg(a.mean + t) : 0.f, __ldg(a.rstd + t)) : make_float2(0.f, 0.f); };
     float2 next = stats(first);
     __syncthreads();
     int turn = 0, stage = 0;
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(Ahead<DYB, XB, TPR>::kCta, Ahead<DYB, XB, TPR>
         row_sum<TPR, 2, B::kCta>(s, red[turn], ReadBarrier{res.bits()});
         if (threadIdx.x == 0) fetch(t + B::kStages * step, stage);
         if (mine) {
-            const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+            const float m1 = a.mean ? s[0] * inv_d : 0.f, m2 = s[1] * inv_d;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[j], m2, v[j] - m1), res.get(j));
             store8<XB>(a.dx, (size_t)t * a.d + c, v);
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const Layernor
     int turn = 0;
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const size_t row = (size_t)t * a.d;
-        const float mean = __ldg(a.mean + t), rstd = __ldg(a.rstd + t);
+        const float mean = a.mean ? __ldg(a.mean + t) : 0.f, rstd = __ldg(a.rstd + t);
         Raw<XB> x[VPT];
         Raw<DYB> dy[VPT];
         float s[2] = {0.f, 0.f};
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kTall, 1) layernorm_tall_kernel(const Layernor
             }
         }
         row_sum<kTall, 2, kTall>(s, red[turn], CtaBarrier());
-        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+        const float m1 = a.mean ? s[0] * inv_d : 0.f, m2 = s[1] * inv_d;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * kTall) * 8;
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_dx_kernel(const Layernor
     int turn = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const size_t row = (size_t)t * a.d;
-        const float mean = __ldg(a.mean + t), rstd = __ldg(a.rstd + t);
+        const float mean = a.mean ? __ldg(a.mean + t) : 0.f, rstd = __ldg(a.rstd + t);
         float s[2] = {0.f, 0.f};
         for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8], x[8], g[8];
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kWide) layernorm_wide_dx_kernel(const Layernor
             }
         }
         row_sum<kWide, 2, kWide>(s, red[turn], CtaBarrier());
-        const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+        const float m1 = a.mean ? s[0] * inv_d : 0.f, m2 = s[1] * inv_d;
         for (int c = threadIdx.x * 8; c < a.d; c += kWide * 8) {
             float v[8], x[8], g[8], r[8] = {};
             load8<DYB>(a.dy, row + c, v);
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(256) layernorm_wide_dweight_kernel(const Layer
                                  : static_cast<const float*>(a.dy)[i];
             const float x = XB ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.x)[i] << 16)
                                : static_cast<const float*>(a.x)[i];
-            g = fmaf(dy, (x - __ldg(a.mean + t)) * __ldg(a.rstd + t), g);
+            g = fmaf(dy, (x - (a.mean ? __ldg(a.mean + t) : 0.f)) * __ldg(a.rstd + t), g);
             b += dy;
         }
     }
@@ -749,7 +750,8 @@ int backward_parts(int T, int d, int sm_count) {
 }
 
 cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
-    return launch_after(layernorm_join_kernel, 2 * a.d / 32, kJoin, 0, s, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
+    // (without dbeta its half of the columns is neither there nor read)
+    return launch_after(layernorm_join_kernel, a.dbeta ? 2 * a.d / 32 : (a.d + 31) / 32, kJoin, 0, s, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
 }
 
 // Launches a kernel whose shared memory may be over the default limit of 48 KB, the static part included;

@@ -12,7 +12,7 @@
 
 #include "moe.h"
 #include "moe_internal.cuh"
-#include "train.cuh"
+#include "serve.cuh"
 
 using namespace moe;
 
@@ -163,6 +163,30 @@ bool map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
 
 bool map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     return encode_bf16_chunks(map, base, rows, cols, box_rows);
+}
+
+bool map_e4m3_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols};
+    cuuint32_t box[2] = {kScaleBlock, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_e4m3_weights(CUtensorMap* map, const void* base, uint64_t E, uint64_t halves, uint64_t n, uint64_t cols) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {cols, n, halves, E};
+    cuuint64_t strides[3] = {cols, n * cols, halves * n * cols};
+    cuuint32_t box[4] = {kScaleBlock, kScaleBlock, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool plan_view(moe_plan_t plan, PlanView* v) {

@@ -1,0 +1,424 @@
+// The router's losses and the gradient of its logits.
+// Tokens are cut into groups (sequences) of seq_len; masked tokens count nowhere.  With p the token's scores in sum 1
+// (softmax, or logistic scores over their sum), n the group's counted tokens and load[e] its picks of expert e:
+//   balance loss  b / G  sum_g E / (k n^2) sum_e load[e] sum_t p[t][e]
+//   z loss        z / N  sum_t lse_t^2,   lse = log sum_e exp(logit),  N all counted tokens
+// and, with w_e = b E load[e] / (G k n^2), the gradient of a counted token's logits
+//   softmax:  p_e (w_e - sum_j p_j w_j),   logistic: the same times 1 - s_e,   + 2 z lse / N softmax_e
+// plus the gates': topk_w as the routing computes it from the picks' logits, times dtopk_w.
+// Bound by HBM (the logits are read once a direction, dlogits written once) and by launch latency when small.
+//
+// A token is held by 8 to 32 lanes, VPL experts each; its sums are shuffles.  A CTA stays within one group, so
+// the forward pass keeps its experts' score sums in registers over all its tokens and the backward pass its w_e.  The
+// CTAs' sums are joined in their order by a second kernel (a third joins the groups).
+#include <algorithm>
+#include <type_traits>
+
+#include "moe_internal.cuh"
+#include "serve.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kRouterThreads = 256, kRouterWarps = kRouterThreads / 32;
+
+// How a call's tokens are shared out: `chunks` CTAs a group, `chunk` tokens each.
+struct Split {
+    int chunk, chunks;
+    long long blocks;
+};
+Split split_of(int T, int E, int seq_len, int groups, int sm_count) {
+    const int per_pass = kRouterWarps * (E <= 8 ? 4 : E <= 16 ? 2 : 1);  // tokens that a CTA takes at a time
+    const long long want = std::max<long long>(2 * per_pass, ((long long)T + 4 * sm_count - 1) / (4 * sm_count));
+    Split s;
+    s.chunks = (int)std::max<long long>(1, (seq_len + want - 1) / want);
+    s.chunk = (seq_len + s.chunks - 1) / s.chunks;
+    s.blocks = (long long)groups * s.chunks;
+    return s;
+}
+
+// Scratch: balance and z sums of the groups, then (chunks > 1) each CTA's score sums, load, z sum and tokens.
+struct Partials {
+    float* group;  // [groups][2]
+    float* part;   // [blocks][2 E + 2]
+    __host__ __device__ Partials(const RouterLossArgs& a)
+        : group(static_cast<float*>(a.scratch)), part(static_cast<float*>(a.scratch) + 2 * (size_t)a.groups) {}
+};
+
+template <int GL>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = GL / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+template <int GL>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = GL / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// s = 1 / (1 + e^-l) and 1 - s from e^-|l|, which does not overflow: neither is the other's difference from 1, which
+// would lose a far logit's small one.  (expf, not the fast exponential: gradients are fp32 results, and that one is off
+// by 1.2 |x| units, 4e-6 of a gradient.)
+struct Logistic {
+    float s, rest;
+    __device__ explicit Logistic(float l) {
+        const float e = expf(-fabsf(l)), big = __fdividef(1.f, 1.f + e), small = e * big;
+        s = l >= 0.f ? big : small;
+        rest = l >= 0.f ? small : big;
+    }
+};
+
+// A token's scores, its lse (where wanted), in: logits (-inf past E).
+template <int GL, int VPL>
+__device__ __forceinline__ void scores(const float (&l)[VPL], bool sigmoid, bool want_lse, float (&s)[VPL], float& total, float& lse,
+                                       float& top, float& esum) {
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
+    top = lanes_max<GL>(top);
+    lse = 0.f;
+    esum = 0.f;
+    if (!sigmoid || want_lse) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            s[i] = expf(l[i] - top);
+            esum += s[i];
+        }
+        esum = lanes_sum<GL>(esum);
+        lse = top + logf(esum);
+        total = esum;
+    }
+    if (sigmoid) {
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            s[i] = Logistic(l[i]).s;
+            total += s[i];
+        }
+        total = lanes_sum<GL>(total);
+    }
+}
+
+// The loss of group g's balance, from its sums; called by one CTA.  `sums` are in shared memory.
+__device__ __forceinline__ void group_done(const RouterLossArgs& a, long long g, float dot, float z, int n) {
+    const float bal = n > 0 ? dot * ((float)a.E / ((float)a.k * (float)n * (float)n)) : 0.f;
+    a.tokens[g] = n;
+    const Partials pt(a);
+    if (a.groups == 1) {
+        a.tokens[1] = n;
+        a.loss[0] = a.balance * bal;
+        a.loss[1] = n > 0 ? a.z * (z / (float)n) : 0.f;
+    } else {
+        pt.group[2 * g] = bal;
+        pt.group[2 * g + 1] = z;
+    }
+}
+
+// Sum over a CTA, in every thread.
+__device__ __forceinline__ float cta_sum(float v, float (&red)[kRouterWarps]) {
+    v = lanes_sum<32>(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRouterWarps; ++i) v += red[i];
+    return v;
+}
+
+template <int GL, int VPL>
+__global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLossArgs a, Split sp) {
+    constexpr int kCols = GL * VPL;
+    __shared__ float sums[kRouterWarps][kCols];
+    __shared__ int hist[kCols];
+    __shared__ float red[kRouterWarps];
+    wait_for_kernel_before();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % GL;
+    const long long g = blockIdx.x / sp.chunks;
+    const int chunk = blockIdx.x % sp.chunks;
+    const long long t0 = g * a.seq_len + (long long)chunk * sp.chunk;
+    const long long t1 = min(min(t0 + sp.chunk, (g + 1) * (long long)a.seq_len), (long long)a.T);
+    for (int e = tid; e < kCols; e += kRouterThreads) hist[e] = 0;
+    __syncthreads();
+    float acc[VPL], z = 0.f;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+    constexpr int kPass = kRouterWarps * (32 / GL);
+    const bool sigmoid = a.sigmoid != 0, want = a.z != 0.f;
+    for (long long tw = t0 + warp * (32 / GL); tw < t1; tw += kPass) {
+        const long long t = tw + lane / GL;
+        const bool live = t < t1 && (!a.mask || a.mask[t]);
+        float l[VPL], s[VPL], total, lse, top, esum;
+        const float* row = a.logits + (live ? (size_t)t * a.E : 0);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = sub + i * GL;
+            l[i] = e < a.E ? (live ? __ldcs(row + e) : 0.f) : __uint_as_float(0xFF800000u);
+        }
+        if (live && sub < a.k) {
+            const unsigned e = (unsigned)__ldg(a.topk_idx + (size_t)t * a.k + sub);
+            if (e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+        }
+        scores<GL, VPL>(l, sigmoid, want, s, total, lse, top, esum);
+        if (live) {
+            const float inv = __fdividef(1.f, total);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+            if (sub == 0) {
+                z = fmaf(lse, lse, z);
+                ++n;
+            }
+        }
+    }
+    // the lane groups' sums, then the warps'
+#pragma unroll
+    for (int o = 16; o >= GL; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+    if (lane < GL)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sums[warp][sub + i * GL] = acc[i];
+    z = cta_sum(z, red);
+    const int tokens = (int)cta_sum((float)n, red);  // (below 2^24: a chunk)
+    float dot = 0.f;
+    float* part = Partials(a).part + (size_t)blockIdx.x * (2 * a.E + 2);
+    for (int e = tid; e < a.E; e += kRouterThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRouterWarps; ++w) v += sums[w][e];
+        if (sp.chunks > 1) {
+            part[e] = v;
+            part[a.E + e] = __int_as_float(hist[e]);
+        } else {
+            a.load[g * a.E + e] = hist[e];
+            dot = fmaf(v, (float)hist[e], dot);
+        }
+    }
+    if (sp.chunks > 1) {
+        if (tid == 0) {
+            part[2 * a.E] = z;
+            part[2 * a.E + 1] = __int_as_float(tokens);
+        }
+        return;
+    }
+    dot = cta_sum(dot, red);
+    if (tid == 0) group_done(a, g, dot, z, tokens);
+}
+
+// One CTA a group: adds its CTAs' sums in their order.
+__global__ void __launch_bounds__(kRouterThreads) balance_groups_kernel(const RouterLossArgs a, Split sp) {
+    __shared__ float red[kRouterWarps];
+    wait_for_kernel_before();
+    const long long g = blockIdx.x;
+    const size_t pitch = 2 * a.E + 2;
+    const float* part = Partials(a).part + (size_t)g * sp.chunks * pitch;
+    float dot = 0.f;
+    for (int e = threadIdx.x; e < a.E; e += kRouterThreads) {
+        float v = 0.f;
+        int load = 0;
+#pragma unroll 8
+        for (int c = 0; c < sp.chunks; ++c) {
+            v += __ldcg(part + c * pitch + e);
+            load += __float_as_int(__ldcg(part + c * pitch + a.E + e));
+        }
+        a.load[g * a.E + e] = load;
+        dot = fmaf(v, (float)load, dot);
+    }
+    float z = 0.f;
+    int n = 0;
+    for (int c = threadIdx.x; c < sp.chunks; c += kRouterThreads) {
+        z += __ldcg(part + c * pitch + 2 * a.E);
+        n += __float_as_int(__ldcg(part + c * pitch + 2 * a.E + 1));
+    }
+    dot = cta_sum(dot, red);
+    z = cta_sum(z, red);
+    __shared__ int count;
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    if (n) atomicAdd(&count, n);
+    __syncthreads();
+    if (threadIdx.x == 0) group_done(a, g, dot, z, count);
+}
+
+// One CTA: the groups' losses in their order.
+__global__ void __launch_bounds__(kRouterThreads) balance_total_kernel(const RouterLossArgs a) {
+    __shared__ float red[kRouterWarps];
+    __shared__ int count;
+    wait_for_kernel_before();
+    const float* group = Partials(a).group;
+    float bal = 0.f, z = 0.f;
+    int n = 0;
+    for (int g = threadIdx.x; g < a.groups; g += kRouterThreads) {
+        bal += __ldcg(group + 2 * (size_t)g);
+        z += __ldcg(group + 2 * (size_t)g + 1);
+        n += __ldcg(a.tokens + g);
+    }
+    if (threadIdx.x == 0) count = 0;
+    bal = cta_sum(bal, red);
+    z = cta_sum(z, red);
+    if (n) atomicAdd(&count, n);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.tokens[a.groups] = count;
+        a.loss[0] = a.balance * (bal / (float)a.groups);
+        a.loss[1] = count > 0 ? a.z * (z / (float)count) : 0.f;
+    }
+}
+
+template <int GL, int VPL>
+__global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterLossArgs a, Split sp) {
+    constexpr int kCols = GL * VPL, kPer = 32 / GL;  // tokens of a warp
+    __shared__ float delta[kRouterWarps * kPer][kCols];    // the gates' gradient of a token's picks
+    wait_for_kernel_before();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % GL;
+    const long long g = blockIdx.x / sp.chunks;
+    const int chunk = blockIdx.x % sp.chunks;
+    const long long t0 = g * a.seq_len + (long long)chunk * sp.chunk;
+    const long long t1 = min(min(t0 + sp.chunk, (g + 1) * (long long)a.seq_len), (long long)a.T);
+    float* mine = delta[warp * kPer + lane / GL];
+    float w[VPL];
+    {
+        const int n = a.balance != 0.f ? __ldg(a.tokens + g) : 0;
+        const float coef = n > 0 ? a.balance * ((float)a.E / ((float)a.groups * (float)a.k * (float)n * (float)n)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = sub + i * GL;
+            w[i] = coef != 0.f && e < a.E ? coef * (float)__ldg(a.load + g * a.E + e) : 0.f;
+            mine[e] = 0.f;
+        }
+    }
+    const int all = a.z != 0.f ? __ldg(a.tokens + a.groups) : 0;
+    const float zc = all > 0 ? 2.f * a.z / (float)all : 0.f;
+    const bool sigmoid = a.sigmoid != 0, losses = a.balance != 0.f || a.z != 0.f;
+    const bool full = losses || (!sigmoid && !a.renorm);  // the gradient is not of the picks alone
+    __syncwarp();
+    for (long long tw = t0 + warp * kPer; tw < t1; tw += kRouterWarps * kPer) {
+        const long long t = tw + lane / GL;
+        const bool there = t < t1, counted = there && (!a.mask || a.mask[t]);
+        const float* row = a.logits + (there ? (size_t)t * a.E : 0);
+        float l[VPL], d[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) d[i] = 0.f;
+        // the picks: lane j holds pick j
+        int pick = -1;
+        float pl = __uint_as_float(0xFF800000u), dw = 0.f;
+        if (a.dtopk_w && there && sub < a.k) {
+            const unsigned e = (unsigned)__ldg(a.topk_idx + (size_t)t * a.k + sub);
+            if (e < (unsigned)a.E) {
+                pick = (int)e;
+                pl = __ldg(row + e);
+                dw = __ldg(a.dtopk_w + (size_t)t * a.k + sub);
+            }
+        }
+        float gate_dot = 0.f, pick_p = 0.f;
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = sub + i * GL;
+                l[i] = e < a.E ? (there ? __ldg(row + e) : 0.f) : __uint_as_float(0xFF800000u);
+            }
+            float s[VPL], total, lse, top, esum;
+            scores<GL, VPL>(l, sigmoid, zc != 0.f, s, total, lse, top, esum);
+            const float inv = __fdividef(1.f, total);
+            if (!sigmoid && !a.renorm) {  // gates that are entries of the softmax over all experts
+                pick_p = pick >= 0 ? expf(pl - top) * inv : 0.f;
+                gate_dot = lanes_sum<GL>(pick_p * dw);
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) dot = fmaf(s[i] * inv, w[i], dot);
+            dot = lanes_sum<GL>(dot);
+            const float zt = counted ? zc * lse : 0.f, zinv = sigmoid && zc != 0.f ? __fdividef(1.f, esum) : inv;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const float p = s[i] * inv;
+                float v = counted ? p * (w[i] - dot) : 0.f;
+                if (sigmoid) v *= Logistic(l[i]).rest;
+                if (zc != 0.f) v = fmaf(zt, sigmoid ? expf(l[i] - top) * zinv : p, v);
+                d[i] = fmaf(-gate_dot, p, v);
+            }
+        }
+        if (a.dtopk_w) {
+            float v;
+            if (!sigmoid && !a.renorm) {
+                v = pick_p * dw;
+            } else if (!a.renorm) {
+                const Logistic g(pl);
+                v = dw * g.s * g.rest;
+            } else {
+                float s = 0.f;
+                if (sigmoid) {
+                    s = pick >= 0 ? Logistic(pl).s : 0.f;
+                } else {
+                    const float top = lanes_max<GL>(pl);
+                    s = pick >= 0 ? expf(pl - top) : 0.f;
+                }
+                const float gate = s * __fdividef(1.f, lanes_sum<GL>(s));
+                v = gate * (dw - lanes_sum<GL>(gate * dw));
+                if (sigmoid) v *= Logistic(pl).rest;
+            }
+            if (pick >= 0) atomicAdd(mine + pick, v);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) d[i] += mine[sub + i * GL];
+            __syncwarp();
+            if (pick >= 0) mine[pick] = 0.f;
+            __syncwarp();
+        }
+        if (there) {
+            float* out = a.dlogits + (size_t)t * a.E;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = sub + i * GL;
+                if (e < a.E) __stcs(out + e, d[i]);
+            }
+        }
+    }
+}
+
+// go(lanes a token, experts a lane)
+template <class Go>
+cudaError_t by_experts(int E, Go go) {
+    using std::integral_constant;
+    if (E <= 8) return go(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (E <= 16) return go(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (E <= 32) return go(integral_constant<int, 32>(), integral_constant<int, 1>());
+    if (E <= 64) return go(integral_constant<int, 32>(), integral_constant<int, 2>());
+    if (E <= 128) return go(integral_constant<int, 32>(), integral_constant<int, 4>());
+    if (E <= 256) return go(integral_constant<int, 32>(), integral_constant<int, 8>());
+    if (E <= 512) return go(integral_constant<int, 32>(), integral_constant<int, 16>());
+    return go(integral_constant<int, 32>(), integral_constant<int, 32>());
+}
+
+}  // namespace
+
+size_t balance_scratch_bytes(int T, int E, int seq_len, int sm_count) {
+    const int groups = (int)(((long long)T + seq_len - 1) / seq_len);
+    const Split s = split_of(T, E, seq_len, groups, sm_count);
+    return sizeof(float) * (2 * (size_t)groups + (s.chunks > 1 ? (size_t)s.blocks * (2 * (size_t)E + 2) : 0));
+}
+
+cudaError_t launch_balance_loss(const RouterLossArgs& a, int sm_count, cudaStream_t stream) {
+    const Split sp = split_of(a.T, a.E, a.seq_len, a.groups, sm_count);
+    if (sp.blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    cudaError_t e = by_experts(a.E, [&](auto gl, auto vpl) {
+        return launch_after(balance_kernel<decltype(gl)::value, decltype(vpl)::value>, (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
+    });
+    if (e == cudaSuccess && sp.chunks > 1) e = launch_after(balance_groups_kernel, (unsigned)a.groups, kRouterThreads, 0, stream, a, sp);
+    if (e == cudaSuccess && a.groups > 1) e = launch_after(balance_total_kernel, 1u, kRouterThreads, 0, stream, a);
+    return e;
+}
+
+cudaError_t launch_router_backward(const RouterLossArgs& a, int sm_count, cudaStream_t stream) {
+    const Split sp = split_of(a.T, a.E, a.seq_len, a.groups, sm_count);
+    if (sp.blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    return by_experts(a.E, [&](auto gl, auto vpl) {
+        return launch_after(router_backward_kernel<decltype(gl)::value, decltype(vpl)::value>, (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
+    });
+}
+
+}  // namespace moe

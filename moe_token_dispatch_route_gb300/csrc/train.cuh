@@ -41,7 +41,7 @@ struct LayernormBackwardArgs {
     const void* x;       // [T][d], fp32 or bf16
     int x_bf16;          // also the type of dres and dx
     const float* gamma;  // [d] or null (1)
-    const float* mean;   // [T]
+    const float* mean;   // [T]; null: the RMS norm's gradient
     const float* rstd;   // [T]
     const void* dres;    // [T][d] or null
     void* dx;            // [T][d]
