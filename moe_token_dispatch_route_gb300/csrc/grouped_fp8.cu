@@ -10,13 +10,18 @@
 // columns, one scale: 128 bytes of a row, one swizzle row.  Its products go to one of two TMEM accumulators of 256
 // columns, and eight epilogue warps read it (lane = row, so a thread has one scale of A and one of each block
 // of W) and add it to their 128 sums while the other accumulator is being filled.  That costs 512 bytes a cycle of TMEM
-// reads and 128 multiply-adds a cycle: half of the time the tensor cores take for the block.
+// reads and 128 multiply-adds a cycle: half of the 512 cycles that the tensor cores take for the block.  The thread
+// that issues the MMAs has as long, so its loop has one commit a k-block (it signals the loads and the
+// epilogue both) and nothing that can be done elsewhere.
 //
-// Roles of a CTA (384 threads): warp 0 loads (one thread, or with gathered rows all lanes, four rows each),
-// warp 1 issues the MMAs (the leader's), warps 4-11 are the epilogue, each with one TMEM lane quarter and half of
-// the columns of both blocks.  Tile i of the list is the CTA's (or pair's) i mod grid: all tiles cost the same.
+// Roles of a CTA (512 threads): warp 0 loads W and, where its rows are in place, A (TMA); warp 1 issues the MMAs (the
+// leader's) or tells the leader that gathered rows have landed (the peer's); warp 2 brings the scales; warps 4-7 copy
+// gathered rows (16-byte cp.async: TMA's gather of four rows took three times as long); warps 8-15 are the epilogue, each
+// with one TMEM lane quarter and half of the columns of both blocks.  Tile i of the list is the CTA's (or pair's) i mod
+// grid: all tiles cost the same.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "bounded_wait.cuh"
 #include "moe_internal.cuh"
@@ -26,14 +31,17 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kFp8Threads = 384;
+constexpr int kFp8Threads = 512;
 constexpr int kBlk = kScaleBlock;           // columns of a k-block
 constexpr int kOpBytes = 128 * kBlk;        // 16 KB: 128 rows of an operand
-constexpr int kEpiFirst = 4, kEpiWarps = 8;
+constexpr int kEpiFirst = 8, kEpiWarps = 8;
 constexpr int kBand = 8;                    // row tiles per schedule band
 constexpr int kFp8K = 32;                   // products of an MMA step
 constexpr int kMaxStages = 6;
 constexpr int kStageOut = 2048;             // a warp's 32 rows of 64 bytes on their way out
+constexpr int kScaleRing = 4;               // slots of four k-blocks' scales
+constexpr int kGatherFirst = 4, kGatherWarps = 4;
+constexpr int kGatherRows = 128 / kGatherWarps;  // of a warp
 
 template <bool PAIR>
 struct Cfg {
@@ -46,21 +54,26 @@ struct Cfg {
 struct Fp8Ctl {
     uint64_t full[kMaxStages];  // leader: the stage's loads of both CTAs
     uint64_t empty[kMaxStages];
-    uint64_t tfull[2];
-    uint64_t tempty[2];         // leader
+    uint64_t tfull[2];          // an accumulator has its k-block's products
+    uint64_t tempty[2];         // leader: it has been read
     uint64_t mma_done;
     uint64_t amax_there;        // all epilogue warps have written a tile's amax
+    uint64_t afull[kMaxStages]; // gathered rows, the pair's peer: its own have landed
+    uint64_t sfull[kScaleRing], sempty[kScaleRing];
     uint32_t tmem_base;
     int abort;
     float amax[2][2][128];      // by tile parity and half of the columns: a row's largest magnitude
+    float4 as[kScaleRing][128]; // four k-blocks' scales of each row
+    float4 ws[kScaleRing][2];   // and of the two blocks of W
 };
 
 struct Fp8Params {
-    CUtensorMap a_map;    // rows in place: boxes of 128 rows; gathered: of one row
+    CUtensorMap a_map;    // rows in place: boxes of 128 rows
     CUtensorMap a_part;   // rows in place: boxes of 32 rows
     CUtensorMap w_map;
     GroupedFp8Args a;
     int c_tiles, nkb;
+    int as_vec;           // rows of A's scales are whole 16 bytes
     int w_blocks;         // scale blocks of an expert's rows of W
 };
 
@@ -83,22 +96,6 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
     if (PAIR) tma_load_2d_pair(dst, map, bar, x, row);
     else tma_load_2d(dst, map, bar, x, row);
 }
-// four rows by index
-template <bool PAIR>
-__device__ __forceinline__ void gather_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int (&r)[4]) {
-    if (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x),
-            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x),
-            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-            : "memory");
-}
 template <bool PAIR>
 __device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int row, int half,
                                              int e) {
@@ -116,12 +113,37 @@ __device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap* ma
             : "memory");
 }
 
-// (a, b) += v * (s, s)
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n}\n" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
+// 32 TMEM lanes x 16 consecutive columns, loaded and there.  (A wait in a statement of its own would take the registers as
+// operands, and they would be copied: 64 more instructions a k-block.)
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
-__device__ __forceinline__ float2 unpack(uint64_t v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+
+// One arrival of a converged warp, without a branch.  PAIR: `bar` is a shared::cluster address.
+template <bool PAIR>
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+            "@p mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+            "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
+            : "memory");
+}
+
+// A wait on a barrier whose arrivals hand over TMEM, which the tcgen05 fences order: acquired at CTA scope.
+__device__ __forceinline__ bool tmem_wait(uint32_t bar, uint32_t parity, const Wait& w, int where) {
+    return mbar_try_wait(bar, parity) || bar_wait_slow(bar, parity, w, where, true);
 }
 
 struct Fp8Tile {
@@ -162,17 +184,23 @@ __device__ __forceinline__ int source_row(const Fp8Params& p, int g) {
     return s < (unsigned)p.a.S ? (int)(s / (unsigned)p.a.k) : 0;
 }
 
-// Bytes of the k-block's rows of A that a CTA with `rows` valid ones loads: boxes of 32 rows, or four rows a gather.
+// Bytes of the k-block's rows of A that a CTA with `rows` valid ones loads by TMA: boxes of 32 rows.
 __device__ __forceinline__ uint32_t a_bytes(const Fp8Params& p, int rows) {
-    return p.a.perm ? (uint32_t)((rows + 3) & ~3) * kBlk : (uint32_t)((rows + 31) & ~31) * kBlk;
+    return p.a.perm ? 0u : (uint32_t)((rows + 31) & ~31) * kBlk;
 }
 
-// Warp 0, all lanes.
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
+}
+
+// Warp 0.  All lanes run the loop and one issues: addresses are then known to be the warp's, not a lane's.
 template <bool PAIR>
 __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const int* off, const int* base, int total, int first,
                          int step, const Wait& w, bool leader, uint32_t lead, int rank) {
     using C = Cfg<PAIR>;
-    const int lane = threadIdx.x & 31;
     const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
     const uint32_t full_lead = PAIR ? mapa_shared(full0, lead) : full0;
     int s = 0;
@@ -183,18 +211,16 @@ __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const
         const int mine = cta_rows(t, rank), row0 = t.seg0 + C::kRowTile * t.r + 128 * rank;
         const uint32_t bytes = PAIR ? a_bytes(p, cta_rows(t, 0)) + a_bytes(p, cta_rows(t, 1)) + 2u * C::kWBytes
                                     : a_bytes(p, mine) + (uint32_t)C::kWBytes;
-        int src[4];
-        if (p.a.perm) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) src[j] = 4 * lane < mine ? source_row(p, row0 + min(4 * lane + j, mine - 1)) : 0;
-        }
         for (int kb = 0; kb < p.nkb; ++kb) {
+            
             ok = bar_wait(empty0 + 8 * s, phase ^ 1u, w, 70);
             if (!(ok = __all_sync(kFull, ok))) break;
-            const uint32_t dst = smem_addr(stages) + s * C::kStageBytes, bar = full_lead + 8 * s;
-            const int x = kb * kBlk;
-            if (lane == 0) {
+            
+            if (elected()) {
+                const uint32_t dst = smem_addr(stages) + s * C::kStageBytes, bar = full_lead + 8 * s;
+                const int x = kb * kBlk;
                 if (leader) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+#pragma unroll
                 for (int b = 0; b < (PAIR ? 1 : 2); ++b) {
                     const int blk = PAIR ? rank : b;
                     load_weights<PAIR>(dst + kOpBytes * (1 + b), &p.w_map, bar, x, p.a.glu ? kBlk * t.c : kBlk * (2 * t.c + blk),
@@ -206,10 +232,8 @@ __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const
                         for (int r = 0; r < mine; r += 32) load_rows<PAIR>(dst + r * kBlk, &p.a_part, bar, x, row0 + r);
                 }
             }
-            if (p.a.perm) {
-                __syncwarp();
-                if (4 * lane < mine) gather_rows<PAIR>(dst + 4 * lane * kBlk, &p.a_map, bar, x, src);
-            }
+            __syncwarp();
+            
             ++uses;
             if (++s == C::kStages) {
                 s = 0;
@@ -218,12 +242,128 @@ __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const
         }
     }
     // no load may still be landing when the CTA leaves
-    if (leader && lane == 0)
+    if (leader)
         for (uint32_t u = uses > C::kStages ? uses - C::kStages : 0; u < uses; ++u)
             bar_wait(full0 + 8 * (u % C::kStages), (u / C::kStages) & 1u, w, 71, false);
 }
 
-// Leader's warp 1, one thread.
+// Gathered rows, kGatherWarps warps: eight lanes copy the 128 bytes of a row, in the swizzled layout that TMA
+// gives (16-byte column c of row r at c ^ (r % 8)).  Every lane's arrival on the stage's barrier follows its copies, so
+// nobody waits for them here.
+template <bool PAIR>
+__device__ void gather_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const int* off, const int* base, int total, int first,
+                            int step, const Wait& w, bool leader, int rank) {
+    using C = Cfg<PAIR>;
+    const int lane = threadIdx.x & 31, c = lane & 7, r_lane = lane >> 3, part = (int)(threadIdx.x >> 5) - kGatherFirst;
+    const uint32_t empty0 = smem_addr(&ctl->empty[0]);
+    const uint32_t landed0 = leader ? smem_addr(&ctl->full[0]) : smem_addr(&ctl->afull[0]);
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = first; ok && i < total; i += step) {
+        const Fp8Tile t = tile_at<PAIR>(p, off, base, i);
+        const int mine = cta_rows(t, rank), row0 = t.seg0 + C::kRowTile * t.r + 128 * rank;
+        // the source rows of this lane's rows kGatherRows part + 4 j + r_lane, first read by a lane each
+        int src[kGatherRows / 4];
+        {
+            const int r = kGatherRows * part + lane;
+            const int read = r < mine ? source_row(p, row0 + r) : -1;
+#pragma unroll
+            for (int j = 0; j < kGatherRows / 4; ++j) src[j] = __shfl_sync(kFull, read, 4 * j + r_lane);
+        }
+        for (int kb = 0; kb < p.nkb; ++kb) {
+            ok = bar_wait(empty0 + 8 * s, phase ^ 1u, w, 77);
+            if (!(ok = __all_sync(kFull, ok))) break;
+            const uint32_t dst = smem_addr(stages) + s * C::kStageBytes;
+            const int x = kb * kBlk + 16 * c;
+            const int bytes = x < p.a.d ? 16 : 0;  // columns past d are zeros
+            const uint8_t* col = p.a.A + (bytes ? x : 0);
+#pragma unroll
+            for (int j = 0; j < kGatherRows / 4; ++j) {
+                const int r = kGatherRows * part + 4 * j + r_lane;
+                if (src[j] >= 0)
+                    cp_async16_cg_zfill(dst + (uint32_t)(r * kBlk + ((c ^ (r & 7)) << 4)), col + (size_t)src[j] * p.a.d, bytes);
+            }
+            cp_async_mbar_arrive_noinc(landed0 + 8 * s);
+            if (++s == C::kStages) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    cp_async_wait_all();  // no copy may still be landing when the CTA leaves
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Warp 2: the scales of four k-blocks at a time, four rows a lane, and those of the two blocks of W.  (Loaded by the
+// epilogue's threads, even four k-blocks ahead, the scales took as long as all else.)
+template <bool PAIR>
+__device__ void scales_role(const Fp8Params& p, Fp8Ctl* ctl, const int* off, const int* base, int total, int first, int step,
+                            const Wait& w, int rank) {
+    const int lane = threadIdx.x & 31;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = first; ok && i < total; i += step) {
+        const Fp8Tile t = tile_at<PAIR>(p, off, base, i);
+        const int mine = cta_rows(t, rank), row0 = t.seg0 + Cfg<PAIR>::kRowTile * t.r + 128 * rank;
+        const float* as[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = lane + 32 * j;
+            as[j] = r < mine ? p.a.A_scales + (size_t)source_row(p, row0 + r) * p.nkb : nullptr;
+        }
+        const int blk0 = p.a.glu ? t.c : 2 * t.c, blk1 = p.a.glu ? p.w_blocks / 2 + t.c : min(2 * t.c + 1, p.w_blocks - 1);
+        const float* ws = p.a.W_scales + ((size_t)t.e * p.w_blocks + (lane < 4 ? blk0 : blk1)) * p.nkb + (lane & 3);
+        for (int kb = 0; kb < p.nkb; kb += 4) {
+            ok = bar_wait(smem_addr(&ctl->sempty[slot]), phase ^ 1u, w, 79);
+            if (!(ok = __all_sync(kFull, ok))) break;
+            const int n = min(4, p.nkb - kb);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!as[j]) continue;
+                const uint32_t dst = smem_addr(&ctl->as[slot][lane + 32 * j]);
+                if (p.as_vec) {
+                    cp_async16_cg(dst, as[j] + kb);
+                } else {
+                    for (int k = 0; k < n; ++k) cp_async4(dst + 4 * k, as[j] + kb + k);
+                }
+            }
+            if (lane < 8 && (lane & 3) < n) cp_async4(smem_addr(&ctl->ws[slot][0]) + 4 * lane, ws + kb);
+            cp_async_mbar_arrive_noinc(smem_addr(&ctl->sfull[slot]));
+            if (++slot == kScaleRing) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    cp_async_wait_all();
+}
+
+// Gathered rows, the peer's warp 1, one thread: passes a stage whose rows have landed on to the leader.
+template <bool PAIR>
+__device__ void relay_role(const Fp8Params& p, Fp8Ctl* ctl, int total, int first, int step, const Wait& w, uint32_t lead) {
+    const uint32_t full_lead = mapa_shared(smem_addr(&ctl->full[0]), lead), afull0 = smem_addr(&ctl->afull[0]);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = first; i < total; i += step) {
+        for (int kb = 0; kb < p.nkb; ++kb) {
+            if (!bar_wait(afull0 + 8 * s, phase, w, 78)) return;
+            fence_proxy_async_smem();  // the copies, before the leader's MMAs read them
+            mbar_arrive_remote(full_lead + 8 * s);
+            if (++s == Cfg<PAIR>::kStages) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+// Leader's warp 1.  All lanes run the loop and one issues: descriptors and addresses are then known to be the warp's, not a
+// lane's.  (Run by one lane alone, an MMA took 75 cycles to issue and the k-block 800.)
 template <bool PAIR>
 __device__ void mma_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, int total, int first, int step, uint32_t tmem,
                          const Wait& w) {
@@ -233,41 +373,51 @@ __device__ void mma_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, int t
     const uint64_t ad0 = smem_desc_sw128(smem_addr(stages), 16, 1024), bd0 = smem_desc_sw128(smem_addr(stages) + kOpBytes, 16, 1024);
     const uint32_t full0 = smem_addr(&ctl->full[0]), empty0 = smem_addr(&ctl->empty[0]);
     const uint32_t tfull0 = smem_addr(&ctl->tfull[0]), tempty0 = smem_addr(&ctl->tempty[0]);
+    const bool gathered = p.a.perm != nullptr;
     const int last_steps = (p.a.d - kBlk * (p.nkb - 1) + kFp8K - 1) / kFp8K;  // columns past d are loaded as zeros
     int s = 0;
-    uint32_t phase = 0, it = 0;
-    bool ok = true;
-    for (int i = first; ok && i < total; i += step) {
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-            const uint32_t buf = it & 1u;
-            if (!(ok = bar_wait(tempty0 + 8 * buf, (it >> 1 & 1u) ^ 1u, w, 72))) break;
-            if (!(ok = bar_wait(full0 + 8 * s, phase, w, 73))) break;
-            tc_fence_after();
-            const uint64_t ad = ad0 + (uint32_t)(s * (C::kStageBytes >> 4)), bd = bd0 + (uint32_t)(s * (C::kStageBytes >> 4));
-            const uint32_t d = tmem + 256u * buf;
-            const int steps = kb + 1 == p.nkb ? last_steps : kBlk / kFp8K;
+    uint32_t phase = 0, free_phase[2] = {1, 1};
+    // a tile's k-blocks go to accumulator 0 and 1 in turn, from 0 on
+    auto block = [&](int buf, int steps) {
+        const bool there = tmem_wait(tempty0 + 8 * buf, free_phase[buf], w, 72) && bar_wait(full0 + 8 * s, phase, w, 73);
+        if (!__all_sync(kFull, there)) return false;
+        free_phase[buf] ^= 1u;
+        if (gathered) fence_proxy_async_smem();  // this CTA's copies
+        tc_fence_after();
+        const uint64_t ad = ad0 + (uint32_t)(s * (C::kStageBytes >> 4)), bd = bd0 + (uint32_t)(s * (C::kStageBytes >> 4));
+        const uint32_t d = tmem + 256u * buf;
+        if (elected()) {
 #pragma unroll
-            for (int k = 0; k < kBlk / kFp8K; ++k) {
-                if (k < steps) {
-                    if (PAIR) umma_fp8_pair(d, ad + 2 * k, bd + 2 * k, kDesc, k != 0);
-                    else umma_fp8(d, ad + 2 * k, bd + 2 * k, kDesc, k != 0);
-                }
+            for (int k = 0; k < steps; ++k) {
+                if (PAIR) umma_fp8_pair(d, ad + 2 * k, bd + 2 * k, kDesc, k != 0);
+                else umma_fp8(d, ad + 2 * k, bd + 2 * k, kDesc, k != 0);
             }
             if (PAIR) {
-                umma_commit_pair_mc(empty0 + 8 * s, 0x3);
                 umma_commit_pair_mc(tfull0 + 8 * buf, 0x3);
+                umma_commit_pair_mc(empty0 + 8 * s, 0x3);
             } else {
-                umma_commit(empty0 + 8 * s);
                 umma_commit(tfull0 + 8 * buf);
-            }
-            if (++s == C::kStages) {
-                s = 0;
-                phase ^= 1u;
+                umma_commit(empty0 + 8 * s);
             }
         }
+        __syncwarp();
+        if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1u;
+        }
+        return true;
+    };
+    bool ok = true;
+    for (int i = first; ok && i < total; i += step) {
+        int kb = 0;
+        for (; ok && kb + 2 < p.nkb; kb += 2) ok = block(0, kBlk / kFp8K) && block(1, kBlk / kFp8K);
+        if (ok && kb + 2 == p.nkb) ok = block(0, kBlk / kFp8K) && block(1, last_steps);
+        else if (ok) ok = block(0, last_steps);
     }
-    if (PAIR) umma_commit_pair(smem_addr(&ctl->mma_done));
-    else umma_commit(smem_addr(&ctl->mma_done));
+    if (elected()) {
+        if (PAIR) umma_commit_pair(smem_addr(&ctl->mma_done));
+        else umma_commit(smem_addr(&ctl->mma_done));
+    }
     bar_wait(smem_addr(&ctl->mma_done), 0u, w, 74, false);
 }
 
@@ -304,76 +454,93 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, h = (warp - kEpiFirst) >> 2;
     const int nkb = p.nkb;
     staging += (warp - kEpiFirst) * kStageOut;
-    const uint32_t tempty0 = PAIR && !leader ? mapa_shared(smem_addr(&ctl->tempty[0]), lead) : smem_addr(&ctl->tempty[0]);
+    const uint32_t tempty_own = smem_addr(&ctl->tempty[0]), tempty0 = PAIR ? mapa_shared(tempty_own, lead) : tempty_own;
     const uint32_t tfull0 = smem_addr(&ctl->tfull[0]);
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 64u * h;
-    uint32_t it = 0;
-    int turn = 0;
+    uint32_t ready_phase[2] = {0, 0}, sphase = 0;
+    int turn = 0, slot = 0;
     for (int i = first; i < total; i += step, turn ^= 1) {
         const Fp8Tile t = tile_at<PAIR>(p, off, base, i);
         const int mine = cta_rows(t, rank) - 32 * q;  // this warp's valid rows, may be <= 0
         const size_t row0 = (size_t)t.seg0 + (size_t)(C::kRowTile * t.r + 128 * rank + 32 * q);
-        const float* as = p.a.A_scales + (mine > 0 ? (size_t)source_row(p, (int)row0 + min(lane, mine - 1)) * nkb : 0);
-        const int blk0 = p.a.glu ? t.c : 2 * t.c, blk1 = p.a.glu ? p.w_blocks / 2 + t.c : min(2 * t.c + 1, p.w_blocks - 1);
-        const float* ws0 = p.a.W_scales + ((size_t)t.e * p.w_blocks + blk0) * nkb;
-        const float* ws1 = p.a.W_scales + ((size_t)t.e * p.w_blocks + blk1) * nkb;
-        uint64_t acc[64];  // columns 64 h .. of the first block, then of the second, in twos
+        float acc[2][64];  // columns 64 h .. of the two blocks
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = 0;
-        // a lane's scales of four k-blocks are on their way while the four before are used
-        float cur[4], next[4];
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) next[j] = j < nkb ? __ldg(as + j) : 0.f;
-        float w0 = __ldg(ws0), w1 = __ldg(ws1);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-            if ((kb & 3) == 0) {
+            for (int j = 0; j < 64; ++j) acc[b][j] = 0.f;
+        // the k-blocks of a warp with (LIVE) and without valid rows; false: a wait gave up.  A branch around the sums
+        // inside the loop would copy them.
+        auto blocks = [&](auto live) {
+            constexpr bool LIVE = decltype(live)::value;
+            float sc[4][2];  // four k-blocks' scales, for either block of W
+            auto block = [&](int buf, float s0, float s1) {
+                const bool ready = tmem_wait(tfull0 + 8 * buf, ready_phase[buf], w, 75);
+                if (!__all_sync(kFull, ready)) return false;
+                ready_phase[buf] ^= 1u;
+                tc_fence_after();
+                if constexpr (LIVE) {
+                    const uint32_t at = lanes + 256u * buf;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    cur[j] = next[j];
-                    next[j] = kb + 4 + j < nkb ? __ldg(as + kb + 4 + j) : 0.f;
+                    for (int g = 0; g < 8; ++g) {
+                        uint32_t v[16];
+                        tmem_ld_32x16(at + 128 * (g >> 2) + 16 * (g & 3), v);
+                        float* sum = acc[g >> 2] + 16 * (g & 3);
+                        const float2 scale = g < 4 ? make_float2(s0, s0) : make_float2(s1, s1);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), scale,
+                                                        make_float2(sum[j], sum[j + 1]));
+                            sum[j] = r.x;
+                            sum[j + 1] = r.y;
+                        }
+                    }
                 }
-            }
-            const float s0 = cur[0] * w0, s1 = cur[0] * w1;
-            cur[0] = cur[1];
-            cur[1] = cur[2];
-            cur[2] = cur[3];
-            if (kb + 1 < nkb) {
-                w0 = __ldg(ws0 + kb + 1);
-                w1 = __ldg(ws1 + kb + 1);
-            }
-            const uint32_t buf = it & 1u;
-            const bool ready = bar_wait(tfull0 + 8 * buf, it >> 1 & 1u, w, 75);
-            if (!__all_sync(kFull, ready)) return;
-            tc_fence_after();
-            if (mine > 0) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t v[32];
-                    tmem_ld_32x32(lanes + 256u * buf + 128u * (g >> 1) + 32u * (g & 1), v);
-                    tmem_ld_wait(v);
-                    const uint32_t sb = __float_as_uint(g < 2 ? s0 : s1);
-                    const uint64_t s = (uint64_t)sb << 32 | sb;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * g + j], v[2 * j], v[2 * j + 1], s);
+                tc_fence_before();
+                warp_arrive<PAIR>(tempty0 + 8 * buf);
+                return true;
+            };
+            int kb = 0;
+            for (; kb < nkb; kb += 2) {
+                if ((kb & 3) == 0) {
+                    const bool there = bar_wait(smem_addr(&ctl->sfull[slot]), sphase, w, 80);
+                    if (!__all_sync(kFull, there)) return false;
+                    const float4 a4 = ctl->as[slot][32 * q + lane], w0 = ctl->ws[slot][0], w1 = ctl->ws[slot][1];
+                    sc[0][0] = a4.x * w0.x;
+                    sc[0][1] = a4.x * w1.x;
+                    sc[1][0] = a4.y * w0.y;
+                    sc[1][1] = a4.y * w1.y;
+                    sc[2][0] = a4.z * w0.z;
+                    sc[2][1] = a4.z * w1.z;
+                    sc[3][0] = a4.w * w0.w;
+                    sc[3][1] = a4.w * w1.w;
                 }
+                if (!block(0, sc[0][0], sc[0][1])) return false;
+                if ((kb & 3) == 0) {
+                    // (the scales are in registers: this warp's multiplications have used them)
+                    warp_arrive<false>(smem_addr(&ctl->sempty[slot]));
+                    if (++slot == kScaleRing) {
+                        slot = 0;
+                        sphase ^= 1u;
+                    }
+                }
+                if (kb + 1 == nkb) break;
+                if (!block(1, sc[1][0], sc[1][1])) return false;
+                sc[0][0] = sc[2][0];
+                sc[0][1] = sc[2][1];
+                sc[1][0] = sc[3][0];
+                sc[1][1] = sc[3][1];
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR && !leader) mbar_arrive_remote(tempty0 + 8 * buf);
-                else mbar_arrive(tempty0 + 8 * buf);
-            }
-        }
+            return true;
+        };
+        if (!(mine > 0 ? blocks(std::true_type()) : blocks(std::false_type()))) return;
         if (p.a.glu) {
             const int F = p.a.N / 2, col = kBlk * t.c + 64 * h;
             float hv[64];
             uint32_t amax = 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float2 g = unpack(acc[j]), u = unpack(acc[32 + j]);
-                hv[2 * j] = silu(g.x) * u.x;
-                hv[2 * j + 1] = silu(g.y) * u.y;
-                amax = max(amax, max(__float_as_uint(hv[2 * j]) & 0x7FFFFFFFu, __float_as_uint(hv[2 * j + 1]) & 0x7FFFFFFFu));
+            for (int j = 0; j < 64; ++j) {
+                hv[j] = silu(acc[0][j]) * acc[1][j];
+                amax = max(amax, __float_as_uint(hv[j]) & 0x7FFFFFFFu);
             }
             ctl->amax[turn][h][32 * q + lane] = __uint_as_float(amax);
             __syncwarp();
@@ -407,10 +574,8 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 f = unpack(acc[32 * b + 16 * g + 4 * c + j]);
-                                x[j] = bf16x2(f.x, f.y);
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = bf16x2(acc[b][32 * g + 8 * c + 2 * j], acc[b][32 * g + 8 * c + 2 * j + 1]);
                             v[c] = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                         rows_out(staging, v, to + 64 * g, 2 * N, mine, 2 * (p.a.N - col) - 64 * g);
@@ -421,10 +586,9 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
                     for (int g = 0; g < 4; ++g) {
                         uint4 v[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint64_t lo = acc[32 * b + 8 * g + 2 * c], hi = acc[32 * b + 8 * g + 2 * c + 1];
-                            v[c] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
-                        }
+                        for (int c = 0; c < 4; ++c)
+                            v[c] = make_uint4(__float_as_uint(acc[b][16 * g + 4 * c]), __float_as_uint(acc[b][16 * g + 4 * c + 1]),
+                                              __float_as_uint(acc[b][16 * g + 4 * c + 2]), __float_as_uint(acc[b][16 * g + 4 * c + 3]));
                         rows_out(staging, v, to + 64 * g, 4 * N, mine, 4 * (p.a.N - col) - 64 * g);
                     }
                 }
@@ -464,7 +628,7 @@ __device__ __forceinline__ void fp8_body(const Fp8Params& p) {
     int* off = reinterpret_cast<int*>(ctl + 1);  // [E+1]
     int* base = off + p.a.E + 1;                 // [E+1] row tiles before expert e
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
     const int rank = (int)(crank & 1u);
     const bool leader = rank == 0;
@@ -472,19 +636,25 @@ __device__ __forceinline__ void fp8_body(const Fp8Params& p) {
     const int E = p.a.E;
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_addr(&ctl->full[s]), 1);
+            // the loading thread, and with gathered rows the copying lanes and the peer's relay
+            mbar_init(smem_addr(&ctl->full[s]), p.a.perm ? 1 + 32 * kGatherWarps + (PAIR ? 1 : 0) : 1);
             mbar_init(smem_addr(&ctl->empty[s]), 1);
+            mbar_init(smem_addr(&ctl->afull[s]), 32 * kGatherWarps);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_addr(&ctl->tfull[a]), 1);
             mbar_init(smem_addr(&ctl->tempty[a]), (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        for (int r = 0; r < kScaleRing; ++r) {
+            mbar_init(smem_addr(&ctl->sfull[r]), 32);
+            mbar_init(smem_addr(&ctl->sempty[r]), kEpiWarps);
         }
         mbar_init(smem_addr(&ctl->mma_done), 1);
         mbar_init(smem_addr(&ctl->amax_there), kEpiWarps);
         ctl->abort = 0;
         mbar_fence_init();
     }
-    if (warp == 2) {
+    if (warp == 3) {
         if (PAIR) {
             tmem_alloc_pair(smem_addr(&ctl->tmem_base), 512);
             tmem_relinquish_pair();
@@ -492,7 +662,7 @@ __device__ __forceinline__ void fp8_body(const Fp8Params& p) {
             tmem_alloc(smem_addr(&ctl->tmem_base), 512);
             tmem_relinquish();
         }
-    } else if (warp == 3 && lane == 0) {
+    } else if (warp == 4 && lane == 0) {
         tma_prefetch_map(&p.a_map);
         tma_prefetch_map(&p.w_map);
     }
@@ -528,17 +698,25 @@ __device__ __forceinline__ void fp8_body(const Fp8Params& p) {
     __syncthreads();
     if (PAIR) cluster_sync_all();  // barriers and TMEM address of both CTAs are there
     tc_fence_after();
-    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);  // the same for all, which the compiler cannot see
     const long long timeout = p.a.timeout_ns * 2 > 500000000LL ? p.a.timeout_ns * 2 : 500000000LL;
     const Wait w{&ctl->abort, p.a.status, timeout};
     const int total = bad ? 0 : base[E] * p.c_tiles;
     const int first = (int)(PAIR ? blockIdx.x / 2 : blockIdx.x), step = (int)(PAIR ? gridDim.x / 2 : gridDim.x);
 
-    // 384 threads x 168 registers: the four warps that load and issue hand some to the epilogue's
+    // 512 threads x 128 registers: the eight warps that load and issue hand some to the epilogue's
     if (warp < kEpiFirst) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 0) producer<PAIR>(p, ctl, stages, off, base, total, first, step, w, leader, lead, rank);
-        else if (warp == 1 && leader && lane == 0) mma_role<PAIR>(p, ctl, stages, total, first, step, tmem, w);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 0) {
+            producer<PAIR>(p, ctl, stages, off, base, total, first, step, w, leader, lead, rank);
+        } else if (warp == 1) {
+            if (leader) mma_role<PAIR>(p, ctl, stages, total, first, step, tmem, w);
+            else if (p.a.perm && lane == 0) relay_role<PAIR>(p, ctl, total, first, step, w, lead);
+        } else if (warp == 2) {
+            scales_role<PAIR>(p, ctl, off, base, total, first, step, w, rank);
+        } else if (p.a.perm && warp >= kGatherFirst) {
+            gather_role<PAIR>(p, ctl, stages, off, base, total, first, step, w, leader, rank);
+        }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -548,7 +726,7 @@ __device__ __forceinline__ void fp8_body(const Fp8Params& p) {
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
-    if (warp == 2) {
+    if (warp == 3) {
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem, 512);
         else tmem_dealloc(tmem, 512);
@@ -611,13 +789,15 @@ cudaError_t launch_grouped_fp8(const GroupedFp8Args& a, int device, int sm_count
     const int halves = a.glu ? 2 : 1, n = a.N / halves;
     p.w_blocks = halves * scale_blocks(n);
     p.nkb = scale_blocks(a.d);
+    p.as_vec = p.nkb % 4 == 0 && reinterpret_cast<uintptr_t>(a.A_scales) % 16 == 0;
     p.c_tiles = a.glu ? scale_blocks(n) : (a.N + 255) / 256;
+    const bool pair = a.S >= 128LL * a.E;  // pairs where the experts have that many rows on average
     const uint64_t rows = a.perm ? (uint64_t)a.T : (uint64_t)a.S;
-    if (!map_e4m3_2d(&p.a_map, a.A, rows, (uint64_t)a.d, a.perm ? 1 : 128) || !map_e4m3_2d(&p.a_part, a.A, rows, (uint64_t)a.d, 32) ||
+    if (!map_e4m3_2d(&p.a_map, a.A, rows, (uint64_t)a.d, 128) || !map_e4m3_2d(&p.a_part, a.A, rows, (uint64_t)a.d, 32) ||
         !map_e4m3_weights(&p.w_map, a.W, (uint64_t)a.E, (uint64_t)halves, (uint64_t)n, (uint64_t)a.d))
         return cudaErrorInvalidValue;
-    // pairs where the experts have that many rows on average
-    return a.S >= 128LL * a.E ? launch<true>(p, device, sm_count, stream) : launch<false>(p, device, sm_count, stream);
+
+    return pair ? launch<true>(p, device, sm_count, stream) : launch<false>(p, device, sm_count, stream);
 }
 
 }  // namespace moe
