@@ -59,48 +59,96 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
+// e^x for x <= 0 within 3 units in the last place.  x log2(e) is rounded, and what the rounding left out is put back
+// to first order; the fast exponential alone is off by 1.2 |x| units, 4e-6 of a gradient.  Below -120 the result is 0 (so for
+// -infinity too); NaN stays NaN.
+__device__ __forceinline__ float exp_of(float x) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-120.f));
+    constexpr float kLog2e = 1.4426950216293335f, kRest = 1.9259629911e-8f;  // log2(e) = kLog2e + kRest
+    const float t = __fmul_rn(x, kLog2e), left = fmaf(x, kRest, fmaf(x, kLog2e, -t));
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return fmaf(p, left * 0.69314718f, p);
+}
+
 // s = 1 / (1 + e^-l) and 1 - s from e^-|l|, which does not overflow: neither is the other's difference from 1, which
-// would lose a far logit's small one.  (expf, not the fast exponential: gradients are fp32 results, and that one is off
-// by 1.2 |x| units, 4e-6 of a gradient.)
+// would lose a far logit's small one.
 struct Logistic {
     float s, rest;
+    __device__ Logistic() {}
     __device__ explicit Logistic(float l) {
-        const float e = expf(-fabsf(l)), big = __fdividef(1.f, 1.f + e), small = e * big;
+        const float e = exp_of(-fabsf(l)), big = __fdividef(1.f, 1.f + e), small = e * big;
         s = l >= 0.f ? big : small;
         rest = l >= 0.f ? small : big;
     }
 };
 
-// A token's scores, its lse (where wanted), in: logits (-inf past E).
-template <int GL, int VPL>
-__device__ __forceinline__ void scores(const float (&l)[VPL], bool sigmoid, bool want_lse, float (&s)[VPL], float& total, float& lse,
-                                       float& top, float& esum) {
-    top = l[0];
+// How a token's experts lie in its lanes: GL lanes, VPL experts each, VEC of them side by side.  With VEC 4 all exist
+// (E = 32 VPL) and are loaded and stored four at a time.
+template <int GL, int VPL, int VEC>
+struct Lanes {
+    static constexpr int kCols = GL * VPL;
+    static __device__ __forceinline__ int expert(int sub, int i) { return i / VEC * GL * VEC + sub * VEC + i % VEC; }
+    static __device__ __forceinline__ void load(const float* row, int sub, int E, bool there, float (&l)[VPL]) {
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
-    top = lanes_max<GL>(top);
-    lse = 0.f;
-    esum = 0.f;
-    if (!sigmoid || want_lse) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            s[i] = expf(l[i] - top);
-            esum += s[i];
+        for (int i = 0; i < VPL; i += VEC) {
+            const int e = expert(sub, i);
+            if constexpr (VEC == 4) {
+                const float4 v = there ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                l[i] = v.x;
+                l[i + 1] = v.y;
+                l[i + 2] = v.z;
+                l[i + 3] = v.w;
+            } else {
+                l[i] = e < E ? (there ? __ldg(row + e) : 0.f) : __uint_as_float(0xFF800000u);
+            }
         }
-        esum = lanes_sum<GL>(esum);
-        lse = top + logf(esum);
-        total = esum;
     }
-    if (sigmoid) {
-        total = 0.f;
+    static __device__ __forceinline__ void store(float* row, int sub, int E, const float (&d)[VPL]) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            s[i] = Logistic(l[i]).s;
-            total += s[i];
+        for (int i = 0; i < VPL; i += VEC) {
+            const int e = expert(sub, i);
+            if constexpr (VEC == 4) __stcs(reinterpret_cast<float4*>(row + e), make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]));
+            else if (e < E) __stcs(row + e, d[i]);
         }
-        total = lanes_sum<GL>(total);
     }
-}
+};
+
+// A token's softmax numerators x (e^(logit - top)) with their sum and lse where they are wanted, and its logistic scores.
+template <int GL, int VPL, bool SIG>
+struct Scores {
+    float x[VPL], top, xsum, lse;
+    Logistic g[SIG ? VPL : 1];
+    float total;  // of the scores
+    __device__ __forceinline__ void compute(const float (&l)[VPL], bool want_lse) {
+        top = xsum = lse = 0.f;
+        if (!SIG || want_lse) {
+            top = l[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
+            top = lanes_max<GL>(top);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                x[i] = exp_of(l[i] - top);
+                xsum += x[i];
+            }
+            xsum = lanes_sum<GL>(xsum);
+            if (want_lse) lse = top + logf(xsum);
+        }
+        if constexpr (SIG) {
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                g[i] = Logistic(l[i]);
+                total += g[i].s;
+            }
+            total = lanes_sum<GL>(total);
+        } else {
+            total = xsum;
+        }
+    }
+    __device__ __forceinline__ float score(int i) const { return SIG ? g[SIG ? i : 0].s : x[i]; }
+};
 
 // The loss of group g's balance, from its sums; called by one CTA.  `sums` are in shared memory.
 __device__ __forceinline__ void group_done(const RouterLossArgs& a, long long g, float dot, float z, int n) {
@@ -129,9 +177,10 @@ __device__ __forceinline__ float cta_sum(float v, float (&red)[kRouterWarps]) {
     return v;
 }
 
-template <int GL, int VPL>
+template <int GL, int VPL, int VEC, bool SIG>
 __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLossArgs a, Split sp) {
-    constexpr int kCols = GL * VPL;
+    using L = Lanes<GL, VPL, VEC>;
+    constexpr int kCols = L::kCols;
     __shared__ float sums[kRouterWarps][kCols];
     __shared__ int hist[kCols];
     __shared__ float red[kRouterWarps];
@@ -148,28 +197,25 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
     constexpr int kPass = kRouterWarps * (32 / GL);
-    const bool sigmoid = a.sigmoid != 0, want = a.z != 0.f;
+    const bool want = a.z != 0.f;
     for (long long tw = t0 + warp * (32 / GL); tw < t1; tw += kPass) {
         const long long t = tw + lane / GL;
         const bool live = t < t1 && (!a.mask || a.mask[t]);
-        float l[VPL], s[VPL], total, lse, top, esum;
-        const float* row = a.logits + (live ? (size_t)t * a.E : 0);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = sub + i * GL;
-            l[i] = e < a.E ? (live ? __ldcs(row + e) : 0.f) : __uint_as_float(0xFF800000u);
-        }
+        if (!__any_sync(kFull, live)) continue;
+        float l[VPL];
+        L::load(a.logits + (live ? (size_t)t * a.E : 0), sub, a.E, live, l);
         if (live && sub < a.k) {
             const unsigned e = (unsigned)__ldg(a.topk_idx + (size_t)t * a.k + sub);
             if (e < (unsigned)a.E) atomicAdd(&hist[e], 1);
         }
-        scores<GL, VPL>(l, sigmoid, want, s, total, lse, top, esum);
+        Scores<GL, VPL, SIG> sc;
+        sc.compute(l, want);
         if (live) {
-            const float inv = __fdividef(1.f, total);
+            const float inv = __fdividef(1.f, sc.total);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+            for (int i = 0; i < VPL; ++i) acc[i] = fmaf(sc.score(i), inv, acc[i]);
             if (sub == 0) {
-                z = fmaf(lse, lse, z);
+                z = fmaf(sc.lse, sc.lse, z);
                 ++n;
             }
         }
@@ -181,7 +227,7 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
         for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
     if (lane < GL)
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sums[warp][sub + i * GL] = acc[i];
+        for (int i = 0; i < VPL; ++i) sums[warp][L::expert(sub, i)] = acc[i];
     z = cta_sum(z, red);
     const int tokens = (int)cta_sum((float)n, red);  // (below 2^24: a chunk)
     float dot = 0.f;
@@ -269,9 +315,10 @@ __global__ void __launch_bounds__(kRouterThreads) balance_total_kernel(const Rou
     }
 }
 
-template <int GL, int VPL>
+template <int GL, int VPL, int VEC, bool SIG>
 __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterLossArgs a, Split sp) {
-    constexpr int kCols = GL * VPL, kPer = 32 / GL;  // tokens of a warp
+    using L = Lanes<GL, VPL, VEC>;
+    constexpr int kCols = L::kCols, kPer = 32 / GL;  // tokens of a warp
     __shared__ float delta[kRouterWarps * kPer][kCols];    // the gates' gradient of a token's picks
     wait_for_kernel_before();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % GL;
@@ -286,15 +333,15 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
         const float coef = n > 0 ? a.balance * ((float)a.E / ((float)a.groups * (float)a.k * (float)n * (float)n)) : 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int e = sub + i * GL;
+            const int e = L::expert(sub, i);
             w[i] = coef != 0.f && e < a.E ? coef * (float)__ldg(a.load + g * a.E + e) : 0.f;
             mine[e] = 0.f;
         }
     }
     const int all = a.z != 0.f ? __ldg(a.tokens + a.groups) : 0;
     const float zc = all > 0 ? 2.f * a.z / (float)all : 0.f;
-    const bool sigmoid = a.sigmoid != 0, losses = a.balance != 0.f || a.z != 0.f;
-    const bool full = losses || (!sigmoid && !a.renorm);  // the gradient is not of the picks alone
+    const bool losses = a.balance != 0.f || a.z != 0.f;
+    const bool full = losses || (!SIG && !a.renorm);  // the gradient is not of the picks alone
     __syncwarp();
     for (long long tw = t0 + warp * kPer; tw < t1; tw += kRouterWarps * kPer) {
         const long long t = tw + lane / GL;
@@ -316,82 +363,83 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
         }
         float gate_dot = 0.f, pick_p = 0.f;
         if (full) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = sub + i * GL;
-                l[i] = e < a.E ? (there ? __ldg(row + e) : 0.f) : __uint_as_float(0xFF800000u);
-            }
-            float s[VPL], total, lse, top, esum;
-            scores<GL, VPL>(l, sigmoid, zc != 0.f, s, total, lse, top, esum);
-            const float inv = __fdividef(1.f, total);
-            if (!sigmoid && !a.renorm) {  // gates that are entries of the softmax over all experts
-                pick_p = pick >= 0 ? expf(pl - top) * inv : 0.f;
+            L::load(row, sub, a.E, there, l);
+            Scores<GL, VPL, SIG> sc;
+            sc.compute(l, zc != 0.f);
+            const float inv = __fdividef(1.f, sc.total);
+            if (!SIG && !a.renorm) {  // gates that are entries of the softmax over all experts
+                pick_p = pick >= 0 ? exp_of(pl - sc.top) * inv : 0.f;
                 gate_dot = lanes_sum<GL>(pick_p * dw);
             }
             float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) dot = fmaf(s[i] * inv, w[i], dot);
+            for (int i = 0; i < VPL; ++i) dot = fmaf(sc.score(i) * inv, w[i], dot);
             dot = lanes_sum<GL>(dot);
-            const float zt = counted ? zc * lse : 0.f, zinv = sigmoid && zc != 0.f ? __fdividef(1.f, esum) : inv;
+            const float zt = counted ? zc * sc.lse * (SIG && zc != 0.f ? __fdividef(1.f, sc.xsum) : inv) : 0.f;
+            const float pinv = counted ? inv : 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                const float p = s[i] * inv;
-                float v = counted ? p * (w[i] - dot) : 0.f;
-                if (sigmoid) v *= Logistic(l[i]).rest;
-                if (zc != 0.f) v = fmaf(zt, sigmoid ? expf(l[i] - top) * zinv : p, v);
-                d[i] = fmaf(-gate_dot, p, v);
+                const float v = sc.score(i) * pinv * (w[i] - dot);
+                if constexpr (SIG) d[i] = v * sc.g[i].rest;
+                else d[i] = fmaf(-gate_dot * inv, sc.x[i], v);
             }
+            if (zc != 0.f)
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) d[i] = fmaf(zt, sc.x[i], d[i]);
         }
         if (a.dtopk_w) {
             float v;
-            if (!sigmoid && !a.renorm) {
+            if (!SIG && !a.renorm) {
                 v = pick_p * dw;
             } else if (!a.renorm) {
                 const Logistic g(pl);
                 v = dw * g.s * g.rest;
             } else {
                 float s = 0.f;
-                if (sigmoid) {
+                if (SIG) {
                     s = pick >= 0 ? Logistic(pl).s : 0.f;
                 } else {
                     const float top = lanes_max<GL>(pl);
-                    s = pick >= 0 ? expf(pl - top) : 0.f;
+                    s = pick >= 0 ? exp_of(pl - top) : 0.f;
                 }
                 const float gate = s * __fdividef(1.f, lanes_sum<GL>(s));
                 v = gate * (dw - lanes_sum<GL>(gate * dw));
-                if (sigmoid) v *= Logistic(pl).rest;
+                if (SIG) v *= Logistic(pl).rest;
             }
             if (pick >= 0) atomicAdd(mine + pick, v);
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) d[i] += mine[sub + i * GL];
+            for (int i = 0; i < VPL; ++i) d[i] += mine[L::expert(sub, i)];
             __syncwarp();
             if (pick >= 0) mine[pick] = 0.f;
             __syncwarp();
         }
-        if (there) {
-            float* out = a.dlogits + (size_t)t * a.E;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = sub + i * GL;
-                if (e < a.E) __stcs(out + e, d[i]);
-            }
-        }
+        if (there) L::store(a.dlogits + (size_t)t * a.E, sub, a.E, d);
     }
 }
 
-// go(lanes a token, experts a lane)
+// go(lanes a token, experts a lane, experts side by side, logistic scores)
 template <class Go>
-cudaError_t by_experts(int E, Go go) {
+cudaError_t by_experts(const RouterLossArgs& a, bool vec, Go go) {
     using std::integral_constant;
-    if (E <= 8) return go(integral_constant<int, 8>(), integral_constant<int, 1>());
-    if (E <= 16) return go(integral_constant<int, 16>(), integral_constant<int, 1>());
-    if (E <= 32) return go(integral_constant<int, 32>(), integral_constant<int, 1>());
-    if (E <= 64) return go(integral_constant<int, 32>(), integral_constant<int, 2>());
-    if (E <= 128) return go(integral_constant<int, 32>(), integral_constant<int, 4>());
-    if (E <= 256) return go(integral_constant<int, 32>(), integral_constant<int, 8>());
-    if (E <= 512) return go(integral_constant<int, 32>(), integral_constant<int, 16>());
-    return go(integral_constant<int, 32>(), integral_constant<int, 32>());
+    auto lanes = [&](auto gl, auto vpl, auto v) {
+        return a.sigmoid ? go(gl, vpl, v, std::true_type()) : go(gl, vpl, v, std::false_type());
+    };
+    constexpr integral_constant<int, 1> one;
+    constexpr integral_constant<int, 4> four;
+    constexpr integral_constant<int, 32> warp;
+    const int E = a.E;
+    if (E <= 8) return lanes(integral_constant<int, 8>(), one, one);
+    if (E <= 16) return lanes(integral_constant<int, 16>(), one, one);
+    if (E <= 32) return lanes(warp, one, one);
+    if (E <= 64) return lanes(warp, integral_constant<int, 2>(), one);
+    if (vec && E == 128) return lanes(warp, four, four);
+    if (vec && E == 256) return lanes(warp, integral_constant<int, 8>(), four);
+    if (vec && E == 512) return lanes(warp, integral_constant<int, 16>(), four);
+    if (E <= 128) return lanes(warp, four, one);
+    if (E <= 256) return lanes(warp, integral_constant<int, 8>(), one);
+    if (E <= 512) return lanes(warp, integral_constant<int, 16>(), one);
+    return lanes(warp, integral_constant<int, 32>(), one);
 }
 
 }  // namespace
@@ -405,8 +453,10 @@ size_t balance_scratch_bytes(int T, int E, int seq_len, int sm_count) {
 cudaError_t launch_balance_loss(const RouterLossArgs& a, int sm_count, cudaStream_t stream) {
     const Split sp = split_of(a.T, a.E, a.seq_len, a.groups, sm_count);
     if (sp.blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-    cudaError_t e = by_experts(a.E, [&](auto gl, auto vpl) {
-        return launch_after(balance_kernel<decltype(gl)::value, decltype(vpl)::value>, (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
+    const bool vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    cudaError_t e = by_experts(a, vec, [&](auto gl, auto vpl, auto v, auto sig) {
+        return launch_after(balance_kernel<decltype(gl)::value, decltype(vpl)::value, decltype(v)::value, decltype(sig)::value>,
+                            (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
     });
     if (e == cudaSuccess && sp.chunks > 1) e = launch_after(balance_groups_kernel, (unsigned)a.groups, kRouterThreads, 0, stream, a, sp);
     if (e == cudaSuccess && a.groups > 1) e = launch_after(balance_total_kernel, 1u, kRouterThreads, 0, stream, a);
@@ -416,8 +466,10 @@ cudaError_t launch_balance_loss(const RouterLossArgs& a, int sm_count, cudaStrea
 cudaError_t launch_router_backward(const RouterLossArgs& a, int sm_count, cudaStream_t stream) {
     const Split sp = split_of(a.T, a.E, a.seq_len, a.groups, sm_count);
     if (sp.blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-    return by_experts(a.E, [&](auto gl, auto vpl) {
-        return launch_after(router_backward_kernel<decltype(gl)::value, decltype(vpl)::value>, (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0;
+    return by_experts(a, vec, [&](auto gl, auto vpl, auto v, auto sig) {
+        return launch_after(router_backward_kernel<decltype(gl)::value, decltype(vpl)::value, decltype(v)::value, decltype(sig)::value>,
+                            (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
     });
 }
 
