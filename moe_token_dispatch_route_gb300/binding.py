@@ -568,8 +568,12 @@ def loss_groups(plan: Plan, seq_len: int) -> int:
 
 
 def _balance_scratch_bytes(plan: Plan, seq_len: int) -> int:
+    known = plan.__dict__.setdefault("balance_scratch_bytes", {})  # of the plan's shape and seq_len alone
+    if seq_len in known:
+        return known[seq_len]
     n = ctypes.c_size_t()
     _check(load_library().moe_balance_scratch(plan.handle, seq_len, ctypes.byref(n)), "moe_balance_scratch")
+    known[seq_len] = n.value
     return n.value
 
 

@@ -54,21 +54,20 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 template <int GL>
 __device__ __forceinline__ float lanes_max(float v) {
+    if constexpr (GL == 32) {
+        asm("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(v));
+    } else {
 #pragma unroll
-    for (int o = GL / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+        for (int o = GL / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    }
     return v;
 }
 
-// e^x for x <= 0 within 3 units in the last place.  x log2(e) is rounded, and what the rounding left out is put back
-// to first order; the fast exponential alone is off by 1.2 |x| units, 4e-6 of a gradient.  Below -120 the result is 0 (so for
-// -infinity too); NaN stays NaN.
+// e^x for x <= 0, within 2 + 1.2 |x| units in the last place: the far terms that are off by more are the small ones.
 __device__ __forceinline__ float exp_of(float x) {
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-120.f));
-    constexpr float kLog2e = 1.4426950216293335f, kRest = 1.9259629911e-8f;  // log2(e) = kLog2e + kRest
-    const float t = __fmul_rn(x, kLog2e), left = fmaf(x, kRest, fmaf(x, kLog2e, -t));
     float p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-    return fmaf(p, left * 0.69314718f, p);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(__fmul_rn(x, 1.4426950408889634f)));
+    return p;
 }
 
 // s = 1 / (1 + e^-l) and 1 - s from e^-|l|, which does not overflow: neither is the other's difference from 1, which
@@ -111,6 +110,25 @@ struct Lanes {
             if constexpr (VEC == 4) __stcs(reinterpret_cast<float4*>(row + e), make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]));
             else if (e < E) __stcs(row + e, d[i]);
         }
+    }
+};
+
+// What is read of a token; in the forward pass while the one before it is worked on.
+template <int GL, int VPL, int VEC>
+struct Token {
+    float l[VPL], dw;
+    int pick;  // lane j's: pick j, or -1
+    bool there, counted;
+    __device__ __forceinline__ void fetch(const RouterLossArgs& a, long long t, long long t1, int sub, bool gates) {
+        there = t < t1;
+        counted = there && (!a.mask || __ldg(a.mask + t));
+        pick = -1;
+        dw = 0.f;
+        if (there && sub < a.k && a.topk_idx) {
+            pick = __ldg(a.topk_idx + (size_t)t * a.k + sub);
+            if (gates) dw = __ldg(a.dtopk_w + (size_t)t * a.k + sub);
+        }
+        Lanes<GL, VPL, VEC>::load(a.logits + (there ? (size_t)t * a.E : 0), sub, a.E, there, l);
     }
 };
 
@@ -198,18 +216,16 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
     for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
     constexpr int kPass = kRouterWarps * (32 / GL);
     const bool want = a.z != 0.f;
+    Token<GL, VPL, VEC> next;
+    next.fetch(a, t0 + warp * (32 / GL) + lane / GL, t1, sub, false);
     for (long long tw = t0 + warp * (32 / GL); tw < t1; tw += kPass) {
-        const long long t = tw + lane / GL;
-        const bool live = t < t1 && (!a.mask || a.mask[t]);
+        const Token<GL, VPL, VEC> now = next;
+        if (tw + kPass < t1) next.fetch(a, tw + kPass + lane / GL, t1, sub, false);
+        const bool live = now.counted;
         if (!__any_sync(kFull, live)) continue;
-        float l[VPL];
-        L::load(a.logits + (live ? (size_t)t * a.E : 0), sub, a.E, live, l);
-        if (live && sub < a.k) {
-            const unsigned e = (unsigned)__ldg(a.topk_idx + (size_t)t * a.k + sub);
-            if (e < (unsigned)a.E) atomicAdd(&hist[e], 1);
-        }
+        if (live && (unsigned)now.pick < (unsigned)a.E) atomicAdd(&hist[now.pick], 1);
         Scores<GL, VPL, SIG> sc;
-        sc.compute(l, want);
+        sc.compute(now.l, want);
         if (live) {
             const float inv = __fdividef(1.f, sc.total);
 #pragma unroll
@@ -319,7 +335,7 @@ template <int GL, int VPL, int VEC, bool SIG>
 __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterLossArgs a, Split sp) {
     using L = Lanes<GL, VPL, VEC>;
     constexpr int kCols = L::kCols, kPer = 32 / GL;  // tokens of a warp
-    __shared__ float delta[kRouterWarps * kPer][kCols];    // the gates' gradient of a token's picks
+    __shared__ __align__(16) float delta[kRouterWarps * kPer][kCols];    // the gates' gradient of a token's picks
     wait_for_kernel_before();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % GL;
     const long long g = blockIdx.x / sp.chunks;
@@ -344,28 +360,20 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
     const bool full = losses || (!SIG && !a.renorm);  // the gradient is not of the picks alone
     __syncwarp();
     for (long long tw = t0 + warp * kPer; tw < t1; tw += kRouterWarps * kPer) {
+        Token<GL, VPL, VEC> now;
+        now.fetch(a, tw + lane / GL, t1, sub, a.dtopk_w != nullptr);
         const long long t = tw + lane / GL;
-        const bool there = t < t1, counted = there && (!a.mask || a.mask[t]);
-        const float* row = a.logits + (there ? (size_t)t * a.E : 0);
-        float l[VPL], d[VPL];
+        const bool there = now.there, counted = now.counted;
+        float d[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = 0.f;
         // the picks: lane j holds pick j
-        int pick = -1;
-        float pl = __uint_as_float(0xFF800000u), dw = 0.f;
-        if (a.dtopk_w && there && sub < a.k) {
-            const unsigned e = (unsigned)__ldg(a.topk_idx + (size_t)t * a.k + sub);
-            if (e < (unsigned)a.E) {
-                pick = (int)e;
-                pl = __ldg(row + e);
-                dw = __ldg(a.dtopk_w + (size_t)t * a.k + sub);
-            }
-        }
+        const int pick = a.dtopk_w && (unsigned)now.pick < (unsigned)a.E ? now.pick : -1;
+        const float pl = pick >= 0 ? __ldg(a.logits + (size_t)t * a.E + pick) : __uint_as_float(0xFF800000u), dw = pick >= 0 ? now.dw : 0.f;
         float gate_dot = 0.f, pick_p = 0.f;
         if (full) {
-            L::load(row, sub, a.E, there, l);
             Scores<GL, VPL, SIG> sc;
-            sc.compute(l, zc != 0.f);
+            sc.compute(now.l, zc != 0.f);
             const float inv = __fdividef(1.f, sc.total);
             if (!SIG && !a.renorm) {  // gates that are entries of the softmax over all experts
                 pick_p = pick >= 0 ? exp_of(pl - sc.top) * inv : 0.f;
@@ -409,7 +417,17 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
             if (pick >= 0) atomicAdd(mine + pick, v);
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) d[i] += mine[L::expert(sub, i)];
+            for (int i = 0; i < VPL; i += VEC) {
+                if constexpr (VEC == 4) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(mine + L::expert(sub, i));
+                    d[i] += v4.x;
+                    d[i + 1] += v4.y;
+                    d[i + 2] += v4.z;
+                    d[i + 3] += v4.w;
+                } else {
+                    d[i] += mine[L::expert(sub, i)];
+                }
+            }
             __syncwarp();
             if (pick >= 0) mine[pick] = 0.f;
             __syncwarp();
