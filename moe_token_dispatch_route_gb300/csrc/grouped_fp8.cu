@@ -379,13 +379,15 @@ __device__ void mma_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, int t
     uint32_t phase = 0, free_phase[2] = {1, 1};
     // a tile's k-blocks go to accumulator 0 and 1 in turn, from 0 on
     auto block = [&](int buf, int steps) {
-        const bool there = tmem_wait(tempty0 + 8 * buf, free_phase[buf], w, 72) && bar_wait(full0 + 8 * s, phase, w, 73);
-        if (!__all_sync(kFull, there)) return false;
-        free_phase[buf] ^= 1u;
+        // (the loads are long there; the accumulator is what this warp waits for, so it is waited for last)
+        const bool landed = bar_wait(full0 + 8 * s, phase, w, 73);
         if (gathered) fence_proxy_async_smem();  // this CTA's copies
-        tc_fence_after();
         const uint64_t ad = ad0 + (uint32_t)(s * (C::kStageBytes >> 4)), bd = bd0 + (uint32_t)(s * (C::kStageBytes >> 4));
         const uint32_t d = tmem + 256u * buf;
+        const bool there = landed && tmem_wait(tempty0 + 8 * buf, free_phase[buf], w, 72);
+        if (!__all_sync(kFull, there)) return false;
+        free_phase[buf] ^= 1u;
+        tc_fence_after();
         if (elected()) {
 #pragma unroll
             for (int k = 0; k < steps; ++k) {
@@ -439,21 +441,27 @@ __device__ __forceinline__ void rows_out(uint8_t* staging, const uint4 (&v)[4], 
     __syncwarp();
 }
 
-// silu(g) u of four values in place of u.  g / (1 + e^-g) from e^-|g|, which does not overflow; the four quotients share one
-// reciprocal (the exponentials and reciprocals are what bounds the activation: five in place of eight).  The
-// exponential is within 2 + 1.173 |g| units in its last place and the quotient within 6.  A NaN makes NaN of all
-// four, as its block's scale does in any case.
+// u *= silu(g) for four values.  With e = e^-|g| and q = e / (1 + e), silu(g) = max(g, 0) - |g| q: nothing overflows, and far
+// negative g keeps its small result (e is the square of e^(-|g| / 2), whose own fast form would flush it).  The four
+// quotients share one reciprocal: the exponentials and reciprocals are what bounds the activation, five in place of
+// eight.  A NaN makes NaN of all four, as its block's scale does in any case.
 __device__ __forceinline__ void silu4(const float* g, float* u) {
-    float e[4], d[4];
+    float e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        e[i] = __expf(-fabsf(g[i]));
-        d[i] = 1.f + e[i];
-    }
-    const float lo = d[0] * d[1], hi = d[2] * d[3], r = __fdividef(1.f, lo * hi), rl = r * hi, rh = r * lo;
-    const float inv[4] = {rl * d[1], rl * d[0], rh * d[3], rh * d[2]};
+    for (int i = 0; i < 4; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(fabsf(g[i]) * -0.72134752f));  // log2(e) / 2
+    float2 lo = make_float2(e[0], e[1]), hi = make_float2(e[2], e[3]);
+    lo = __fmul2_rn(lo, lo);
+    hi = __fmul2_rn(hi, hi);
+    const float2 dl = __fadd2_rn(lo, make_float2(1.f, 1.f)), dh = __fadd2_rn(hi, make_float2(1.f, 1.f));
+    const float pl = dl.x * dl.y, ph = dh.x * dh.y;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pl * ph));
+    const float rl = r * ph, rh = r * pl;
+    const float2 ql = __fmul2_rn(lo, __fmul2_rn(make_float2(rl, rl), make_float2(dl.y, dl.x)));
+    const float2 qh = __fmul2_rn(hi, __fmul2_rn(make_float2(rh, rh), make_float2(dh.y, dh.x)));
+    const float q[4] = {ql.x, ql.y, qh.x, qh.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] *= g[i] * (inv[i] * (g[i] >= 0.f ? 1.f : e[i]));
+    for (int i = 0; i < 4; ++i) u[i] *= fmaf(-fabsf(g[i]), q[i], g[i] < 0.f ? 0.f : g[i]);
 }
 
 // Warps 4-11: TMEM lane quarter q = warp & 3 (rows) and half h of the columns of both blocks.
@@ -562,11 +570,12 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
         if (p.a.glu) {
             const int F = p.a.N / 2, col = kBlk * t.c + 64 * h;
             float(&hv)[64] = acc[1];
-            uint32_t amax = 0;
+            float big = 0.f;
 #pragma unroll
             for (int j = 0; j < 64; j += 4) silu4(acc[0] + j, hv + j);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) amax = max(amax, __float_as_uint(hv[j]) & 0x7FFFFFFFu);
+            for (int j = 0; j < 64; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(big) : "f"(fabsf(hv[j])));
+            uint32_t amax = __float_as_uint(big);
             ctl->amax[turn][h][32 * q + lane] = __uint_as_float(amax);
             __syncwarp();
             warp_arrive<false>(smem_addr(&ctl->amax_there[q]));
@@ -816,7 +825,11 @@ cudaError_t launch_grouped_fp8(const GroupedFp8Args& a, int device, int sm_count
     p.nkb = scale_blocks(a.d);
     p.as_vec = p.nkb % 4 == 0 && reinterpret_cast<uintptr_t>(a.A_scales) % 16 == 0;
     p.c_tiles = a.glu ? scale_blocks(n) : (a.N + 255) / 256;
-    const bool pair = a.S >= 128LL * a.E;  // pairs where the experts have that many rows on average
+    // Pairs of CTAs load half of W each, but waste more rows of an expert's last tile, and gathered rows reach the leader's
+    // MMAs through one more thread.  us with one CTA a tile and in pairs: rows in place, 32 experts of 4096 x 4096, 256
+    // rows each 161 and 178, 512 265 and 264, 768 417 and 379, 2048 983 and 941; gathered, 2048 x 2816 SwiGLU, 1024 rows
+    // 433 and 459, 4096 x 8192, 2048 rows 500 and 493.
+    const bool pair = a.S >= (a.perm ? 1536LL : 512LL) * a.E;
     const uint64_t rows = a.perm ? (uint64_t)a.T : (uint64_t)a.S;
     if (!map_e4m3_2d(&p.a_map, a.A, rows, (uint64_t)a.d, 128) || !map_e4m3_2d(&p.a_part, a.A, rows, (uint64_t)a.d, 32) ||
         !map_e4m3_weights(&p.w_map, a.W, (uint64_t)a.E, (uint64_t)halves, (uint64_t)n, (uint64_t)a.d))

@@ -96,9 +96,10 @@ __device__ __forceinline__ float block_quotient(uint32_t amax_bits, bool inverse
 
 // four codes; inv = 0 is a block of codes 0 (its values may be infinite or NaN)
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
+    const float2 scale = make_float2(inv, inv), x = __fmul2_rn(make_float2(a, b), scale), y = __fmul2_rn(make_float2(c, d), scale);
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(b, inv)), "f"(__fmul_rn(a, inv)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(d, inv)), "f"(__fmul_rn(c, inv)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y.y), "f"(y.x));
     return inv == 0.f ? 0u : (uint32_t)lo | (uint32_t)hi << 16;
 }
 

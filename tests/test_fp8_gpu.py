@@ -333,7 +333,8 @@ def fp8_run(T, d, E, k, N, ops, dtype):
 FP8_SHAPES = [(1, 16, 1, 1, 16, "even"), (1, 64, 4, 2, 48, "even"), (5, 128, 3, 1, 272, "even"), (37, 144, 8, 2, 528, "skew"),
               (64, 1040, 16, 8, 512, "even"), (200, 1040, 5, 3, 1296, "skew"), (600, 2064, 2, 2, 784, "even"),
               (129, 4096, 1, 1, 256, "even"), (3000, 512, 8, 2, 1024, "skew"), (4096, 256, 64, 2, 1408, "even"),
-              (500, 384, 256, 2, 512, "even"), (20, 14336, 8, 2, 272, "even")]
+              (500, 384, 256, 2, 512, "even"), (20, 14336, 8, 2, 272, "even"), (3300, 400, 2, 1, 784, "even"),
+              (5000, 1040, 2, 2, 288, "skew")]
 
 
 @pytest.mark.parametrize("T,d,E,k,N,load", FP8_SHAPES)
@@ -348,7 +349,8 @@ def test_grouped_gemm_fp8(T, d, E, k, N, load, gather, dtype):
 
 @pytest.mark.parametrize("T,d,E,k,F,load", [(1, 16, 1, 1, 16, "even"), (5, 128, 3, 1, 144, "even"), (37, 144, 8, 2, 272, "skew"),
                                             (64, 1040, 16, 8, 256, "even"), (600, 2064, 2, 2, 400, "even"),
-                                            (4096, 256, 64, 2, 704, "skew"), (500, 384, 256, 2, 128, "even")])
+                                            (4096, 256, 64, 2, 704, "skew"), (500, 384, 256, 2, 128, "even"),
+                                            (3300, 400, 2, 1, 272, "even"), (5000, 1040, 2, 2, 144, "skew")])
 @pytest.mark.parametrize("gather", [False, True])
 def test_grouped_gemm_fp8_swiglu(T, d, E, k, F, load, gather):
     ops = operands(T, d, E, k, 2 * F, 2, gather, load)
@@ -372,7 +374,7 @@ def test_grouped_gemm_fp8_swiglu(T, d, E, k, F, load, gather):
     check_8bit(H[:S], Hs[:S], ref, err, "H")
 
 
-@pytest.mark.parametrize("T,E", [(40, 4), (1200, 4)])
+@pytest.mark.parametrize("T,E", [(40, 4), (1200, 4), (3300, 4)])
 @pytest.mark.parametrize("gather", [False, True])
 def test_fp8_rows_and_columns_that_are_not_numbers_stay_alone(T, E, gather):
     """A NaN code or scale of a row of A is that row's alone, one of W's rows its expert's column's."""
@@ -459,3 +461,90 @@ def test_fp8_is_the_same_in_a_graph_and_on_another_stream():
     graph.replay()
     ref, mag = product((offsets, perm, A, As, W, Ws), k, 1)
     within(Y, ref, product_rounds(d) * U * mag + 2.0 ** -126)
+
+
+def test_operators_beyond_two_to_the_31_elements():
+    """Offsets of rows and results that pass 32 bits: the last rows are right."""
+    T, d, N = 1 << 20, 16, 2064
+    ops = operands(T, d, 1, 1, N, 1, False, "even", seed=100)
+    plan = binding.moe_plan(T, d, 1, 1, N, out_dtype=binding.MOE_OUT_BF16)
+    Y = torch.empty(T, N, dtype=BF16, device=DEV)
+    ws, st = buffers(plan)
+    binding.moe_grouped_gemm_fp8(plan, *ops[2:4], None, ops[0], *ops[4:], Y, ws, st)
+    assert binding.moe_read_status(st)[0] == 0
+    last = (torch.tensor([0, 300], dtype=I32, device=DEV), None, ops[2][-300:], ops[3][-300:], ops[4], ops[5])
+    ref, mag = product(last, 1, 1)
+    within(Y[-300:], ref, product_rounds(d) * U * mag + 2.0 ** -8 * ref.abs() + 2.0 ** -126)
+    del Y
+    T, d = (1 << 17) + 5, 16400
+    x = randn((T, d), 101, BF16)
+    plan = binding.moe_plan(T, d, 1, 1, 256)
+    y, codes, scales = torch.empty_like(x), torch.empty(T, d, dtype=E4M3, device=DEV), torch.empty(T, blocks(d), device=DEV)
+    binding.moe_rmsnorm(plan, x, None, None, 1e-5, None, y, codes, scales)
+    _, _, ref = rms_ref(x[-3:], None, None, BF16)
+    err = ((d / 64 + 64) / 2 + 8) * U * ref.abs()
+    within(y[-3:], ref, err + 2.0 ** -8 * ref.abs())
+    check_8bit(codes[-3:], scales[-3:], ref, err)
+
+
+def test_calls_on_two_streams_at_once():
+    """The products keep nothing in the workspace or between calls: two at a time on one plan give what each gives alone."""
+    T, d, E, k, N = 2000, 1024, 4, 2, 1024
+    a, c = operands(T, d, E, k, N, 1, True, "even", seed=110), operands(T, d, E, k, N, 1, True, "skew", seed=120)
+    plan = binding.moe_plan(T, d, E, k, N)
+    ws, st = buffers(plan)
+    alone, both = [], [torch.zeros(T * k, N, device=DEV) for _ in range(2)]
+    for o in (a, c):
+        Y = torch.zeros(T * k, N, device=DEV)
+        binding.moe_grouped_gemm_fp8(plan, o[2], o[3], o[1], o[0], o[4], o[5], Y, ws, st)
+        alone.append(Y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o, Y, s in zip((a, c), both, streams):
+            binding.moe_grouped_gemm_fp8(plan, o[2], o[3], o[1], o[0], o[4], o[5], Y, ws, st, stream=s)
+    torch.cuda.synchronize()
+    assert binding.moe_read_status(st)[0] == 0
+    for x, y in zip(alone, both):
+        assert torch.equal(x, y)
+
+
+def test_unaligned_scales_and_views():
+    """Scales that start at any 4 bytes, and results that are views of larger buffers."""
+    T, d, E, k, N = 300, 512, 4, 2, 256   # four k-blocks: the aligned form copies 16 bytes of scales at a time
+    offsets, perm, A, As, W, Ws = operands(T, d, E, k, N, 1, True, "even", seed=130)
+    want = fp8_run(T, d, E, k, N, (offsets, perm, A, As, W, Ws), F32)
+    room = torch.empty(As.numel() + 1, device=DEV)
+    room[1:] = As.reshape(-1)
+    assert torch.equal(fp8_run(T, d, E, k, N, (offsets, perm, A, room[1:].reshape(As.shape), W, Ws), F32), want)
+    wide = torch.empty(Ws.numel() + 3, device=DEV)
+    wide[3:] = Ws.reshape(-1)
+    assert torch.equal(fp8_run(T, d, E, k, N, (offsets, perm, A, As, W, wide[3:].reshape(Ws.shape)), F32), want)
+
+
+def test_misaligned_operands_are_refused():
+    T, d, E, k, N = 8, 128, 2, 1, 256
+    offsets, perm, A, As, W, Ws = operands(T, d, E, k, N, 1, False, "even")
+    plan = binding.moe_plan(T, d, E, k, N)
+    ws, st = buffers(plan)
+    room = torch.empty(A.numel() + 8, dtype=torch.uint8, device=DEV)[8:].view(E4M3).reshape(A.shape)
+    Y = torch.full((T, N), 7.0, device=DEV)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):
+        binding.moe_grouped_gemm_fp8(plan, room, As, perm, offsets, W, Ws, Y, ws, st)
+    odd = binding.moe_plan(T, d, E, k, 272)
+    H, Hs = torch.empty(T, 136, device=DEV).to(E4M3), torch.empty(T, 2, device=DEV)
+    W, Ws = codes_of((E, 272, d), 1), scales_of((E, 4, 1), 2, 1.0)
+    ws, st = buffers(odd)
+    with pytest.raises(binding.MoeError, match="UNSUPPORTED"):
+        binding.moe_grouped_gemm_fp8_swiglu(odd, A, As, perm, offsets, W, Ws, H, Hs, ws, st)
+    with pytest.raises(binding.MoeError, match="UNSUPPORTED"):
+        binding.moe_quantize_weights(odd, randn((E, d, 272), 1, BF16), W, Ws, halves=2)
+    x = randn((T, d), 5)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):  # neither output
+        binding.moe_rmsnorm(plan, x, None, None, 1e-5, None, None)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):  # codes without scales
+        binding.moe_rmsnorm(plan, x, None, None, 1e-5, None, None, A)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):
+        binding.moe_rmsnorm(plan, x, None, None, 0.0, None, x.to(BF16))
+    torch.cuda.synchronize()
+    assert (Y == 7.0).all()

@@ -222,3 +222,58 @@ def test_the_same_bits_on_every_run_and_in_a_graph():
         binding.moe_router_backward(plan, logits, idx, dw, mask, seq, 1.0, 0.1, out[1], out[2], dl2)
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(first, out)) and torch.equal(dl, dl2)
+
+
+def test_scratch_and_coefficients_that_are_refused():
+    plan, logits, idx, dw, _ = setup(5000, 64, 2, "softmax", False, 0)
+    loss, load, tokens = torch.empty(2, device=DEV), torch.empty(1, 64, dtype=I32, device=DEV), torch.empty(2, dtype=I32, device=DEV)
+    scratch = binding.balance_scratch(plan, 0)
+    with pytest.raises(ValueError, match="scratch"):
+        binding.moe_balance_loss(plan, logits, idx, None, 0, 1.0, 1.0, loss, load, tokens, scratch[:-4])
+    with pytest.raises(binding.MoeError, match="WORKSPACE"):
+        binding.moe_balance_loss(plan, logits, idx, None, 0, 1.0, 1.0, loss, load, tokens, None)
+    for bad in (float("nan"), float("inf")):
+        with pytest.raises(binding.MoeError, match="INVALID_ARG"):
+            binding.moe_balance_loss(plan, logits, idx, None, 0, bad, 1.0, loss, load, tokens, scratch)
+    dl = torch.empty_like(logits)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):  # a loss without its counts
+        binding.moe_router_backward(plan, logits, idx, dw, None, 0, 1.0, 0.0, None, tokens, dl)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):
+        binding.moe_router_backward(plan, logits, idx, dw, None, 0, 0.0, 1.0, None, None, dl)
+    with pytest.raises(binding.MoeError, match="INVALID_ARG"):  # gates without their picks
+        binding.moe_router_backward(plan, logits, None, dw, None, 0, 0.0, 0.0, None, None, dl)
+
+
+def test_picks_outside_the_experts_are_not_counted_and_get_no_gradient():
+    T, E, k = 70, 40, 3
+    plan, logits, idx, dw, _ = setup(T, E, k, "sigmoid", False, 0, seed=41)
+    idx[5, 1], idx[9, 2] = -1, E
+    loss, load, tokens = forward(plan, logits, idx, None, 0, 1.0, 0.0)
+    assert int(load.sum()) == T * k - 2
+    dl = torch.full_like(logits, float("nan"))
+    binding.moe_router_backward(plan, logits, idx, dw, None, 0, 0.0, 0.0, None, None, dl)
+    x = logits.double().requires_grad_(True)
+    ok = (idx >= 0) & (idx < E)
+    (torch.sigmoid(x).gather(1, idx.clamp(0, E - 1).long()) * dw.double() * ok).sum().backward()
+    assert ((dl.double() - x.grad).abs() <= 64 * U * x.grad.abs() + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("E", [128, 256, 512])
+def test_logits_at_any_four_bytes(E):
+    """The vectorised form is for 16-byte aligned rows; others give the same."""
+    T, k = 60, 4
+    plan, logits, idx, dw, mask = setup(T, E, k, "renorm", True, 25, seed=51)
+    room = torch.empty(T * E + 1, device=DEV)
+    room[1:] = logits.reshape(-1)
+    odd = room[1:].reshape(T, E)
+    results = []
+    for x in (logits, odd):
+        loss, load, tokens = forward(plan, x, idx, mask, 25, 1.0, 0.5)
+        dl = torch.full((T * E + 1,), float("nan"), device=DEV)[1:].reshape(T, E) if x is odd else torch.full_like(x, float("nan"))
+        binding.moe_router_backward(plan, x, idx, dw, mask, 25, 1.0, 0.5, load, tokens, dl)
+        results.append((loss, load, tokens, dl))
+    assert torch.equal(results[0][1], results[1][1]) and torch.equal(results[0][2], results[1][2])
+    assert ((results[0][0] - results[1][0]).abs() <= 400 * U * results[0][0].abs()).all()
+    grad = reference(logits, idx, dw, mask, 25, 1.0, 0.5, "renorm")[4]
+    for _, load, tokens, dl in results:
+        check_gradient(dl, grad, logits, idx, dw, load, tokens.tolist(), 25, 1.0, 0.5, "renorm")
