@@ -67,12 +67,30 @@ struct Fp8Ctl {
     float4 ws[kScaleRing][2];   // and of the two blocks of W
 };
 
+// Division of an int >= 0 by a number that the host knows: by ceil(2^64 / n), exact below 2^31.  (Three integer divisions were
+// most of the thousand cycles that a tile's place took.)
+struct Divisor {
+    uint64_t inverse;  // 0: n is 1
+    static Divisor of(int n) { return Divisor{n == 1 ? 0 : ~0ull / (uint64_t)n + 1}; }
+    __device__ __forceinline__ int operator()(int v) const { return inverse ? (int)__umul64hi((uint64_t)v, inverse) : v; }
+};
+// v / n for 0 < n <= kBand and v below 2^26
+__device__ __forceinline__ int divide_small(int v, int n) {
+    static_assert(kBand == 8, "an inverse for each");
+    constexpr uint32_t kInverse[9] = {0, 0, 0x80000000u, 0x55555556u, 0x40000000u, 0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
+    uint32_t inverse = 0;
+#pragma unroll
+    for (int i = 2; i <= 8; ++i) inverse = n == i ? kInverse[i] : inverse;
+    return n == 1 ? v : (int)__umulhi((uint32_t)v, inverse);
+}
+
 struct Fp8Params {
     CUtensorMap a_map;    // rows in place: boxes of 128 rows
     CUtensorMap a_part;   // rows in place: boxes of 32 rows
     CUtensorMap w_map;
     GroupedFp8Args a;
     int c_tiles, nkb;
+    Divisor by_c, by_band;  // c_tiles, and kBand times it
     int as_vec;           // rows of A's scales are whole 16 bytes
     int w_blocks;         // scale blocks of an expert's rows of W
 };
@@ -157,7 +175,7 @@ __device__ __forceinline__ int cta_rows(const Fp8Tile& t, int rank) { return max
 template <bool PAIR>
 __device__ __forceinline__ Fp8Tile tile_at(const Fp8Params& p, const int* off, const int* base, int i) {
     Fp8Tile t;
-    const int u = i / p.c_tiles;
+    const int u = p.by_c(i);
     int lo = 0, hi = p.a.E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -167,11 +185,11 @@ __device__ __forceinline__ Fp8Tile tile_at(const Fp8Params& p, const int* off, c
     t.e = lo;
     const int local = i - base[lo] * p.c_tiles, rt = base[lo + 1] - base[lo];
     // bands of kBand row tiles, all column tiles of a band together: each operand is read from DRAM about once
-    const int band = local / (kBand * p.c_tiles);
+    const int band = p.by_band(local);
     const int nr = min(kBand, rt - band * kBand);
     const int j = local - band * kBand * p.c_tiles;
-    t.c = j / nr;
-    t.r = band * kBand + j % nr;
+    t.c = divide_small(j, nr);
+    t.r = band * kBand + j - t.c * nr;
     t.seg0 = off[lo];
     t.rows = min(Cfg<PAIR>::kRowTile, off[lo + 1] - off[lo] - Cfg<PAIR>::kRowTile * t.r);
     return t;
@@ -825,6 +843,8 @@ cudaError_t launch_grouped_fp8(const GroupedFp8Args& a, int device, int sm_count
     p.nkb = scale_blocks(a.d);
     p.as_vec = p.nkb % 4 == 0 && reinterpret_cast<uintptr_t>(a.A_scales) % 16 == 0;
     p.c_tiles = a.glu ? scale_blocks(n) : (a.N + 255) / 256;
+    p.by_c = Divisor::of(p.c_tiles);
+    p.by_band = Divisor::of(kBand * p.c_tiles);
     // Pairs of CTAs load half of W each, but waste more rows of an expert's last tile, and gathered rows reach the leader's
     // MMAs through one more thread.  us with one CTA a tile and in pairs: rows in place, 32 experts of 4096 x 4096, 256
     // rows each 161 and 178, 512 265 and 264, 768 417 and 379, 2048 983 and 941; gathered, 2048 x 2816 SwiGLU, 1024 rows
