@@ -13,7 +13,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 5;  // (64 experts of 2048 x 2816: 184 us with four, 177 with five, 181 with six)
 
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_weights_kernel(const QuantizeWeightsArgs a) {
     __shared__ uint32_t words[128 * 32];  // [column of W][words of 4 rows]; word w of column n is at w ^ 2 (n / 8)
