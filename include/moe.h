@@ -658,8 +658,9 @@ MOE_API moe_status_t moe_quantize_weights(moe_plan_t plan, const uint16_t* W, in
  *   offsets  in:  int32 [E+1] from moe_route.
  *   W, W_scales in: from moe_quantize_weights with halves 1.
  *   Y        out: [S][N] in the plan's out_dtype.
- * Workspace and status as for moe_grouped_gemm.  Offsets that are not an ascending list from 0 to S write
- * MOE_ERR_DEVICE to dev_status and nothing to Y.  Launches one kernel.
+ * Workspace and status as for moe_grouped_gemm (this product keeps nothing in the workspace: calls of one plan may
+ * overlap).  Offsets that are not an ascending list from 0 to S write MOE_ERR_DEVICE to dev_status and nothing to Y.
+ * Launches one kernel.
  */
 MOE_API moe_status_t moe_grouped_gemm_fp8(moe_plan_t plan, const uint8_t* A, const float* A_scales, const int32_t* perm,
                                           const int32_t* offsets, const uint8_t* W, const float* W_scales, void* Y,
@@ -702,7 +703,7 @@ MOE_API moe_status_t moe_grouped_gemm_fp8_swiglu(moe_plan_t plan, const uint8_t*
  *   loss     out: fp32 [2].
  *   load     out: int32 [G][E], the counted picks.
  *   tokens   out: int32 [G + 1], n[g] and at last N.
- * Launches one to three kernels.  The same bits on every run.
+ * Launches one or two kernels.  The same bits on every run.
  */
 MOE_API moe_status_t moe_balance_scratch(moe_plan_t plan, int32_t seq_len, size_t* bytes);
 MOE_API moe_status_t moe_balance_loss(moe_plan_t plan, const float* logits, const int32_t* topk_idx, const uint8_t* mask,

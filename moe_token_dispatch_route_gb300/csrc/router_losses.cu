@@ -10,7 +10,7 @@
 //
 // A token is held by 8 to 32 lanes, VPL experts each; its sums are shuffles.  A CTA stays within one group, so
 // the forward pass keeps its experts' score sums in registers over all its tokens and the backward pass its w_e.  The
-// CTAs' sums are joined in their order by a second kernel (a third joins the groups).
+// CTAs' sums are joined in a fixed order by a second kernel, whose last CTA adds the groups'.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,12 +38,20 @@ Split split_of(int T, int E, int seq_len, int groups, int sm_count) {
     return s;
 }
 
-// Scratch: balance and z sums of the groups, then (chunks > 1) each CTA's score sums, load, z sum and tokens.
+// Experts of a joining CTA, and how many CTAs a group's experts are shared out to (one where a group has one CTA's sums).
+constexpr int kJoinExperts = 32;
+__host__ __device__ inline int expert_parts(int E, const Split& s) { return s.chunks > 1 ? (E + kJoinExperts - 1) / kJoinExperts : 1; }
+
+// Scratch: a count of the CTAs that have joined; sum_e load[e] sum_t p[t][e] of each group and part of its experts; the groups' z
+// sums; then (chunks > 1) each CTA's score sums, load, z sum and tokens.
 struct Partials {
-    float* group;  // [groups][2]
-    float* part;   // [blocks][2 E + 2]
-    __host__ __device__ Partials(const RouterLossArgs& a)
-        : group(static_cast<float*>(a.scratch)), part(static_cast<float*>(a.scratch) + 2 * (size_t)a.groups) {}
+    unsigned* joined;  // the first kernel sets it to 0
+    float* dot;        // [groups][expert_parts]
+    float* z;          // [groups]
+    float* part;       // [blocks][2 E + 2]
+    __host__ __device__ Partials(const RouterLossArgs& a, const Split& s)
+        : joined(static_cast<unsigned*>(a.scratch)), dot(static_cast<float*>(a.scratch) + 4),
+          z(dot + (size_t)a.groups * expert_parts(a.E, s)), part(z + a.groups) {}
 };
 
 template <int GL>
@@ -168,31 +176,20 @@ struct Scores {
     __device__ __forceinline__ float score(int i) const { return SIG ? g[SIG ? i : 0].s : x[i]; }
 };
 
-// The loss of group g's balance, from its sums; called by one CTA.  `sums` are in shared memory.
-__device__ __forceinline__ void group_done(const RouterLossArgs& a, long long g, float dot, float z, int n) {
-    const float bal = n > 0 ? dot * ((float)a.E / ((float)a.k * (float)n * (float)n)) : 0.f;
-    a.tokens[g] = n;
-    const Partials pt(a);
-    if (a.groups == 1) {
-        a.tokens[1] = n;
-        a.loss[0] = a.balance * bal;
-        a.loss[1] = n > 0 ? a.z * (z / (float)n) : 0.f;
-    } else {
-        pt.group[2 * g] = bal;
-        pt.group[2 * g + 1] = z;
-    }
+// A group's E / (k n^2) sum_e load[e] sum_t p[t][e].
+__device__ __forceinline__ float group_balance(const RouterLossArgs& a, float dot, int n) {
+    return n > 0 ? dot * ((float)a.E / ((float)a.k * (float)n * (float)n)) : 0.f;
 }
 
 // Sum over a CTA, in every thread.
-__device__ __forceinline__ float cta_sum(float v, float (&red)[kRouterWarps]) {
+template <int WARPS>
+__device__ __forceinline__ float cta_sum(float v, float (&red)[WARPS]) {
     v = lanes_sum<32>(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRouterWarps; ++i) v += red[i];
-    return v;
+    v = (threadIdx.x & 31) < WARPS ? red[threadIdx.x & 31] : 0.f;
+    return lanes_sum<32>(v);
 }
 
 template <int GL, int VPL, int VEC, bool SIG>
@@ -208,6 +205,8 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
     const int chunk = blockIdx.x % sp.chunks;
     const long long t0 = g * a.seq_len + (long long)chunk * sp.chunk;
     const long long t1 = min(min(t0 + sp.chunk, (g + 1) * (long long)a.seq_len), (long long)a.T);
+    const Partials pt(a, sp);
+    if (blockIdx.x == 0 && tid == 0) *pt.joined = 0u;
     for (int e = tid; e < kCols; e += kRouterThreads) hist[e] = 0;
     __syncthreads();
     float acc[VPL], z = 0.f;
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
     z = cta_sum(z, red);
     const int tokens = (int)cta_sum((float)n, red);  // (below 2^24: a chunk)
     float dot = 0.f;
-    float* part = Partials(a).part + (size_t)blockIdx.x * (2 * a.E + 2);
+    float* part = pt.part + (size_t)blockIdx.x * (2 * a.E + 2);
     for (int e = tid; e < a.E; e += kRouterThreads) {
         float v = 0.f;
 #pragma unroll
@@ -268,67 +267,118 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
         return;
     }
     dot = cta_sum(dot, red);
-    if (tid == 0) group_done(a, g, dot, z, tokens);
+    if (tid == 0) {
+        pt.dot[g] = dot;
+        pt.z[g] = z;
+        a.tokens[g] = tokens;
+        if (a.groups == 1) {
+            a.tokens[1] = tokens;
+            a.loss[0] = a.balance * group_balance(a, dot, tokens);
+            a.loss[1] = tokens > 0 ? a.z * (z / (float)tokens) : 0.f;
+        }
+    }
 }
 
-// One CTA a group: adds its CTAs' sums in their order.
-__global__ void __launch_bounds__(kRouterThreads) balance_groups_kernel(const RouterLossArgs a, Split sp) {
-    __shared__ float red[kRouterWarps];
+// The groups' losses, added in their order by one CTA.
+template <int WARPS>
+__device__ __forceinline__ void total_of_groups(const RouterLossArgs& a, const Split& sp, float (&red)[WARPS], int* count) {
+    const Partials pt(a, sp);
+    const int parts = expert_parts(a.E, sp);
+    float bal = 0.f, z = 0.f;
+    int n = 0;
+#pragma unroll 4
+    for (int g = threadIdx.x; g < a.groups; g += 32 * WARPS) {
+        float dot = 0.f;
+        for (int i = 0; i < parts; ++i) dot += __ldcg(pt.dot + (size_t)g * parts + i);
+        const int tokens = __ldcg(a.tokens + g);
+        bal += group_balance(a, dot, tokens);
+        z += __ldcg(pt.z + g);
+        n += tokens;
+    }
+    if (threadIdx.x == 0) *count = 0;
+    bal = cta_sum(bal, red);
+    z = cta_sum(z, red);
+    if (n) atomicAdd(count, n);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.tokens[a.groups] = *count;
+        a.loss[0] = a.balance * (bal / (float)a.groups);
+        a.loss[1] = *count > 0 ? a.z * (z / (float)*count) : 0.f;
+    }
+}
+
+// Adds the CTAs' sums of a group: a CTA takes 32 experts, a warp every 32nd CTA's, joined in their order.  (One CTA a group
+// took 190 us for 16384 tokens of 1000 experts in one group.)  The last one to end adds the groups'.
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) balance_groups_kernel(const RouterLossArgs a, Split sp) {
+    __shared__ float sums[32][kJoinExperts + 1];
+    __shared__ int loads[32][kJoinExperts + 1];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ int count;
+    __shared__ bool last;
     wait_for_kernel_before();
-    const long long g = blockIdx.x;
+    const int parts = expert_parts(a.E, sp), g = (int)(blockIdx.x / parts), piece = (int)(blockIdx.x % parts);
     const size_t pitch = 2 * a.E + 2;
-    const float* part = Partials(a).part + (size_t)g * sp.chunks * pitch;
-    float dot = 0.f;
-    for (int e = threadIdx.x; e < a.E; e += kRouterThreads) {
-        float v = 0.f;
-        int load = 0;
+    const Partials pt(a, sp);
+    const float* part = pt.part + (size_t)g * sp.chunks * pitch;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = piece * kJoinExperts + lane;
+    float v = 0.f;
+    int load = 0;
+    if (e < a.E) {
 #pragma unroll 8
-        for (int c = 0; c < sp.chunks; ++c) {
+        for (int c = warp; c < sp.chunks; c += 32) {
             v += __ldcg(part + c * pitch + e);
             load += __float_as_int(__ldcg(part + c * pitch + a.E + e));
         }
-        a.load[g * a.E + e] = load;
-        dot = fmaf(v, (float)load, dot);
     }
     float z = 0.f;
     int n = 0;
-    for (int c = threadIdx.x; c < sp.chunks; c += kRouterThreads) {
-        z += __ldcg(part + c * pitch + 2 * a.E);
-        n += __float_as_int(__ldcg(part + c * pitch + 2 * a.E + 1));
-    }
-    dot = cta_sum(dot, red);
-    z = cta_sum(z, red);
-    __shared__ int count;
+    if (piece == 0)
+        for (int c = threadIdx.x; c < sp.chunks; c += kJoinThreads) {
+            z += __ldcg(part + c * pitch + 2 * a.E);
+            n += __float_as_int(__ldcg(part + c * pitch + 2 * a.E + 1));
+        }
+    sums[warp][lane] = v;
+    loads[warp][lane] = load;
     if (threadIdx.x == 0) count = 0;
     __syncthreads();
-    if (n) atomicAdd(&count, n);
-    __syncthreads();
-    if (threadIdx.x == 0) group_done(a, g, dot, z, count);
-}
-
-// One CTA: the groups' losses in their order.
-__global__ void __launch_bounds__(kRouterThreads) balance_total_kernel(const RouterLossArgs a) {
-    __shared__ float red[kRouterWarps];
-    __shared__ int count;
-    wait_for_kernel_before();
-    const float* group = Partials(a).group;
-    float bal = 0.f, z = 0.f;
-    int n = 0;
-    for (int g = threadIdx.x; g < a.groups; g += kRouterThreads) {
-        bal += __ldcg(group + 2 * (size_t)g);
-        z += __ldcg(group + 2 * (size_t)g + 1);
-        n += __ldcg(a.tokens + g);
+    if (warp == 0) {
+        v = 0.f;
+        load = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v += sums[i][lane];
+            load += loads[i][lane];
+        }
+        if (e < a.E) a.load[(size_t)g * a.E + e] = load;
+        const float dot = lanes_sum<32>(e < a.E ? v * (float)load : 0.f);
+        if (lane == 0) pt.dot[(size_t)g * parts + piece] = dot;
     }
-    if (threadIdx.x == 0) count = 0;
-    bal = cta_sum(bal, red);
-    z = cta_sum(z, red);
-    if (n) atomicAdd(&count, n);
+    if (piece == 0) {
+        z = cta_sum(z, red);
+        if (n) atomicAdd(&count, n);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            pt.z[g] = z;
+            a.tokens[g] = count;
+        }
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-        a.tokens[a.groups] = count;
-        a.loss[0] = a.balance * (bal / (float)a.groups);
-        a.loss[1] = count > 0 ? a.z * (z / (float)count) : 0.f;
+        __threadfence();
+        last = atomicAdd(pt.joined, 1u) == gridDim.x - 1u;
+        __threadfence();
     }
+    __syncthreads();
+    if (last) total_of_groups(a, sp, red, &count);
+}
+
+// Groups that a CTA of the first kernel each has done: their total.
+__global__ void __launch_bounds__(kJoinThreads) balance_total_kernel(const RouterLossArgs a, Split sp) {
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ int count;
+    wait_for_kernel_before();
+    total_of_groups(a, sp, red, &count);
 }
 
 template <int GL, int VPL, int VEC, bool SIG>
@@ -465,7 +515,7 @@ cudaError_t by_experts(const RouterLossArgs& a, bool vec, Go go) {
 size_t balance_scratch_bytes(int T, int E, int seq_len, int sm_count) {
     const int groups = (int)(((long long)T + seq_len - 1) / seq_len);
     const Split s = split_of(T, E, seq_len, groups, sm_count);
-    return sizeof(float) * (2 * (size_t)groups + (s.chunks > 1 ? (size_t)s.blocks * (2 * (size_t)E + 2) : 0));
+    return sizeof(float) * (4 + (size_t)groups * (expert_parts(E, s) + 1) + (s.chunks > 1 ? (size_t)s.blocks * (2 * (size_t)E + 2) : 0));
 }
 
 cudaError_t launch_balance_loss(const RouterLossArgs& a, int sm_count, cudaStream_t stream) {
@@ -476,8 +526,9 @@ cudaError_t launch_balance_loss(const RouterLossArgs& a, int sm_count, cudaStrea
         return launch_after(balance_kernel<decltype(gl)::value, decltype(vpl)::value, decltype(v)::value, decltype(sig)::value>,
                             (unsigned)sp.blocks, kRouterThreads, 0, stream, a, sp);
     });
-    if (e == cudaSuccess && sp.chunks > 1) e = launch_after(balance_groups_kernel, (unsigned)a.groups, kRouterThreads, 0, stream, a, sp);
-    if (e == cudaSuccess && a.groups > 1) e = launch_after(balance_total_kernel, 1u, kRouterThreads, 0, stream, a);
+    if (e == cudaSuccess && sp.chunks > 1)
+        e = launch_after(balance_groups_kernel, (unsigned)(a.groups * expert_parts(a.E, sp)), kJoinThreads, 0, stream, a, sp);
+    if (e == cudaSuccess && sp.chunks == 1 && a.groups > 1) e = launch_after(balance_total_kernel, 1u, kJoinThreads, 0, stream, a, sp);
     return e;
 }
 
