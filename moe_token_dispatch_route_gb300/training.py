@@ -29,6 +29,9 @@ class MoeTrainLayer:
     The buffers belong to the stream that is current when the layer is made: keep the layer until its
     passes on other streams are done."""
 
+    norm, balance, z, seq_len = "layer", 0.0, 0.0, 0
+    loss = mask = load = None
+
     def __init__(self, T: int, d: int, F: int, E: int, k: int, eps: float = 1e-5, device: int = 0, norm: str = "layer",
                  balance: float = 0.0, z: float = 0.0, seq_len: int = 0):
         if norm not in ("layer", "rms"):
@@ -55,7 +58,6 @@ class MoeTrainLayer:
         self.H, self.dH, self.dY, self.dA = new(S, F), new(S, F), new(S, d), new(S, d)
         self.dw, self.dy = new(T, k, dtype=_F32), new(T, d, dtype=_F32)
         self.ones = torch.ones(T, k, dtype=_F32, device=dev)
-        self.loss = self.mask = self.load = None
         if balance or z:
             groups = b.loss_groups(self.up, seq_len)
             self.load, self.tokens = new(groups, E, dtype=torch.int32), new(groups + 1, dtype=torch.int32)
@@ -75,7 +77,7 @@ class MoeTrainLayer:
         with torch.no_grad(), self._on(stream):
             return self._forward(x, gamma, beta, W_r, W1, W2, mask)
 
-    def _forward(self, x, gamma, beta, W_r, W1, W2, mask):
+    def _forward(self, x, gamma, beta, W_r, W1, W2, mask=None):
         u, r = self.up, self.bufs
         if self.norm == "rms" and beta is not None:
             raise ValueError("MoeTrainLayer.forward: the RMS norm has no beta")
