@@ -1,6 +1,6 @@
 // The experts' weights in 8 bits: W bf16 [E][d][N] -> e4m3 codes [E][N][d] and a scale for each block of 128 x 128, the
 // layout of the block-scaled per-expert product (the reduction d is the contiguous axis of both its operands).
-// Bound by HBM: 2 bytes in and 1 out a weight.
+// Bound by HBM: 2 bytes in and 1 out a weight (64 experts of 2048 x 2816: 175 us, 0.93 of a plain copy's rate).
 //
 // A CTA takes a block at a time.  A thread holds 4 consecutive rows of d by 8 columns, twice; it packs the codes of four
 // rows into a word a column, and the words cross shared memory to leave as rows of 128 bytes.
@@ -13,7 +13,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 5;  // (64 experts of 2048 x 2816: 184 us with four, 177 with five, 181 with six)
+constexpr int kCtasPerSm = 5;  // (64 experts of 2048 x 2816: 184 us with four, 177 with five)
 
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_weights_kernel(const QuantizeWeightsArgs a) {
     __shared__ uint32_t words[128 * 32];  // [column of W][words of 4 rows]; word w of column n is at w ^ 2 (n / 8)
