@@ -690,7 +690,9 @@ MOE_API moe_status_t moe_grouped_gemm_fp8_swiglu(moe_plan_t plan, const uint8_t*
  *   loss[0] = balance / G * sum over g of  E / (k n[g]^2) * sum_e load[g][e] * sum over g's tokens of p[t][e]
  *             (a group whose load and scores are uniform adds balance / G; one without counted tokens adds 0),
  *   loss[1] = z / N * sum over the counted tokens of lse[t]^2,  lse = log sum_e exp(logit).
- * Logits of masked experts may be -infinity or the type's lowest value, but not all of a row's.
+ * Logits of masked experts may be -infinity or the type's lowest value, but not all of a counted token's.  Logits of masked
+ * tokens may be anything: they reach neither the losses nor their gradient (the gates' gradient is that of the gates as they
+ * are, NaN where those are).
  *
  * moe_balance_scratch -- bytes of device scratch that moe_balance_loss needs (256-byte aligned; nothing is kept in it
  * from call to call; calls that share one must be ordered on one stream).  Host only.

@@ -123,13 +123,14 @@ struct Lanes {
     }
 };
 
-// What is read of a token; in the forward pass while the one before it is worked on.
+// What is read of a token; in the forward pass while the one before it is worked on.  A masked token may hold anything, and 0
+// times a NaN is one: its logits are read only where `masked_too` (gates that are entries of the softmax over them all).
 template <int GL, int VPL, int VEC>
 struct Token {
     float l[VPL], dw;
     int pick;  // lane j's: pick j, or -1
     bool there, counted;
-    __device__ __forceinline__ void fetch(const RouterLossArgs& a, long long t, long long t1, int sub, bool gates) {
+    __device__ __forceinline__ void fetch(const RouterLossArgs& a, long long t, long long t1, int sub, bool gates, bool masked_too) {
         there = t < t1;
         counted = there && (!a.mask || __ldg(a.mask + t));
         pick = -1;
@@ -138,7 +139,8 @@ struct Token {
             pick = __ldg(a.topk_idx + (size_t)t * a.k + sub);
             if (gates) dw = __ldg(a.dtopk_w + (size_t)t * a.k + sub);
         }
-        Lanes<GL, VPL, VEC>::load(a.logits + (there ? (size_t)t * a.E : 0), sub, a.E, there, l);
+        const bool read = counted || (there && masked_too);
+        Lanes<GL, VPL, VEC>::load(a.logits + (read ? (size_t)t * a.E : 0), sub, a.E, read, l);
     }
 };
 
@@ -218,10 +220,10 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const RouterLos
     constexpr int kPass = kRouterWarps * (32 / GL);
     const bool want = a.z != 0.f;
     Token<GL, VPL, VEC> next;
-    next.fetch(a, t0 + warp * (32 / GL) + lane / GL, t1, sub, false);
+    next.fetch(a, t0 + warp * (32 / GL) + lane / GL, t1, sub, false, false);
     for (long long tw = t0 + warp * (32 / GL); tw < t1; tw += kPass) {
         const Token<GL, VPL, VEC> now = next;
-        if (tw + kPass < t1) next.fetch(a, tw + kPass + lane / GL, t1, sub, false);
+        if (tw + kPass < t1) next.fetch(a, tw + kPass + lane / GL, t1, sub, false, false);
         const bool live = now.counted;
         if (!__any_sync(kFull, live)) continue;
         if (live && (unsigned)now.pick < (unsigned)a.E) atomicAdd(&hist[now.pick], 1);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
     __syncwarp();
     for (long long tw = t0 + warp * kPer; tw < t1; tw += kRouterWarps * kPer) {
         Token<GL, VPL, VEC> now;
-        now.fetch(a, tw + lane / GL, t1, sub, a.dtopk_w != nullptr);
+        now.fetch(a, tw + lane / GL, t1, sub, a.dtopk_w != nullptr, a.dtopk_w && !SIG && !a.renorm);
         const long long t = tw + lane / GL;
         const bool there = now.there, counted = now.counted;
         float d[VPL];
