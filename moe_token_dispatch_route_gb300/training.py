@@ -93,6 +93,7 @@ class MoeTrainLayer:
         b.route(u, self.logits, r)
         if self.load is not None:
             self.loss, self.mask = torch.empty(2, dtype=_F32, device=self.device), mask
+            self._hold_mask()
             b.moe_balance_loss(u, self.logits, r.topk_idx, mask, self.seq_len, self.balance, self.z, self.loss, self.load,
                                self.tokens, self.loss_scratch)
         b.dispatch_gemm(u, self.y, W1, r)                                          # GU in r.Y
@@ -100,6 +101,12 @@ class MoeTrainLayer:
         b.moe_grouped_gemm(self.down, self.H, r.offsets, W2, self.Y, self.down_ws, r.status)
         b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out)
         return torch.add(self.out, x)
+
+    def _hold_mask(self):
+        """The mask may be the caller's temporary, made on another stream: its memory is not handed out again before this
+        stream's calls have read it."""
+        if self.mask is not None and self.mask.is_cuda:
+            self.mask.record_stream(torch.cuda.current_stream(self.device))
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
         """The gradients of the latest forward pass (which may be taken more than once).  x and the weights are that pass's,
@@ -120,6 +127,7 @@ class MoeTrainLayer:
         b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy)                     # the dispatch's gradient
         if self.load is not None:  # the gates and the router's losses
             dlogits = self.dlogits
+            self._hold_mask()
             b.moe_router_backward(u, self.logits, r.topk_idx, self.dw, self.mask, self.seq_len, self.balance, self.z, self.load,
                                   self.tokens, dlogits)
         else:  # the gates: softmax over the chosen logits
