@@ -99,8 +99,8 @@ moe_status_t moe_rmsnorm(moe_plan_t plan, const void* x, int32_t x_dtype, const 
     PlanView v;
     if (!plan_view(plan, &v) || !dtype_ok(x_dtype) || !dtype_ok(h_dtype) || !(eps > 0.f) || std::isinf(eps))
         return MOE_ERR_INVALID_ARG;
+    if (v.T == 0) return MOE_OK;  // (arrays of no rows may have no address)
     if (!res && h_dtype != x_dtype) return MOE_ERR_INVALID_ARG;  // without a residual h is x
-    if (v.T == 0) return MOE_OK;
     if (!need(x, 16) || !may(res, 16) || !may(h, 16) || (res && !h) || !may(gamma, 16) || !may(y, 16) || !may(codes, 16) ||
         !may(scales, 4) || !may(rstd, 4) || (codes != nullptr) != (scales != nullptr) || (!y && !codes))
         return MOE_ERR_INVALID_ARG;

@@ -1,4 +1,4 @@
-"""What a layer keeps of its caller's, and passes whose first call is captured."""
+"""What a layer keeps of its caller's, layers of no tokens, and passes whose first call is captured."""
 import os
 import subprocess
 import sys
@@ -37,6 +37,17 @@ def test_a_mask_that_the_caller_drops_stays_until_the_pass_has_read_it():
     taken = [torch.empty(T, dtype=torch.uint8, device=DEV) for _ in range(8)]
     assert at not in [t.data_ptr() for t in taken]
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("h_dtype", [torch.float32, BF16])
+def test_a_serving_layer_of_no_tokens(h_dtype):
+    gamma, W_r, W1, W2 = weights(64, 32, 8)
+    layer = MoeServeLayer(0, gamma, W_r, W1, W2, 2)
+    h = torch.empty(0, 64, dtype=h_dtype, device=DEV)
+    assert layer.forward(None, h).shape == (0, 64)
+    assert layer.forward(torch.empty(0, 64, device=DEV), h).shape == (0, 64)
+    torch.cuda.synchronize()
+    assert layer.status.tolist() == [0, 0, 0, 0]
 
 
 CAPTURE = """
