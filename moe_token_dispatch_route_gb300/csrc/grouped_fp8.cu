@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap* ma
 }
 
 // 32 TMEM lanes x 16 consecutive columns, loaded and there.  (A wait in a statement of its own would take the registers as
-// operands, and they would be copied: 64 more instructions a k-block.)
+// operands, and they would be copied.)
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -234,10 +234,10 @@ __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const
         const uint32_t bytes = PAIR ? a_bytes(p, cta_rows(t, 0)) + a_bytes(p, cta_rows(t, 1)) + 2u * C::kWBytes
                                     : a_bytes(p, mine) + (uint32_t)C::kWBytes;
         for (int kb = 0; kb < p.nkb; ++kb) {
-            
+
             ok = bar_wait(empty0 + 8 * s, phase ^ 1u, w, 70);
             if (!(ok = __all_sync(kFull, ok))) break;
-            
+
             if (elected()) {
                 const uint32_t dst = smem_addr(stages) + s * C::kStageBytes, bar = full_lead + 8 * s;
                 const int x = kb * kBlk;
@@ -255,7 +255,7 @@ __device__ void producer(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, const
                 }
             }
             __syncwarp();
-            
+
             ++uses;
             if (++s == C::kStages) {
                 s = 0;
@@ -321,7 +321,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 // Warp 2: the scales of four k-blocks at a time, four rows a lane, and those of the two blocks of W.  (Loaded by the
-// epilogue's threads, even four k-blocks ahead, the scales took as long as all else.)
+// epilogue's threads, even four k-blocks ahead, they held its loop up.)
 template <bool PAIR>
 __device__ void scales_role(const Fp8Params& p, Fp8Ctl* ctl, const int* off, const int* base, int total, int first, int step,
                             const Wait& w, int rank) {
@@ -385,7 +385,7 @@ __device__ void relay_role(const Fp8Params& p, Fp8Ctl* ctl, int total, int first
 }
 
 // Leader's warp 1.  All lanes run the loop and one issues: descriptors and addresses are then known to be the warp's, not a
-// lane's.  (Run by one lane alone, an MMA took 75 cycles to issue and the k-block 800.)
+// lane's.  (Run by one lane alone, an MMA took some 75 cycles to issue.)
 template <bool PAIR>
 __device__ void mma_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* stages, int total, int first, int step, uint32_t tmem,
                          const Wait& w) {
@@ -486,7 +486,7 @@ __device__ __forceinline__ void silu4(const float* g, float* u) {
     for (int i = 0; i < 4; ++i) u[i] *= fmaf(-fabsf(g[i]), q[i], g[i] < 0.f ? 0.f : g[i]);
 }
 
-// Warps 4-11: TMEM lane quarter q = warp & 3 (rows) and half h of the columns of both blocks.
+// Warps 8-15: TMEM lane quarter q = warp & 3 (rows) and half h of the columns of both blocks.
 template <bool PAIR>
 __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging, const int* off, const int* base, int total,
                               int first, int step, uint32_t tmem, const Wait& w, bool leader, uint32_t lead, int rank) {
@@ -553,7 +553,8 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
                 sc[3][1] = a4.w * w1.w;
                 return true;
             };
-            auto read = [&]() {  // the scales are in registers: this warp's multiplications have used them
+            auto read = [&]() {  // the scales are in registers
+                __syncwarp();    // all lanes' reads, before one lane's arrival hands the slot back
                 warp_arrive<false>(smem_addr(&ctl->sempty[slot]));
                 if (++slot == kScaleRing) {
                     slot = 0;
