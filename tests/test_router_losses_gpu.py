@@ -277,3 +277,25 @@ def test_logits_at_any_four_bytes(E):
     grad = reference(logits, idx, dw, mask, 25, 1.0, 0.5, "renorm")[4]
     for _, load, tokens, dl in results:
         check_gradient(dl, grad, logits, idx, dw, load, tokens.tolist(), 25, 1.0, 0.5, "renorm")
+
+
+@pytest.mark.parametrize("gates", ["sigmoid", "sigmoid_renorm"])
+@pytest.mark.parametrize("E,k", [(5, 2), (8, 2), (16, 3), (30, 3), (64, 4), (256, 8), (300, 6), (1000, 6)])
+@pytest.mark.parametrize("balance,z", [(0.0, 0.3), (0.7, 0.0), (0.7, 0.3)])
+def test_tokens_whose_logits_are_all_far_below_zero(gates, E, k, balance, z):
+    """Logistic scores that fp32 flushes to 0 (below about -87) have a sum and a share of it all the same: they are the softmax's,
+    1 + e^l being 1.  Beside tokens of ordinary logits in the same warp."""
+    T, seq = 61, 25
+    plan, logits, idx, dw, mask = setup(T, E, k, gates, True, seq, seed=61)
+    for first, shift in ((0, 100.0), (1, 60.0), (2, 500.0), (3, 20.0)):
+        logits[first::5] -= shift
+    dw = dw if gates == "sigmoid" else None  # (the gates of picks that are all that far below are not numbers)
+    loss, load, tokens = forward(plan, logits, idx, mask, seq, balance, z)
+    rb, rz, rload, rtokens, grad = reference(logits, idx, dw, mask, seq, balance, z, gates)
+    assert torch.equal(load, rload) and tokens.tolist() == rtokens
+    rel = (32 + E / 32 + T / 64 + 64 + 64) * 2 * U
+    assert abs(float(loss[0]) - float(rb)) <= rel * float(rb)
+    assert abs(float(loss[1]) - float(rz)) <= 2 * rel * float(rz)  # lse, to rel of itself, is squared
+    dl = torch.full_like(logits, float("nan"))
+    binding.moe_router_backward(plan, logits, None if dw is None else idx, dw, mask, seq, balance, z, load, tokens, dl)
+    check_gradient(dl, grad, logits, idx, dw, load, rtokens, seq, balance, z, gates)
