@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kRouterThreads, VEC == 4 && VPL == 16 ? 4 : 0)
         a.tokens[g] = tokens;
         if (a.groups == 1) {
             a.tokens[1] = tokens;
-            a.loss[0] = a.balance * group_balance(a, dot, tokens);
+            a.loss[0] = a.balance != 0.f ? a.balance * group_balance(a, dot, tokens) : 0.f;  // (0 times what may be no number)
             a.loss[1] = tokens > 0 ? a.z * (z / (float)tokens) : 0.f;
         }
     }
@@ -327,7 +327,7 @@ __device__ __forceinline__ void total_of_groups(const RouterLossArgs& a, const S
     __syncthreads();
     if (threadIdx.x == 0) {
         a.tokens[a.groups] = *count;
-        a.loss[0] = a.balance * (bal / (float)a.groups);
+        a.loss[0] = a.balance != 0.f ? a.balance * (bal / (float)a.groups) : 0.f;
         a.loss[1] = *count > 0 ? a.z * (z / (float)*count) : 0.f;
     }
 }

@@ -299,3 +299,15 @@ def test_tokens_whose_logits_are_all_far_below_zero(gates, E, k, balance, z):
     dl = torch.full_like(logits, float("nan"))
     binding.moe_router_backward(plan, logits, None if dw is None else idx, dw, mask, seq, balance, z, load, tokens, dl)
     check_gradient(dl, grad, logits, idx, dw, load, rtokens, seq, balance, z, gates)
+
+
+@pytest.mark.parametrize("T,seq", [(20, 0), (20, 5), (5000, 0), (5000, 2000)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_balance_loss_without_a_coefficient_is_zero(T, seq, bad):
+    """Whatever the logits are: counted ones that are not numbers, too."""
+    plan, logits, idx, dw, _ = setup(T, 16, 2, "softmax", False, seq, seed=71)
+    logits[3, 4] = bad
+    loss, load, tokens = forward(plan, logits, idx, None, seq, 0.0, 0.0)
+    assert loss.tolist() == [0.0, 0.0] and int(load.sum()) == 2 * T and int(tokens[-1]) == T
+    loss, _, _ = forward(plan, logits, idx, None, seq, 0.0, 1.0)
+    assert float(loss[0]) == 0.0 and not torch.isfinite(loss[1])
