@@ -422,12 +422,18 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
     {
         const int n = a.balance != 0.f ? __ldg(a.tokens + g) : 0;
         const float coef = n > 0 ? a.balance * ((float)a.E / ((float)a.groups * (float)a.k * (float)n * (float)n)) : 0.f;
+        float picks = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = L::expert(sub, i);
-            w[i] = coef != 0.f && e < a.E ? coef * (float)__ldg(a.load + g * a.E + e) : 0.f;
+            w[i] = coef != 0.f && e < a.E ? (float)__ldg(a.load + g * a.E + e) : 0.f;
+            picks += w[i];
             mine[e] = 0.f;
         }
+        // Less their mean: p_e (w_e - sum_j p_j w_j) is the same for it, and an even load's common part does not cancel in fp32.
+        const float mean = lanes_sum<GL>(picks) / (float)a.E;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) w[i] = L::expert(sub, i) < a.E ? coef * (w[i] - mean) : 0.f;
     }
     const int all = a.z != 0.f ? __ldg(a.tokens + a.groups) : 0;
     const float zc = all > 0 ? 2.f * a.z / (float)all : 0.f;

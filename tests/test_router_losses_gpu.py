@@ -311,3 +311,34 @@ def test_a_balance_loss_without_a_coefficient_is_zero(T, seq, bad):
     assert loss.tolist() == [0.0, 0.0] and int(load.sum()) == 2 * T and int(tokens[-1]) == T
     loss, _, _ = forward(plan, logits, idx, None, seq, 0.0, 1.0)
     assert float(loss[0]) == 0.0 and not torch.isfinite(loss[1])
+
+
+@pytest.mark.parametrize("gates", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [6, 8, 16, 48, 64, 256, 1000])
+@pytest.mark.parametrize("step", [0, 1])
+def test_balance_gradient_of_an_even_and_a_nearly_even_load(gates, E, step):
+    """p (w - sum p w) is the same for w less any constant, and what the load's common part adds cancels: it is 0 for an even
+    load, and for a nearly even one known to the rounding of what differs (the scores' units and a row's sums)."""
+    T, k, balance = 50, 2, 0.7
+    plan, logits, idx, _, _ = setup(T, E, k, gates, False, 0, seed=81)
+    load = torch.full((1, E), 10000, dtype=I32, device=DEV)
+    load[0, ::2] += step
+    tokens = torch.full((2,), 10000 * E // k, dtype=I32, device=DEV)
+    dl = torch.full_like(logits, float("nan"))
+    binding.moe_router_backward(plan, logits, None, None, None, 0, balance, 0.0, load, tokens, dl)
+    if step == 0:
+        assert (dl == 0).all()
+        return
+    x = logits.double()
+    score = torch.sigmoid(x) if gates == "sigmoid" else torch.softmax(x, 1)
+    p = score / score.sum(1, keepdim=True)
+    n = float(tokens[0])
+    w = (balance * E / (k * n * n)) * (load[0].double() - load[0].double().mean())
+    grad = p * (w - (p * w).sum(1, keepdim=True)) * ((1 - score) if gates == "sigmoid" else 1)
+    mag = p * (w.abs() + (p * w.abs()).sum(1, keepdim=True))
+    # the mean is rounded once: a constant of 10000 u beside differences of a half, whose share is p times 1 - sum p, both
+    # known to the units below
+    bound = (32 + E / 32 + 64) * 2 * U * (1 + 10000 * U / 0.5) * mag + 2.0 ** -126
+    torch.cuda.synchronize()
+    off = (dl.double() - grad).abs()
+    assert (off <= bound).all(), (float((off / bound).max()), int((off > bound).sum()))
