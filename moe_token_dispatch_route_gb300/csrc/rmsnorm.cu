@@ -1,7 +1,7 @@
 // RMS norm of token rows with the residual's addition before it and an 8-bit output beside or in place of the bf16 one.
 //   h = x + res (rounded to the residual's type, stored),  rstd = 1 / sqrt(sum h^2 / d + eps),  y = h rstd gamma,
-// the sum in fp32 over the stored values.  The 8-bit output is y before it is rounded to bf16: e4m3 codes and a scale
-// for each 128 columns of a row.  Bound by HBM: x and the residual are read once and h stays in registers between the
+// the sum in fp32 over the stored values (where their squares pass its range, of scaled ones).  The 8-bit output is y before it
+// is rounded to bf16: e4m3 codes and a scale for each 128 columns of a row.  Bound by HBM: x and the residual are read once and h stays in registers between the
 // sum and the results (rows above 32768 columns are read back from L2).
 //
 // A row is held by TPR threads (a power of two from 16 to 1024), vectors of 8 columns, so 16 neighbouring threads hold a
@@ -19,6 +19,7 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kVpt = 4;       // vectors of a thread
 constexpr int kMaxRow = 1024 * 8 * kVpt;
 constexpr int kWide = 1024;
+constexpr float kLargest = 3.402823466e38f;
 __host__ __device__ constexpr int cta_threads(int tpr) { return tpr > 128 ? tpr : 128; }
 
 template <bool BF16>
@@ -81,6 +82,51 @@ __device__ __forceinline__ void results8(const RmsnormArgs& a, const float (&h)[
     }
 }
 
+// Rows that are finite but whose mean square and eps are not (values from some 1e18 up): a CTA that has met one (`met`, by thread) goes
+// over its rows again, sums the squares of 2^-96 h and writes the results of such rows once more.  h is what each thread
+// has stored, or x; its plain sum is the same bits as before.  (Done where it is met, the second sum cost the other rows 5 to 6%.)
+template <bool XB, bool HB, int TPR, int CTA>
+__device__ __forceinline__ void far_rows(const RmsnormArgs& a, bool met, float inv_d, float (&red)[2][CTA / 32]) {
+    if (!__syncthreads_or(met)) return;
+    constexpr int kRows = CTA / TPR;
+    constexpr float kDown = 0x1p-96f;
+    const int c0 = (int)(threadIdx.x % TPR) * 8;
+    for (long long t0 = (long long)blockIdx.x * kRows; t0 < a.T; t0 += (long long)gridDim.x * kRows) {
+        const long long t = t0 + threadIdx.x / TPR;
+        const bool row = t < a.T;
+        const size_t at = row ? (size_t)t * a.d : 0;
+        auto load = [&](int c, float(&h)[8]) {
+            if (a.h) load8<HB>(a.h, at + c, h);
+            else load8<XB>(a.x, at + c, h);
+        };
+        float s = 0.f, v = 0.f;
+#pragma unroll 1
+        for (int c = c0; row && c < a.d; c += TPR * 8) {
+            float h[8];
+            load(c, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s = fmaf(h[j], h[j], s);
+                v = fmaf(h[j] * kDown, h[j] * kDown, v);
+            }
+        }
+        s = row_sum<TPR, CTA>(s, red[0]);
+        v = row_sum<TPR, CTA>(v, red[1]);
+        const bool far = s * inv_d + a.eps > kLargest;
+        if (!__syncthreads_or(far)) continue;  // (and all have read the sums)
+        const float rstd = kDown / sqrtf(v * inv_d + a.eps * kDown * kDown);
+        if (row && far && c0 == 0 && a.rstd) a.rstd[t] = rstd;
+#pragma unroll 1
+        for (int base = 0; base < a.d; base += TPR * 8) {  // (whole warps: the blocks' amax is found by shuffles)
+            const int c = base + c0;
+            const bool mine = row && far && c < a.d;
+            float h[8] = {};
+            if (mine) load(c, h);
+            results8(a, h, rstd, row ? (size_t)t : 0, c, mine);
+        }
+    }
+}
+
 template <bool XB, bool HB, int TPR>
 __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rmsnorm_kernel(const RmsnormArgs a) {
     constexpr int kCta = cta_threads(TPR), kRows = kCta / TPR;
@@ -89,6 +135,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
     const int sub = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const float inv_d = 1.f / (float)a.d;
     int turn = 0;
+    bool met = false;
     for (long long t0 = (long long)blockIdx.x * kRows; t0 < a.T; t0 += (long long)gridDim.x * kRows, turn ^= 1) {
         const long long t = t0 + group;
         const bool row = t < a.T;
@@ -119,7 +166,8 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
         }
         s = row_sum<TPR, kCta>(s, red[turn]);
-        const float rstd = 1.f / sqrtf(s * inv_d + a.eps);
+        const float mean = s * inv_d + a.eps, rstd = 1.f / sqrtf(mean);
+        met |= mean > kLargest;
         if (row && sub == 0 && a.rstd) a.rstd[t] = rstd;
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
@@ -127,6 +175,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             results8(a, h[i], rstd, row ? (size_t)t : 0, c, row && c < a.d);
         }
     }
+    far_rows<XB, HB, TPR, kCta>(a, met, inv_d, red);
 }
 
 // d > 32768: h is read back
@@ -136,6 +185,7 @@ __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(const RmsnormArgs a
     wait_for_kernel_before();
     const float inv_d = 1.f / (float)a.d;
     int turn = 0;
+    bool met = false;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const size_t at = (size_t)t * a.d;
         float s = 0.f;
@@ -153,7 +203,8 @@ __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(const RmsnormArgs a
             for (int j = 0; j < 8; ++j) s = fmaf(h[j], h[j], s);
         }
         s = row_sum<kWide, kWide>(s, red[turn]);
-        const float rstd = 1.f / sqrtf(s * inv_d + a.eps);
+        const float mean = s * inv_d + a.eps, rstd = 1.f / sqrtf(mean);
+        met |= mean > kLargest;
         if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
         for (int c0 = 0; c0 < a.d; c0 += kWide * 8) {  // (whole warps: the blocks' amax is found by shuffles)
             const int c = c0 + threadIdx.x * 8;
@@ -165,6 +216,7 @@ __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(const RmsnormArgs a
             results8(a, h, rstd, (size_t)t, c, c < a.d);
         }
     }
+    far_rows<XB, HB, kWide, kWide>(a, met, inv_d, red);
 }
 
 template <bool XB, bool HB>

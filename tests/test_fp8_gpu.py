@@ -147,6 +147,51 @@ def test_rmsnorm_of_rows_that_are_zero_tiny_huge_or_not_numbers():
     assert (out["codes"][5].float() == 0).all()
 
 
+@pytest.mark.parametrize("d", [16, 48, 400, 1024, 2064, 4096, 7168, 16400, 32768, 40016])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rmsnorm_of_rows_whose_squares_pass_the_range(d, dtype):
+    """Finite rows up to the type's largest values, beside ordinary ones: their sum of squares is beyond fp32."""
+    scale = torch.tensor([1.0, 1e18, 1e19, 1e20, 1e30, 1e36, 6e37], device=DEV)[:, None]
+    x = (randn((7, d), 15).clamp(-5, 5) * scale).to(dtype)
+    x[6, 0] = torch.finfo(dtype).max
+    gamma = 1 + randn((d,), 16, scale=0.1)
+    _, out = rms_run(x, None, gamma, dtype)
+    rms_check(out, rms_ref(x, None, gamma, dtype), d)
+    res = (randn((7, d), 17).clamp(-5, 5) * scale * 0.25).to(dtype)
+    x[6, 0] = 0
+    _, placed = rms_run(x * 0.25, res, gamma, dtype, in_place=True)
+    rms_check(placed, rms_ref(x * 0.25, res, gamma, dtype), d, "in place")
+
+
+@pytest.mark.parametrize("T,d", [(20000, 16), (9000, 272), (5000, 1040), (3001, 4096), (700, 16400), (400, 40016)])
+def test_rmsnorm_of_a_few_such_rows_among_many(T, d):
+    """Rows are worked on several to a CTA, and more than one after the other: the others stay to the bit as without them."""
+    x, res = randn((T, d), 18, BF16), randn((T, d), 19, BF16)
+    at = torch.tensor([0, 5, T // 2, T - 1], device=DEV)
+    big, big_res = x.clone(), res.clone()
+    big[at] *= 1e30
+    big_res[at] *= 1e30
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    for r, br in ((None, None), (res, big_res)):
+        _, plain = rms_run(x, r, None, BF16, in_place=r is not None)
+        _, out = rms_run(big, br, None, BF16, in_place=r is not None)
+        ref = rms_ref(big[at], None if br is None else br[at], None, BF16)
+        rms_check({n: None if v is None else v[at] for n, v in out.items()}, ref, d)
+        for n, v in out.items():
+            if v is not None:
+                assert torch.equal(v[rest].float(), plain[n][rest].float()), n
+
+
+def test_rmsnorm_with_an_eps_near_the_range():
+    """h^2 / d and eps are in range, their sum is not."""
+    d = 64
+    x = torch.full((3, d), 1.5e19, device=DEV)
+    x[0] = 1.0
+    _, out = rms_run(x, None, None, F32, eps=3e38)
+    rms_check(out, rms_ref(x, None, None, F32, eps=3e38), d)
+
+
 def test_blocks_below_the_smallest_scale_are_stored_as_zeros():
     d = 256
     x = torch.full((2, d), 1.0, device=DEV)
