@@ -613,8 +613,9 @@ MOE_API moe_status_t moe_grouped_gemm_wgrad(moe_plan_t plan, const uint16_t* A, 
  *   codes   out: e4m3 [T][d], 16-byte aligned, of y before it is rounded; or NULL (with scales).
  *   scales  out: fp32 [T][ceil(d / 128)]; or NULL (with codes).  y and codes may not both be NULL.
  *   rstd    out: fp32 [T], or NULL (inference).
- * A row that holds an infinity or a NaN gives NaN.  No output may overlap an input or another output (but h may be res).
- * Launches one kernel.
+ * A row that holds a NaN gives NaN.  Of one that holds infinities and no NaN rstd is 0, y NaN at the infinities (in 8 bits
+ * their blocks) and 0 elsewhere.  Finite rows give finite results, whatever their size.
+ * No output may overlap an input or another output (but h may be res).  Launches one kernel.
  */
 MOE_API moe_status_t moe_rmsnorm(moe_plan_t plan, const void* x, int32_t x_dtype, const void* res, int32_t h_dtype,
                                  const float* gamma, float eps, void* h, uint16_t* y, uint8_t* codes, float* scales,

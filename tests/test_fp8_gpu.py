@@ -192,6 +192,25 @@ def test_rmsnorm_with_an_eps_near_the_range():
     rms_check(out, rms_ref(x, None, None, F32, eps=3e38), d)
 
 
+@pytest.mark.parametrize("d", [16, 400, 4096, 40016])
+def test_rmsnorm_of_a_row_with_infinities(d):
+    """NaN where they are (in 8 bits their block) and 0 elsewhere; its neighbours are not touched."""
+    x = randn((3, d), 14)
+    _, plain = rms_run(x, None, None, F32)
+    x[1, 3], x[1, d - 1] = float("inf"), float("-inf")
+    _, out = rms_run(x, None, None, F32)
+    torch.cuda.synchronize()
+    there = torch.zeros(d, dtype=torch.bool, device=DEV)
+    there[3] = there[d - 1] = True
+    block = torch.nn.functional.pad(there, (0, blocks(d) * 128 - d)).reshape(-1, 128).any(1)
+    assert out["rstd"][1] == 0
+    assert torch.equal(torch.isnan(out["y"][1]), there) and (out["y"][1][~there] == 0).all()
+    assert torch.equal(torch.isnan(out["scales"][1]), block) and (out["scales"][1][~block] == 0).all()
+    assert (out["codes"][1].float() == 0).all()
+    for n in ("y", "codes", "scales", "rstd"):
+        assert torch.equal(out[n][::2].float(), plain[n][::2].float()), n
+
+
 def test_blocks_below_the_smallest_scale_are_stored_as_zeros():
     d = 256
     x = torch.full((2, d), 1.0, device=DEV)
