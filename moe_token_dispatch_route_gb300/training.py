@@ -62,6 +62,7 @@ class MoeTrainLayer:
             groups = b.loss_groups(self.up, seq_len)
             self.load, self.tokens = new(groups, E, dtype=torch.int32), new(groups + 1, dtype=torch.int32)
             self.dlogits, self.loss_scratch = new(T, E, dtype=_F32), b.balance_scratch(self.up, seq_len)
+            self.mask_copy = new(T, dtype=torch.uint8)
         # the fills above, and what the memory was used for before, are over before any stream uses it
         torch.cuda.current_stream(dev).synchronize()
 
@@ -73,7 +74,8 @@ class MoeTrainLayer:
 
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None, mask=None):
         """The layer's output, a tensor of its own.  The layer keeps one pass: a second forward replaces what the
-        first one's backward would need.  mask (bool or uint8 [T], 0: padding): tokens that count in the router's losses."""
+        first one's backward would need.  mask (bool or uint8 [T], 0: padding): tokens that count in the router's losses; it is
+        copied, and the caller's may change before the backward pass."""
         with torch.no_grad(), self._on(stream):
             return self._forward(x, gamma, beta, W_r, W1, W2, mask)
 
@@ -92,9 +94,8 @@ class MoeTrainLayer:
         b.moe_router_logits(u, self.y, W_r, None, self.logits)
         b.route(u, self.logits, r)
         if self.load is not None:
-            self.loss, self.mask = torch.empty(2, dtype=_F32, device=self.device), mask
-            self._hold_mask()
-            b.moe_balance_loss(u, self.logits, r.topk_idx, mask, self.seq_len, self.balance, self.z, self.loss, self.load,
+            self.loss, self.mask = torch.empty(2, dtype=_F32, device=self.device), self._own_mask(mask)
+            b.moe_balance_loss(u, self.logits, r.topk_idx, self.mask, self.seq_len, self.balance, self.z, self.loss, self.load,
                                self.tokens, self.loss_scratch)
         b.dispatch_gemm(u, self.y, W1, r)                                          # GU in r.Y
         b.moe_swiglu_checkpoint(u, r.Y, self.H, self.codes, self.scales)
@@ -102,11 +103,14 @@ class MoeTrainLayer:
         b.moe_combine(self.down, self.Y, r.topk_w, r.dest, self.out)
         return torch.add(self.out, x)
 
-    def _hold_mask(self):
-        """The mask may be the caller's temporary, made on another stream: its memory is not handed out again before this
-        stream's calls have read it."""
-        if self.mask is not None and self.mask.is_cuda:
-            self.mask.record_stream(torch.cuda.current_stream(self.device))
+    def _own_mask(self, mask):
+        """A copy of the mask, which the caller may refill or drop before the backward pass reads it.  It may be a temporary
+        made on another stream: its memory is not handed out again before this stream has copied it."""
+        if mask is None:
+            return None
+        b._arg("MoeTrainLayer.forward", self.up, "mask", mask, self.T, b._IS_MASK)
+        mask.record_stream(torch.cuda.current_stream(self.device))
+        return self.mask_copy.copy_(mask)
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
         """The gradients of the latest forward pass (which may be taken more than once).  x and the weights are that pass's,
@@ -127,7 +131,6 @@ class MoeTrainLayer:
         b.moe_combine(dn, self.dA, self.ones, r.dest, self.dy)                     # the dispatch's gradient
         if self.load is not None:  # the gates and the router's losses
             dlogits = self.dlogits
-            self._hold_mask()
             b.moe_router_backward(u, self.logits, r.topk_idx, self.dw, self.mask, self.seq_len, self.balance, self.z, self.load,
                                   self.tokens, dlogits)
         else:  # the gates: softmax over the chosen logits

@@ -101,6 +101,39 @@ def test_losses_alone_leave_the_output_and_add_to_the_router():
     assert torch.equal(zed[2]["W1"], plain[2]["W1"])
 
 
+def test_a_mask_that_is_refilled_before_the_backward_pass():
+    """The backward pass is that of the mask which the forward pass was given."""
+    T, d, F, E, k, seq = 150, 128, 112, 8, 2, 40
+    p = weights(d, F, E, 7)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x, dout = torch.randn(T, d, generator=g, device=DEV), torch.randn(T, d, generator=g, device=DEV)
+    mask = torch.rand(T, generator=g, device=DEV) < 0.6
+    layer = MoeTrainLayer(T, d, F, E, k, norm="rms", balance=20.0, z=5.0, seq_len=seq)
+    results = []
+    for refill in (False, True):
+        given = mask.clone()
+        layer.forward(x, p["gamma"], None, p["W_r"], p["W1"], p["W2"], mask=given)
+        if refill:
+            given.logical_not_()
+        grads = {n: torch.full(v.shape, float("nan"), device=DEV) for n, v in p.items()}
+        dx = layer.backward(dout, x, p["gamma"], p["W_r"], p["W1"], p["W2"], grads)
+        results.append((dx, grads["W_r"]))
+    assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(*results))
+
+
+def test_passes_with_and_without_a_mask_alternate():
+    T, d, F, E, k = 70, 64, 32, 8, 2
+    p = weights(d, F, E, 7)
+    x = torch.randn(T, d, device=DEV)
+    layer = MoeTrainLayer(T, d, F, E, k, norm="rms", balance=1.0, z=1.0)
+    mask = torch.arange(T, device=DEV) % 3 != 0
+    counts = []
+    for m in (None, mask, None, mask.to(torch.uint8) * 2, ~mask):
+        layer.forward(x, p["gamma"], None, p["W_r"], p["W1"], p["W2"], mask=m)
+        counts.append(int(layer.tokens[-1]))
+    assert counts == [T, int(mask.sum()), T, int(mask.sum()), int((~mask).sum())]
+
+
 def test_arguments_of_the_layer():
     with pytest.raises(ValueError):
         MoeTrainLayer(8, 64, 32, 4, 2, norm="batch")
