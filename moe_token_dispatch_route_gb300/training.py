@@ -110,7 +110,7 @@ class MoeTrainLayer:
             return None
         b._arg("MoeTrainLayer.forward", self.up, "mask", mask, self.T, b._IS_MASK)
         mask.record_stream(torch.cuda.current_stream(self.device))
-        return self.mask_copy.copy_(mask)
+        return self.mask_copy.copy_(mask.reshape(-1))
 
     def backward(self, dout, x, gamma, W_r, W1, W2, grads: dict, accumulate: bool = False, stream=None):
         """The gradients of the latest forward pass (which may be taken more than once).  x and the weights are that pass's,

@@ -134,6 +134,16 @@ def test_passes_with_and_without_a_mask_alternate():
     assert counts == [T, int(mask.sum()), T, int(mask.sum()), int((~mask).sum())]
 
 
+def test_a_mask_of_batches_by_tokens():
+    T, d, F, E, k = 60, 64, 32, 8, 2
+    p = weights(d, F, E, 7)
+    x = torch.randn(T, d, device=DEV)
+    layer = MoeTrainLayer(T, d, F, E, k, norm="rms", balance=1.0, z=1.0, seq_len=20)
+    mask = torch.arange(T, device=DEV).reshape(3, 20) % 7 < 4
+    layer.forward(x, p["gamma"], None, p["W_r"], p["W1"], p["W2"], mask=mask)
+    assert layer.tokens.tolist() == [*mask.sum(1).tolist(), int(mask.sum())]
+
+
 def test_arguments_of_the_layer():
     with pytest.raises(ValueError):
         MoeTrainLayer(8, 64, 32, 4, 2, norm="batch")
