@@ -74,8 +74,8 @@ class MoeTrainLayer:
 
     def forward(self, x, gamma, beta, W_r, W1, W2, stream=None, mask=None):
         """The layer's output, a tensor of its own.  The layer keeps one pass: a second forward replaces what the
-        first one's backward would need.  mask (bool or uint8 [T], 0: padding): tokens that count in the router's losses; it is
-        copied, and the caller's may change before the backward pass."""
+        first one's backward would need.  mask (bool or uint8 [T], 0: padding): tokens that count in the router's losses (a
+        layer without them has no use for it); it is copied, and the caller's may change before the backward pass."""
         with torch.no_grad(), self._on(stream):
             return self._forward(x, gamma, beta, W_r, W1, W2, mask)
 
@@ -87,6 +87,7 @@ class MoeTrainLayer:
         for name, w, n in (("W_r", W_r, self.d * self.E), ("W1", W1, self.E * self.d * 2 * self.F),
                            ("W2", W2, self.E * self.F * self.d)):
             b._arg("MoeTrainLayer.forward", u, name, w, n, b._IS_BF16)
+        b._opt("MoeTrainLayer.forward", u, "mask", mask, self.T, b._IS_MASK)
         if self.norm == "rms":
             b.moe_rmsnorm(u, x, None, gamma, self.eps, None, self.y, rstd=self.rstd)
         else:
@@ -108,7 +109,6 @@ class MoeTrainLayer:
         made on another stream: its memory is not handed out again before this stream has copied it."""
         if mask is None:
             return None
-        b._arg("MoeTrainLayer.forward", self.up, "mask", mask, self.T, b._IS_MASK)
         mask.record_stream(torch.cuda.current_stream(self.device))
         return self.mask_copy.copy_(mask.reshape(-1))
 

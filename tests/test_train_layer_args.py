@@ -50,3 +50,13 @@ def test_a_weight_that_would_be_misread_is_refused(layer, name):
 
 def test_the_weights_that_a_layer_takes(layer):
     assert torch.equal(run(layer, **weights()), torch.ones(T, D)) and len(layer.calls) == 7
+
+
+def test_a_mask_is_looked_at_where_there_are_no_losses_too(layer):
+    x, w = torch.ones(T, D), weights()
+    args = (x, torch.ones(D), torch.zeros(D), w["W_r"], w["W1"], w["W2"])
+    for bad, word in ((torch.ones(T - 1, dtype=torch.bool), "elements"), (torch.ones(T), "float32")):
+        with pytest.raises(ValueError, match=f"mask .*{word}"):
+            layer._forward(*args, bad)
+    assert layer.calls == []
+    assert torch.equal(layer._forward(*args, torch.ones(T, dtype=torch.bool)), x)  # and counts for nothing
