@@ -53,7 +53,7 @@ class MoeTrainLayer:
         self.codes = new(S, 2 * F, dtype=torch.int8)
         self.scales = new(S, 2 * b.checkpoint_blocks(F), dtype=_F32)
         self.Y = new(S, d)
-        # passing through
+        # passing through (the logits are kept where there are losses)
         self.logits, self.out = new(T, E, dtype=_F32), new(T, d, dtype=_F32)
         self.H, self.dH, self.dY, self.dA = new(S, F), new(S, F), new(S, d), new(S, d)
         self.dw, self.dy = new(T, k, dtype=_F32), new(T, d, dtype=_F32)
@@ -161,4 +161,6 @@ class MoeTrainLayer:
         r = self.bufs
         kept = [self.y, self.mean, self.rstd, self.codes, self.scales, self.Y, r.recv[0], r.topk_idx, r.topk_w,
                 r.offsets, r.perm, r.dest]
+        if self.load is not None:  # the gradient of the router's losses starts from the logits
+            kept += [self.logits, self.load, self.tokens, self.mask_copy]
         return sum(t.numel() * t.element_size() for t in kept)

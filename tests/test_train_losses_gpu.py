@@ -144,6 +144,13 @@ def test_a_mask_of_batches_by_tokens():
     assert layer.tokens.tolist() == [*mask.sum(1).tolist(), int(mask.sum())]
 
 
+def test_kept_bytes_count_what_the_losses_keep():
+    T, d, F, E, k, seq = 70, 64, 32, 8, 2, 20
+    plain, losses = (MoeTrainLayer(T, d, F, E, k, norm="rms", **kw) for kw in (dict(), dict(balance=1.0, seq_len=seq)))
+    # logits, picks and tokens of four sequences, a mask
+    assert losses.kept_bytes() - plain.kept_bytes() == 4 * T * E + 4 * 4 * E + 4 * 5 + T
+
+
 def test_arguments_of_the_layer():
     with pytest.raises(ValueError):
         MoeTrainLayer(8, 64, 32, 4, 2, norm="batch")
