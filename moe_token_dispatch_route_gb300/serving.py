@@ -17,14 +17,22 @@ _F32, _BF16, _I32, _E4M3 = torch.float32, torch.bfloat16, torch.int32, torch.flo
 class MoeServeLayer:
     """A layer for T token rows of width d: gamma fp32 [d], W_r bf16 [d, E], W1 bf16 [E, d, 2F] (gate columns, then up), W2
     bf16 [E, F, d]; d and F are multiples of 16.  The experts' weights are stored in 8 bits and not kept as they came.
-    route_flags and selection_bias (fp32 [E]) as moe_route_biased takes them.  A program with batches of several sizes makes a
-    layer for each and passes the first as `like`, whose weights the others share.
+    eps is 1e-5 and route_flags MOE_ROUTE_RENORM unless given; route_flags and selection_bias (fp32 [E]) as moe_route_biased takes
+    them.  A program with batches of several sizes makes a layer for each and passes the first as `like`, which the others share
+    everything but T with: their other arguments are None (k may be 0) or `like`'s own.
     Everything that a pass needs is allocated here, so a pass can be captured in a CUDA graph; `out` and the buffers
     belong to the stream that the passes run on."""
 
-    def __init__(self, T: int, gamma, W_r, W1, W2, k: int, eps: float = 1e-5, route_flags: int = b.MOE_ROUTE_RENORM,
+    def __init__(self, T: int, gamma, W_r, W1, W2, k: int | None, eps: float | None = None, route_flags: int | None = None,
                  selection_bias=None, like: "MoeServeLayer | None" = None):
         if like is not None:
+            other = [name for name, v in (("gamma", gamma), ("W_r", W_r), ("selection_bias", selection_bias))
+                     if v is not None and v is not getattr(like, name)]
+            other += [name for name, v in (("W1", W1), ("W2", W2)) if v is not None]  # like's are not kept as they came
+            other += [name for name, v, none in (("k", k, (None, 0)), ("eps", eps, (None,)), ("route_flags", route_flags, (None,)))
+                      if v not in none and v != getattr(like, name)]
+            if other:
+                raise ValueError(f"MoeServeLayer: {', '.join(other)} beside `like`, whose own are used")
             self.d, self.F, self.E, k, eps, route_flags = like.d, like.F, like.E, like.k, like.eps, like.route_flags
             gamma, W_r, selection_bias = like.gamma, like.W_r, like.selection_bias
         else:
@@ -32,6 +40,8 @@ class MoeServeLayer:
             self.F = F2 // 2
             if tuple(W2.shape) != (self.E, self.F, self.d) or tuple(W_r.shape) != (self.d, self.E) or F2 % 32:
                 raise ValueError(f"MoeServeLayer: W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)} and W_r {tuple(W_r.shape)} do not fit")
+            eps = 1e-5 if eps is None else eps
+            route_flags = b.MOE_ROUTE_RENORM if route_flags is None else route_flags
         self.T, self.k, self.eps, self.route_flags = T, k, eps, route_flags
         self.gamma, self.W_r, self.selection_bias = gamma, W_r, selection_bias
         d, F, E, S = self.d, self.F, self.E, T * k

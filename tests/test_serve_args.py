@@ -170,3 +170,39 @@ def test_scale_blocks_and_groups():
     assert [binding.scale_blocks(n) for n in (16, 128, 144, 1408)] == [1, 1, 2, 11]
     p = plan()
     assert [binding.loss_groups(p, n) for n in (0, 1, 4, 6, 7)] == [1, 6, 2, 1, 1]
+
+
+class Planned(Exception):
+    """A stand-in's constructor has come as far as its plan."""
+
+
+@pytest.fixture
+def like(monkeypatch):
+    def no_plan(*a, **kw):
+        raise Planned
+    monkeypatch.setattr(binding, "moe_plan", no_plan)
+    from moe_token_dispatch_route_gb300 import serving
+    v = object.__new__(serving.MoeServeLayer)
+    v.T, v.d, v.F, v.E, v.k, v.eps, v.route_flags = T, 32, 48, E, K, 1e-6, binding.MOE_ROUTE_SIGMOID
+    v.gamma, v.W_r, v.selection_bias, v.device = buf(32), buf((32, E), BF16), None, torch.device("cpu")
+    v.weights = (None,) * 4
+    return v
+
+
+def test_what_a_layer_shares_may_be_left_out_or_said_again(like):
+    from moe_token_dispatch_route_gb300.serving import MoeServeLayer
+    for args, kw in (((None, None, None, None, 0), {}), ((None, None, None, None, None), {}), ((like.gamma, like.W_r, None, None, K), {}),
+                     ((None, None, None, None, 0), dict(eps=1e-6, route_flags=binding.MOE_ROUTE_SIGMOID))):
+        with pytest.raises(Planned):
+            MoeServeLayer(3, *args, like=like, **kw)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(k=K + 1), dict(gamma=buf(32)), dict(W_r=buf((32, E), BF16)), dict(W1=buf((E, 32, 96), BF16)), dict(W2=buf((E, 48, 32), BF16)),
+    dict(eps=1e-5), dict(route_flags=binding.MOE_ROUTE_RENORM), dict(route_flags=0), dict(selection_bias=buf(E)),
+])
+def test_what_a_layer_shares_is_not_dropped_in_silence(like, bad):
+    from moe_token_dispatch_route_gb300.serving import MoeServeLayer
+    name = next(iter(bad))
+    with pytest.raises(ValueError, match=name):
+        MoeServeLayer(3, **{**dict(gamma=None, W_r=None, W1=None, W2=None, k=0), **bad}, like=like)
