@@ -621,7 +621,7 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
             const size_t N = p.a.N;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int col = 256 * t.c + 128 * b + 64 * h;
+                const int col = 256 * t.c + 128 * b + 64 * h, cols = min(p.a.N - col, 64);  // (a long row's bytes pass 32 bits)
                 if (p.a.out_bf16) {
                     uint8_t* to = static_cast<uint8_t*>(p.a.Y) + (row0 * N + col) * 2;
 #pragma unroll
@@ -635,7 +635,7 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
                                 x[j] = bf16x2(acc[b][32 * g + 8 * c + 2 * j], acc[b][32 * g + 8 * c + 2 * j + 1]);
                             v[c] = make_uint4(x[0], x[1], x[2], x[3]);
                         }
-                        rows_out(staging, v, to + 64 * g, 2 * N, mine, 2 * (p.a.N - col) - 64 * g);
+                        rows_out(staging, v, to + 64 * g, 2 * N, mine, 2 * cols - 64 * g);
                     }
                 } else {
                     uint8_t* to = static_cast<uint8_t*>(p.a.Y) + (row0 * N + col) * 4;
@@ -646,7 +646,7 @@ __device__ void epilogue_role(const Fp8Params& p, Fp8Ctl* ctl, uint8_t* staging,
                         for (int c = 0; c < 4; ++c)
                             v[c] = make_uint4(__float_as_uint(acc[b][16 * g + 4 * c]), __float_as_uint(acc[b][16 * g + 4 * c + 1]),
                                               __float_as_uint(acc[b][16 * g + 4 * c + 2]), __float_as_uint(acc[b][16 * g + 4 * c + 3]));
-                        rows_out(staging, v, to + 64 * g, 4 * N, mine, 4 * (p.a.N - col) - 64 * g);
+                        rows_out(staging, v, to + 64 * g, 4 * N, mine, 4 * cols - 64 * g);
                     }
                 }
             }
@@ -847,7 +847,7 @@ cudaError_t launch_grouped_fp8(const GroupedFp8Args& a, int device, int sm_count
     p.w_blocks = halves * scale_blocks(n);
     p.nkb = scale_blocks(a.d);
     p.as_vec = p.nkb % 4 == 0 && reinterpret_cast<uintptr_t>(a.A_scales) % 16 == 0;
-    p.c_tiles = a.glu ? scale_blocks(n) : (a.N + 255) / 256;
+    p.c_tiles = a.glu ? scale_blocks(n) : (a.N - 1) / 256 + 1;
     p.by_c = Divisor::of(p.c_tiles);
     p.by_band = Divisor::of(kBand * p.c_tiles);
     // Pairs of CTAs load half of W each, but waste more rows of an expert's last tile, and gathered rows reach the leader's

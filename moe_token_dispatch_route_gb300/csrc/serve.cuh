@@ -7,7 +7,7 @@
 namespace moe {
 
 constexpr int kScaleBlock = 128;  // columns (and, of weights, rows) that share one scale
-__host__ __device__ constexpr int scale_blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+__host__ __device__ constexpr int scale_blocks(int n) { return n / kScaleBlock + (n % kScaleBlock != 0); }
 
 struct RmsnormArgs {
     const void* x;       // [T][d], fp32 or bf16

@@ -551,6 +551,23 @@ def test_operators_beyond_two_to_the_31_elements():
     check_8bit(codes[-3:], scales[-3:], ref, err)
 
 
+@pytest.mark.parametrize("N,dtype", [((1 << 29) + 272, F32), ((1 << 30) + 272, BF16)])
+def test_rows_of_two_to_the_31_bytes_and_more(N, dtype):
+    """The bytes that are left of a row, from a tile's first column on, pass 32 bits."""
+    plan = binding.moe_plan(1, 16, 1, 1, N, out_dtype=binding.MOE_OUT_F32 if dtype == F32 else binding.MOE_OUT_BF16)
+    one = torch.full((1, 16), 0x38, dtype=torch.uint8, device=DEV)  # 1.0
+    W = torch.full((1, N, 16), 0x38, dtype=torch.uint8, device=DEV)
+    Ws = (1 + torch.arange(blocks(N), device=DEV) % 7).float().reshape(1, -1, 1)
+    Y = nan((1, N), dtype)
+    ws, st = buffers(plan)
+    offsets = torch.tensor([0, 1], dtype=I32, device=DEV)
+    binding.moe_grouped_gemm_fp8(plan, one, torch.ones(1, 1, device=DEV), None, offsets, W, Ws, Y, ws, st)
+    assert binding.moe_read_status(st)[0] == 0
+    del W
+    want = (16 * Ws.reshape(-1)).to(dtype).repeat_interleave(128)[:N]
+    assert torch.equal(Y[0], want)
+
+
 def test_calls_on_two_streams_at_once():
     """The products keep nothing in the workspace or between calls: two at a time on one plan give what each gives alone."""
     T, d, E, k, N = 2000, 1024, 4, 2, 1024
