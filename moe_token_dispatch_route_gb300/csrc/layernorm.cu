@@ -595,6 +595,8 @@ __global__ void __launch_bounds__(kJoin) layernorm_join_kernel(const float* part
     const int c = blockIdx.x * 32 + q * 4;  // 2 d is a multiple of 32
     wait_for_kernel_before();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    // nobody has written dbeta's half where it is not wanted, and the last CTA's columns may reach into it
+    if (c >= d && !dbeta) parts = 0;
 #pragma unroll 5
     for (int p = warp * 4 + (lane >> 3); p < parts; p += kJoin / 8) {
         const float4 u = __ldcg(reinterpret_cast<const float4*>(partial + (size_t)p * 2 * d + c));
@@ -752,8 +754,9 @@ int backward_parts(int T, int d, int sm_count) {
 }
 
 cudaError_t join(const LayernormBackwardArgs& a, int parts, cudaStream_t s) {
-    // (without dbeta its half of the columns is neither there nor read)
-    return launch_after(layernorm_join_kernel, a.dbeta ? 2 * a.d / 32 : (a.d + 31) / 32, kJoin, 0, s, (const float*)a.partial, parts, a.d, a.dgamma, a.dbeta);
+    // without dbeta its half of the partial sums is neither written nor read
+    return launch_after(layernorm_join_kernel, a.dbeta ? 2 * a.d / 32 : (a.d + 31) / 32, kJoin, 0, s, (const float*)a.partial, parts, a.d,
+                        a.dgamma, a.dbeta);
 }
 
 // Launches a kernel whose shared memory may be over the default limit of 48 KB, the static part included;

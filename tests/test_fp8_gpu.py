@@ -249,6 +249,20 @@ def test_rmsnorm_backward(T, d, dy_dtype, h_dtype):
     assert torch.equal(placed, dx2)
 
 
+@pytest.mark.parametrize("d", [272, 2064])
+def test_rmsnorm_backward_takes_scratch_that_holds_anything(d):
+    """Also where the weights' columns end within a CTA of the kernel that joins them (d an odd multiple of 16)."""
+    T = 333
+    h, dy, rstd = randn((T, d), 7), randn((T, d), 8), 1 + randn((T,), 9, scale=0.1)
+    plan = binding.moe_plan(T, d, 1, 1, 256)
+    results = []
+    for fill in (0, 0xFF):  # zeros, NaN
+        dx, dgamma = nan((T, d)), nan((d,))
+        binding.moe_rmsnorm_backward(plan, dy, h, None, rstd, None, dx, dgamma, torch.full_like(binding.backward_scratch(plan), fill))
+        results.append((dx, dgamma))
+    assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(*results))
+
+
 def test_rmsnorm_backward_is_the_derivative_of_the_forward_formula():
     T, d = 4, 48
     h, dy, gamma = randn((T, d), 11), randn((T, d), 12), 1 + randn((d,), 13, scale=0.1)
