@@ -1,11 +1,11 @@
 // RMS norm of token rows with the residual's addition before it and an 8-bit output beside or in place of the bf16 one.
 //   h = x + res (rounded to the residual's type, stored),  rstd = 1 / sqrt(sum h^2 / d + eps),  y = h rstd gamma,
-// the sum in fp32 over the stored values (where their squares pass its range, of scaled ones).  The 8-bit output is y before it
-// is rounded to bf16: e4m3 codes and a scale for each 128 columns of a row.  Bound by HBM: x and the residual are read once and h stays in registers between the
-// sum and the results (rows above 32768 columns are read back from L2).
+// the sum in fp32 over the stored values (where their squares pass its range, of scaled ones).  The 8-bit output is y before
+// it is rounded to bf16: e4m3 codes and a scale for each 128 columns of a row.  Bound by HBM: x and the residual are read once
+// and h stays in registers between the sum and the results (rows above 32768 columns are read back from L2).
 //
 // A row is held by TPR threads (a power of two from 16 to 1024), vectors of 8 columns, so 16 neighbouring threads hold a
-// block of 128 and find its amax by shuffles.  8192 x 4096, fp32 x, bf16 residual, both outputs: 59.6 us, 0.91 of a plain
+// block of 128 and find its amax by shuffles.  8192 x 4096, fp32 x, bf16 residual, both outputs: 60.1 us, 0.91 of a plain
 // copy's rate.
 #include <algorithm>
 #include <type_traits>
@@ -112,7 +112,7 @@ __device__ __forceinline__ void far_rows(const RmsnormArgs& a, bool met, float i
         }
         s = row_sum<TPR, CTA>(s, red[0]);
         v = row_sum<TPR, CTA>(v, red[1]);
-        const bool far = s * inv_d + a.eps > kLargest;
+        const bool far = fmaf(s, inv_d, a.eps) > kLargest;
         if (!__syncthreads_or(far)) continue;  // (and all have read the sums)
         const float rstd = kDown / sqrtf(v * inv_d + a.eps * kDown * kDown);
         if (row && far && c0 == 0 && a.rstd) a.rstd[t] = rstd;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
         }
         s = row_sum<TPR, kCta>(s, red[turn]);
-        const float mean = s * inv_d + a.eps, rstd = 1.f / sqrtf(mean);
+        const float mean = fmaf(s, inv_d, a.eps), rstd = 1.f / sqrtf(mean);
         met |= mean > kLargest;
         if (row && sub == 0 && a.rstd) a.rstd[t] = rstd;
 #pragma unroll
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(const RmsnormArgs a
             for (int j = 0; j < 8; ++j) s = fmaf(h[j], h[j], s);
         }
         s = row_sum<kWide, kWide>(s, red[turn]);
-        const float mean = s * inv_d + a.eps, rstd = 1.f / sqrtf(mean);
+        const float mean = fmaf(s, inv_d, a.eps), rstd = 1.f / sqrtf(mean);
         met |= mean > kLargest;
         if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
         for (int c0 = 0; c0 < a.d; c0 += kWide * 8) {  // (whole warps: the blocks' amax is found by shuffles)
