@@ -14,8 +14,8 @@
 // that issues the MMAs has as long, so its loop has two commits a k-block (the accumulator is there, the stage is free) and
 // nothing that can be done elsewhere.  Bound by the two accumulators taking turns: an MMA's latency, the additions and the handing
 // back are about 1500 cycles, 720 to 770 a k-block.
-// One GB300: 16384 rows of 8 experts, 14336 x 4096, bf16 out: 680 to 817 us by the length of the timed loop (2.8 to 2.36
-// PFLOP/s); SwiGLU, 65536 gathered rows of 64 experts, 2048 x 2 x 1408: 427 to 437 us; 512 rows of 128 experts, 1536 x 4096: 115 to 119 us
+// One GB300: 16384 rows of 8 experts, 14336 x 4096, bf16 out: 782 to 817 us (2.46 to 2.36 PFLOP/s; 678 to 705 in loops of a few
+// calls); SwiGLU, 65536 gathered rows of 64 experts, 2048 x 2 x 1408: 427 to 437 us; 512 rows of 128 experts, 1536 x 4096: 115 to 119 us
 // (HBM: the weights).
 //
 // Roles of a CTA (512 threads): warp 0 loads W and, where its rows are in place, A (TMA); warp 1 issues the MMAs (the

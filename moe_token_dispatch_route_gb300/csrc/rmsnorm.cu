@@ -84,7 +84,7 @@ __device__ __forceinline__ void results8(const RmsnormArgs& a, const float (&h)[
 
 // Rows that are finite but whose mean square and eps are not (values from some 1e18 up): a CTA that has met one (`met`, by thread) goes
 // over its rows again, sums the squares of 2^-96 h and writes the results of such rows once more.  h is what each thread
-// has stored, or x; its plain sum is the same bits as before.  (Done where it is met, the second sum cost the other rows 5 to 6%.)
+// has stored, or x; its plain sum is the same bits as before.  (Done where it is met, the second sum cost the other rows up to 6%.)
 template <bool XB, bool HB, int TPR, int CTA>
 __device__ __forceinline__ void far_rows(const RmsnormArgs& a, bool met, float inv_d, float (&red)[2][CTA / 32]) {
     if (!__syncthreads_or(met)) return;

@@ -6,9 +6,12 @@
 // and, with w_e = b E load[e] / (G k n^2), the gradient of a counted token's logits
 //   softmax:  p_e (w_e - sum_j p_j w_j),   logistic: the same times 1 - s_e,   + 2 z lse / N softmax_e
 // plus the gates': topk_w as the routing computes it from the picks' logits, times dtopk_w.
-// Bound by instruction issue when large (the exponentials and sums: 60 to 65% of the slots, DRAM below a third) and by launch
-// latency when small.  32768 tokens of 256 experts: 37 to 38 us in all; the logits twice and dlogits once
-// would be 15 at a plain copy's rate.
+// With logistic scores p and the gradient are taken of logits relative to the token's largest one where that is far below 0, and
+// the w_e less their mean: neither changes the formulas.
+// Bound by instruction issue when large (the exponentials and sums: 60 to 67% of the slots, DRAM a quarter) and by launch
+// latency when small.  32768 tokens of 256 experts: 38 us in all; the logits twice and dlogits once
+// would be 15 at a plain copy's rate.  65536 tokens of 8 and of 64 experts: 21 to 22 and 46 to 51 us, 0.9 and 7.4 at that rate: a
+// token's shuffles, picks and loop are paid for one or two experts a lane.
 //
 // A token is held by 8 to 32 lanes, VPL experts each; its sums are shuffles.  A CTA stays within one group, so
 // the forward pass keeps its experts' score sums in registers over all its tokens and the backward pass its w_e.  The
@@ -101,7 +104,9 @@ struct Logistic {
 };
 
 // How a token's experts lie in its lanes: GL lanes, VPL experts each, VEC of them side by side.  With VEC 4 all exist
-// (E = 32 VPL) and are loaded and stored four at a time.
+// (E = 32 VPL) and are loaded and stored four at a time.  Forward and backward in us, logistic scores, with four and with one
+// side by side: 65536 tokens of 128 experts 24.4 + 30.2 and 25.1 + 31.3, 32768 of 256 20.4 + 19.4 and 21.1 + 30.6, 16384 of 512
+// 18.9 + 23.1 and 21.4 + 24.3.  Other numbers of experts have not been tried with four.
 template <int GL, int VPL, int VEC>
 struct Lanes {
     static constexpr int kCols = GL * VPL;

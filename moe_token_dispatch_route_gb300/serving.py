@@ -21,7 +21,8 @@ class MoeServeLayer:
     them.  A program with batches of several sizes makes a layer for each and passes the first as `like`, which the others share
     everything but T with: their other arguments are None (k may be 0) or `like`'s own.
     Everything that a pass needs is allocated here, so a pass can be captured in a CUDA graph; `out` and the buffers
-    belong to the stream that the passes run on."""
+    belong to the stream that the passes run on: keep the layer until passes on other streams than the one that is current
+    when it is made are done."""
 
     def __init__(self, T: int, gamma, W_r, W1, W2, k: int | None, eps: float | None = None, route_flags: int | None = None,
                  selection_bias=None, like: "MoeServeLayer | None" = None):
